@@ -17,7 +17,8 @@ __all__ = [
     "sparse_attn", "sparse_attn_merge", "sparse_attn_workspace", "merge", "recall_async", "commit_residency",
     "plan_recall", "plan_recall_pages", "recall_intervals", "cpu_attend", "RecallOp", "Launch", "Prepared",
     "INJECT_NONE", "INJECT_ABANDON", "INJECT_COPY_FAIL", "recall_gather_async", "CpuPool", "resident_list",
-    "POOL_SUM",
+    "POOL_SUM", "build_tables", "append_kv", "append_kv8", "build_digest8", "sparse_attn8", "sparse_attn8_merge",
+    "sparse_attn8_workspace",
 ]
 
 MINMAX = 0
@@ -74,6 +75,16 @@ _SIGS = {
     "scout_cpu_pool_destroy": ([_p], None),
     "scout_cpu_attend_async": ([_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _f, _p, _p], _i),
     "scout_cpu_pool_wait": ([_p, _i64], _i),
+    "scout_build_tables": ([_p, _p, _p, _i, _i64, _i, _i, _i, _i, _p, _p, _p, _p, _i, _p, _i, _p, _p, _p], _i),
+    "scout_append_kv": ([_p, _i64, _p, _i64, _p, _i, _i, _i, _i, _p, _p, _i64, _p, _p], _i),
+    "scout_append_kv8": ([_i, _p, _i64, _p, _i64, _i, _p, _p, _p, _i, _i, _i, _i, _i, _p, _p, _p, _p, _i64, _p, _p],
+                         _i),
+    "scout_build_digest8": ([_i, _i, _p, _p, _i64, _p, _p, _i, _i, _i, _i, _i, _p, _i, _p, _p, _p], _i),
+    "scout_sparse_attn8_workspace_bytes": ([_i, _i, _i, _i, _i], _sz),
+    "scout_sparse_attn8": ([_i, _p, _p, _p, _p, _p, _i64, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p,
+                            _sz, _p, _p, _p], _i),
+    "scout_sparse_attn8_merge": ([_i, _p, _p, _p, _p, _p, _i64, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _f, _p,
+                                  _p, _p, _p, _p, _sz, _p, _p, _p], _i),
     "scout_plan_recall_pages": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _p, _i, _p], _i),
 }
 
@@ -293,6 +304,207 @@ def merge(O_a, lse_a, O_b, lse_b, O_out=None, lse_out=None, stream=None):
                              _dev(O_b, torch.float32, "O_b"), _dev(lse_b, torch.float32, "lse_b"), rows, D,
                              _dev(O_out, torch.bfloat16, "O_out"), _dev(lse_out, torch.float32, "lse_out"),
                              _stream(stream)), "scout_merge")
+    return O_out, lse_out
+
+
+# ---------------------------------------------------------------------------
+# tables, cache writes and 8-bit caches
+# ---------------------------------------------------------------------------
+_FP8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+
+
+def _sized(t, dtype, numel, name: str, device: int) -> int:
+    """Device pointer of a contiguous tensor of this type and size on the call's device."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
+        have = f"{t.dtype} of {tuple(t.shape)}" if isinstance(t, torch.Tensor) else type(t).__name__
+        raise ScoutError(f"{name} must be a contiguous {dtype} tensor of {numel} elements, got {have}")
+    if t.get_device() != device:
+        raise ScoutError(f"{name} must be on the call's CUDA device, got {t.device}")
+    return t.data_ptr()
+
+
+def _opt_sized(t, dtype, numel, name, device):
+    return None if t is None else _sized(t, dtype, numel, name, device)
+
+
+def _here(t, name: str) -> int:
+    """The device of a call: that of ``t``, which must be the current one."""
+    d = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if d < 0 or d != torch.cuda.current_device():
+        raise ScoutError(f"{name} must be a CUDA tensor on the current device")
+    return d
+
+
+def _pool8(K_pool, V_pool, P):
+    """(format, slots) of an 8-bit pool or pair of pools [n_slots][P][128]."""
+    fmt = _FP8.get(K_pool.dtype)
+    if fmt is None:
+        raise ScoutError(f"an 8-bit pool must be float8_e4m3fn or float8_e5m2, got {K_pool.dtype}")
+    if K_pool.dim() != 3 or K_pool.shape[1] != P or (V_pool is not None and V_pool.shape != K_pool.shape):
+        raise ScoutError(f"the pools must be [n_slots][{P}][D] alike, got {tuple(K_pool.shape)}")
+    return fmt, K_pool.shape[0]
+
+
+def _rows(t, Hkv, D, name, device):
+    """(pointer, token stride) of new rows [n_tokens][Hkv][D], each token's heads contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (Hkv, D):
+        raise ScoutError(f"{name} must be a bf16 tensor [n_tokens][{Hkv}][{D}]")
+    if t.get_device() != device:
+        raise ScoutError(f"{name} must be on the call's CUDA device, got {t.device}")
+    n, (s0, s1, s2) = t.shape[0], t.stride()
+    if n and (s2 != 1 or (Hkv > 1 and s1 != D)):
+        raise ScoutError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
+    return t.data_ptr(), (s0 if n > 1 else Hkv * D)
+
+
+def build_tables(seq_len, free_slots, n_slots, B, Hkv, P, page_table, resident_bits, prev_len=None, cu_tokens=None,
+                 slot_map=None, block_list=None, counts=None, status=None, stream=None):
+    """Page table, residency bits and slot map of a batch from its request lengths.
+
+    Sequence b grows from ``prev_len[b]`` (None: a fresh batch, every table row is written) to
+    ``seq_len[b]`` tokens; its new blocks take the entries of ``free_slots`` (None: slots 0, 1, ...
+    of the pool) in (b, head, block) order.  ``page_table`` int32 [B][Hkv][nblk_cap] and
+    ``resident_bits`` int32 [B][Hkv][words] are updated in place.  Optional outputs: ``cu_tokens``
+    int32 [B + 1], ``slot_map`` int64 [max_tokens][Hkv] (-1 past the last new token),
+    ``block_list`` int32 [max_list][2] (the touched blocks, -1 past the last), ``counts`` int32 [3]
+    (new tokens, touched blocks, new blocks).  ``status`` receives SCOUT_DEV_OVERFLOW (4) when
+    something did not fit and SCOUT_DEV_BAD_INDEX (1) for a bad slot or length."""
+    d = _here(page_table, "page_table")
+    cap = page_table.shape[-1]
+    i32, L = torch.int32, lib()
+    n_free = n_slots if free_slots is None else free_slots.numel()
+    max_tokens = 0 if slot_map is None else slot_map.shape[0]
+    max_list = 0 if block_list is None else block_list.shape[0]
+    _check(L.scout_build_tables(
+        _opt_sized(prev_len, i32, B, "prev_len", d), _sized(seq_len, i32, B, "seq_len", d),
+        _opt_sized(free_slots, i32, n_free, "free_slots", d), n_free, n_slots, B, Hkv, P, cap,
+        _sized(page_table, i32, B * Hkv * cap, "page_table", d),
+        _sized(resident_bits, i32, B * Hkv * (-(-cap // 32)), "resident_bits", d),
+        _opt_sized(cu_tokens, i32, B + 1, "cu_tokens", d),
+        _opt_sized(slot_map, torch.int64, max_tokens * Hkv, "slot_map", d), max_tokens,
+        _opt_sized(block_list, i32, max_list * 2, "block_list", d), max_list, _opt_sized(counts, i32, 3, "counts", d),
+        _opt_sized(status, i32, 1, "status", d), _stream(stream)), "scout_build_tables")
+    return page_table, resident_bits
+
+
+def append_kv(K_new, V_new, slot_map, Hkv, P, K_pool, V_pool, status=None, stream=None):
+    """New bf16 K/V rows [n_tokens][Hkv][D] (token strides free) into bf16 pools [n_slots][P][D] at
+    the pool rows of ``slot_map`` int64 [n_tokens][Hkv] (negative: skipped)."""
+    d = _here(K_pool, "K_pool")
+    D, n, n_slots = K_pool.shape[-1], K_new.shape[0], K_pool.shape[0]
+    kp, ld_k = _rows(K_new, Hkv, D, "K_new", d)
+    vp, ld_v = _rows(V_new, Hkv, D, "V_new", d)
+    if V_new.shape[0] != n:
+        raise ScoutError("K_new and V_new must hold the same tokens")
+    if n == 0:
+        return K_pool, V_pool
+    _check(lib().scout_append_kv(
+        kp, ld_k, vp, ld_v, _sized(slot_map, torch.int64, n * Hkv, "slot_map", d), n, Hkv, D, P,
+        _sized(K_pool, torch.bfloat16, n_slots * P * D, "K_pool", d),
+        _sized(V_pool, torch.bfloat16, n_slots * P * D, "V_pool", d), n_slots,
+        _opt_sized(status, torch.int32, 1, "status", d), _stream(stream)), "scout_append_kv")
+    return K_pool, V_pool
+
+
+def append_kv8(K_new, V_new, page_table, seq_len, B, Hkv, P, K_pool, V_pool, K_scale, V_scale, prev_len=None,
+               status=None, stream=None):
+    """New bf16 K/V rows [n_tokens][Hkv][D] (packed by sequence, token strides free) into 8-bit pools
+    [n_slots][P][D] (float8_e4m3fn or float8_e5m2) with a power-of-two scale per slot, fp32
+    [n_slots].  Sequence b grows from ``prev_len[b]`` (None: 0) to ``seq_len[b]`` tokens.  The scale of
+    a block that holds tokens already never shrinks; when it grows, their codes are rounded to it."""
+    d = _here(K_pool, "K_pool")
+    fmt, n_slots = _pool8(K_pool, V_pool, P)
+    D, n, cap = K_pool.shape[-1], K_new.shape[0], page_table.shape[-1]
+    kp, ld_k = _rows(K_new, Hkv, D, "K_new", d)
+    vp, ld_v = _rows(V_new, Hkv, D, "V_new", d)
+    if V_new.shape[0] != n:
+        raise ScoutError("K_new and V_new must hold the same tokens")
+    if n == 0:
+        return K_pool, V_pool
+    i32, f32, pool = torch.int32, torch.float32, n_slots * P * D
+    _check(lib().scout_append_kv8(
+        fmt, kp, ld_k, vp, ld_v, n, _opt_sized(prev_len, i32, B, "prev_len", d), _sized(seq_len, i32, B, "seq_len", d),
+        _sized(page_table, i32, B * Hkv * cap, "page_table", d), B, Hkv, D, P, cap,
+        _sized(K_pool, K_pool.dtype, pool, "K_pool", d), _sized(V_pool, K_pool.dtype, pool, "V_pool", d),
+        _sized(K_scale, f32, n_slots, "K_scale", d), _sized(V_scale, f32, n_slots, "V_scale", d), n_slots,
+        _opt_sized(status, i32, 1, "status", d), _stream(stream)), "scout_append_kv8")
+    return K_pool, V_pool
+
+
+def build_digest8(kind, K_pool, K_scale, page_table, seq_len, B, Hkv, P, digest, block_list=None, status=None,
+                  stream=None):
+    """Block digests of an 8-bit pool: as build_digest, over code * scale (minima rounded down, maxima
+    up).  (-1, -1) entries of ``block_list`` are skipped."""
+    kind = _KIND[kind]
+    d = _here(K_pool, "K_pool")
+    fmt, n_slots = _pool8(K_pool, None, P)
+    D, cap, i32 = K_pool.shape[-1], page_table.shape[-1], torch.int32
+    n_list = 0 if block_list is None else block_list.shape[0]
+    ddt, per = (torch.bfloat16, 2 * D) if kind == MINMAX else (torch.float32, D)
+    _check(lib().scout_build_digest8(
+        kind, fmt, _sized(K_pool, K_pool.dtype, n_slots * P * D, "K_pool", d),
+        _sized(K_scale, torch.float32, n_slots, "K_scale", d), n_slots,
+        _sized(page_table, i32, B * Hkv * cap, "page_table", d), _sized(seq_len, i32, B, "seq_len", d), B, Hkv, D, P, cap,
+        _opt_sized(block_list, i32, n_list * 2, "block_list", d), n_list,
+        _sized(digest, ddt, B * Hkv * cap * per, "digest", d), _opt_sized(status, i32, 1, "status", d),
+        _stream(stream)), "scout_build_digest8")
+    return digest
+
+
+def sparse_attn8_workspace(B, Hq, Hkv, P, D=128, device="cuda") -> torch.Tensor:
+    n = lib().scout_sparse_attn8_workspace_bytes(B, Hq, Hkv, D, P)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _attn8_args(q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq, Hkv, P, k, scale):
+    """The arguments both 8-bit attention calls begin with."""
+    d = _here(q, "q")
+    fmt, n_slots = _pool8(K_pool, V_pool, P)
+    D, cap, i32, f32 = K_pool.shape[-1], page_table.shape[-1], torch.int32, torch.float32
+    pool = n_slots * P * D
+    return d, D, (
+        fmt, _sized(q, torch.bfloat16, B * Hq * D, "q", d), _sized(K_pool, K_pool.dtype, pool, "K_pool", d),
+        _sized(V_pool, K_pool.dtype, pool, "V_pool", d), _sized(K_scale, f32, n_slots, "K_scale", d),
+        _sized(V_scale, f32, n_slots, "V_scale", d), n_slots, _sized(page_table, i32, B * Hkv * cap, "page_table", d),
+        _sized(seq_len, i32, B, "seq_len", d), _sized(res_list, i32, B * Hkv * k, "res_list", d),
+        _sized(res_count, i32, B * Hkv, "res_count", d), B, Hq, Hkv, D, P, cap, k, float(scale))
+
+
+def sparse_attn8(q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq, Hkv, P, k, scale,
+                 workspace, O=None, lse=None, status=None, max_ctas=None, stream=None):
+    """Partial attention over the listed blocks of an 8-bit cache (float8 pools [n_slots][P][D], fp32
+    scales [n_slots]) -> (O fp32 [B][Hq][D], lse fp32 [B][Hq])."""
+    d, D, args = _attn8_args(q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq, Hkv,
+                             P, k, scale)
+    if O is None:
+        O = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    f32 = torch.float32
+    _check(lib().scout_sparse_attn8(
+        *args, _sized(O, f32, B * Hq * D, "O", d), _sized(lse, f32, B * Hq, "lse", d),
+        _sized(workspace, torch.uint8, workspace.numel(), "workspace", d), workspace.numel(),
+        _opt_sized(status, torch.int32, 1, "status", d), _launch(max_ctas), _stream(stream)), "scout_sparse_attn8")
+    return O, lse
+
+
+def sparse_attn8_merge(q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq, Hkv, P, k,
+                       scale, workspace, O_cpu, lse_cpu, O_out=None, lse_out=None, status=None, max_ctas=None,
+                       stream=None):
+    """The same merged with the CPU partial -> (O bf16 [B][Hq][D], lse fp32 [B][Hq])."""
+    d, D, args = _attn8_args(q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq, Hkv,
+                             P, k, scale)
+    if O_out is None:
+        O_out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if lse_out is None:
+        lse_out = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    f32 = torch.float32
+    _check(lib().scout_sparse_attn8_merge(
+        *args, _sized(O_cpu, f32, B * Hq * D, "O_cpu", d), _sized(lse_cpu, f32, B * Hq, "lse_cpu", d),
+        _sized(O_out, torch.bfloat16, B * Hq * D, "O_out", d), _sized(lse_out, f32, B * Hq, "lse_out", d),
+        _sized(workspace, torch.uint8, workspace.numel(), "workspace", d), workspace.numel(),
+        _opt_sized(status, torch.int32, 1, "status", d), _launch(max_ctas), _stream(stream)),
+        "scout_sparse_attn8_merge")
     return O_out, lse_out
 
 

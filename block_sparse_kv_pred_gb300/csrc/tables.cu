@@ -1,0 +1,272 @@
+// scout_build_tables: page table, residency bits, slot map and touched-block list of a batch from
+// its request lengths; scout_append_kv: new bf16 K/V rows into a paged pool by that slot map.
+// The pages leave the paging open (ScoutAttention (arXiv HTML), section 3.2 takes the KV blocks
+// as given); the tables here are the ones the library's other entry points read.
+//
+// Tables: every CTA makes the same three prefixes over the batch (new tokens, touched blocks, new
+// blocks) in shared memory, and after that no item depends on another: a warp takes a word of 32
+// blocks of a unit (one coalesced row piece, one ballot for the residency word), a touched block
+// of a sequence (its tokens x heads are one contiguous piece of the slot map), or 32 list
+// entries.  One launch, no atomics but the OR of a grown row's residency word.
+#include "fp8.cuh"
+
+namespace scout {
+namespace {
+
+constexpr int kTabWarps = 8;
+
+struct TabArgs {
+  const int32_t* prev_len;
+  const int32_t* seq_len;
+  const int32_t* free_slots;
+  int n_free;
+  int64_t n_slots;
+  int B, Hkv, P, nblk_cap, words;
+  int32_t* page_table;
+  uint32_t* bits;
+  int32_t* cu_tokens;
+  int64_t* slot_map;
+  int max_tokens;
+  int32_t* block_list;
+  int max_list;
+  int32_t* counts;
+  int32_t* status;
+};
+
+// Slot of the i-th new block of the batch: -1 (reported) past the free list or outside the pool.
+__device__ __forceinline__ int take_slot(const TabArgs& a, int i) {
+  if (i >= a.n_free) {
+    report(a.status, SCOUT_DEV_OVERFLOW);
+    return -1;
+  }
+  const int s = a.free_slots != nullptr ? a.free_slots[i] : i;
+  if (s < 0 || s >= a.n_slots) {
+    report(a.status, SCOUT_DEV_BAD_INDEX);
+    return -1;
+  }
+  return s;
+}
+
+__global__ void __launch_bounds__(kTabWarps * 32) tables_kernel(const TabArgs a) {
+  extern __shared__ int sm[];
+  __shared__ int partial[32];
+  const int B = a.B, P = a.P;
+  int* tok = sm;              // [B + 1] new tokens before sequence b
+  int* tou = sm + (B + 1);    // [B + 1] touched blocks (of one KV head)
+  int* neu = tou + (B + 1);   // [B + 1] new blocks (of one KV head)
+  int* prv = neu + (B + 1);   // [B] clamped previous lengths
+  int* seq = prv + B;         // [B] clamped lengths
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int cap_tokens = a.nblk_cap * P;
+  for (int b = tid; b < B; b += blockDim.x) {
+    const SeqSpan s = seq_span(a.prev_len, a.seq_len, b, cap_tokens);
+    prv[b] = s.prev;
+    seq[b] = s.seq;
+    const int nb = (s.seq + P - 1) / P;
+    tok[b] = s.seq - s.prev;
+    tou[b] = s.seq > s.prev ? nb - s.prev / P : 0;
+    neu[b] = nb - (s.prev + P - 1) / P;
+    if (blockIdx.x == 0) report_span(a.status, a.prev_len, a.seq_len, b, cap_tokens);
+  }
+  __syncthreads();
+  cta_exclusive_prefix(tok, B, partial);
+  cta_exclusive_prefix(tou, B, partial);
+  cta_exclusive_prefix(neu, B, partial);
+  const int n_tok = tok[B], n_tou = tou[B];
+  const int64_t n_list = (int64_t)n_tou * a.Hkv;
+  if (blockIdx.x == 0) {
+    if (a.cu_tokens != nullptr)
+      for (int b = tid; b <= B; b += blockDim.x) a.cu_tokens[b] = tok[b];
+    if (tid == 0) {
+      if (a.counts != nullptr) {
+        a.counts[0] = n_tok;
+        a.counts[1] = (int32_t)n_list;
+        a.counts[2] = neu[B] * a.Hkv;
+      }
+      if ((a.slot_map != nullptr && n_tok > a.max_tokens) || (a.block_list != nullptr && n_list > a.max_list))
+        report(a.status, SCOUT_DEV_OVERFLOW);
+    }
+  }
+  const int64_t w0 = (int64_t)blockIdx.x * kTabWarps + (tid >> 5), wn = (int64_t)gridDim.x * kTabWarps;
+
+  // rows of the page table, a word of 32 blocks at a time; a grown row gets its new blocks only
+  const int64_t n_words = (int64_t)B * a.Hkv * a.words;
+  for (int64_t it = w0; it < n_words; it += wn) {
+    const int64_t u = it / a.words;
+    const int w = (int)(it - u * a.words);
+    const int b = (int)(u / a.Hkv), h = (int)(u - (int64_t)b * a.Hkv);
+    const int j0 = (prv[b] + P - 1) / P, j1 = (seq[b] + P - 1) / P;  // new blocks
+    if (a.prev_len != nullptr && (w * 32 + 32 <= j0 || w * 32 >= j1)) continue;
+    const int j = w * 32 + lane;
+    int s = -1;
+    const bool fresh = j >= j0 && j < j1;
+    if (fresh) s = take_slot(a, neu[b] * a.Hkv + h * (j1 - j0) + (j - j0));
+    if (j < a.nblk_cap && (fresh || a.prev_len == nullptr)) a.page_table[u * a.nblk_cap + j] = s;
+    const uint32_t m = __ballot_sync(0xffffffffu, s >= 0);
+    if (lane == 0) {
+      if (a.prev_len == nullptr) a.bits[it] = m;
+      else if (m != 0u) atomicOr(&a.bits[it], m);
+    }
+  }
+
+  // slot map: the tokens of one touched block of a sequence, all heads
+  if (a.slot_map != nullptr) {
+    for (int64_t it = w0; it < n_tou; it += wn) {
+      const int b = owner_of(tou, B, (int)it);
+      const int j = prv[b] / P + ((int)it - tou[b]);
+      const int t0 = max(j * P, prv[b]), t1 = min((j + 1) * P, seq[b]);
+      const int j0 = (prv[b] + P - 1) / P, nb = (seq[b] + P - 1) / P - j0;
+      const int i0 = tok[b] + t0 - prv[b];  // first of its tokens
+      const int rows = min(t1 - t0, a.max_tokens - i0);
+      for (int h0 = 0; h0 < a.Hkv && rows > 0; h0 += 32) {
+        const int hn = min(32, a.Hkv - h0);
+        int s = -1;
+        if (lane < hn) {
+          const int h = h0 + lane;
+          if (j >= j0) {
+            s = take_slot(a, neu[b] * a.Hkv + h * nb + (j - j0));
+          } else {  // the partly filled last block of the previous length
+            s = a.page_table[((int64_t)b * a.Hkv + h) * a.nblk_cap + j];
+            if (s < 0 || s >= a.n_slots) {
+              s = -1;
+              report(a.status, SCOUT_DEV_BAD_INDEX);
+            }
+          }
+        }
+        for (int e0 = 0; e0 < rows * hn; e0 += 32) {
+          const int e = e0 + lane;
+          const int r = e / hn, hh = e - r * hn;
+          const int se = __shfl_sync(0xffffffffu, s, hh);
+          if (e < rows * hn)
+            a.slot_map[(int64_t)(i0 + r) * a.Hkv + h0 + hh] = se < 0 ? -1 : (int64_t)se * P + (t0 + r) % P;
+        }
+      }
+    }
+    // rows past the last new token hold -1: a padded batch's rows are skipped
+    const int64_t from = (int64_t)min(n_tok, a.max_tokens) * a.Hkv, to = (int64_t)a.max_tokens * a.Hkv;
+    for (int64_t e = from + w0 * 32 + lane; e < to; e += wn * 32) a.slot_map[e] = -1;
+  }
+
+  // touched blocks in (sequence, head, block) order, -1 past the last
+  if (a.block_list != nullptr) {
+    for (int64_t i = w0 * 32 + lane; i < a.max_list; i += wn * 32) {
+      int u = -1, j = -1;
+      if (i < n_list) {
+        const int b = owner_of(tou, B, (int)(i / a.Hkv));
+        const int nt = tou[b + 1] - tou[b], r = (int)(i - (int64_t)tou[b] * a.Hkv);
+        const int h = r / nt;
+        u = b * a.Hkv + h;
+        j = prv[b] / P + (r - h * nt);
+      }
+      reinterpret_cast<int2*>(a.block_list)[i] = make_int2(u, j);
+    }
+  }
+}
+
+// Sixteen lanes move one (token, KV head) row of K and of V, 16 bytes a lane; kRows rows a lane are
+// in flight together.
+constexpr int kAppThreads = 256, kAppRows = 4;
+
+__global__ void __launch_bounds__(kAppThreads) append_kernel(const __nv_bfloat16* __restrict__ K,
+                                                             const __nv_bfloat16* __restrict__ V, int64_t ld_k,
+                                                             int64_t ld_v, const int64_t* __restrict__ slot_map,
+                                                             int64_t n_items, int Hkv, __nv_bfloat16* K_pool,
+                                                             __nv_bfloat16* V_pool, int64_t pool_rows, int32_t* status) {
+  const int chunk = threadIdx.x & 15;
+  constexpr int kGroups = kAppThreads / 16;
+  const int64_t first = (int64_t)blockIdx.x * kGroups * kAppRows + (threadIdx.x >> 4);
+  int64_t row[kAppRows];
+  uint4 k[kAppRows], v[kAppRows];
+#pragma unroll
+  for (int r = 0; r < kAppRows; ++r) {
+    const int64_t it = first + r * kGroups;
+    row[r] = it < n_items ? slot_map[it] : -1;
+  }
+#pragma unroll
+  for (int r = 0; r < kAppRows; ++r) {
+    if (row[r] >= pool_rows) {
+      if (chunk == 0) report(status, SCOUT_DEV_BAD_INDEX);
+      row[r] = -1;
+    }
+    if (row[r] < 0) continue;
+    const int64_t it = first + r * kGroups, i = it / Hkv;
+    const int h = (int)(it - i * Hkv);
+    k[r] = ldg_stream(K + i * ld_k + h * kD + chunk * 8);
+    v[r] = ldg_stream(V + i * ld_v + h * kD + chunk * 8);
+  }
+#pragma unroll
+  for (int r = 0; r < kAppRows; ++r) {
+    if (row[r] < 0) continue;
+    *reinterpret_cast<uint4*>(K_pool + row[r] * kD + chunk * 8) = k[r];
+    *reinterpret_cast<uint4*>(V_pool + row[r] * kD + chunk * 8) = v[r];
+  }
+}
+
+}  // namespace
+}  // namespace scout
+
+extern "C" int scout_build_tables(const int32_t* prev_len, const int32_t* seq_len, const int32_t* free_slots,
+                                  int n_free, int64_t n_slots, int B, int Hkv, int P, int nblk_cap,
+                                  int32_t* page_table, uint32_t* resident_bits, int32_t* cu_tokens, int64_t* slot_map,
+                                  int max_tokens, int32_t* block_list, int max_list, int32_t* counts,
+                                  int32_t* dev_status, cudaStream_t stream) {
+  using namespace scout;
+  if (seq_len == nullptr || page_table == nullptr || resident_bits == nullptr) return SCOUT_ERR_INVALID_ARG;
+  if (B <= 0 || Hkv <= 0 || nblk_cap <= 0 || n_slots <= 0 || n_free < 0 || max_tokens < 0 || max_list < 0)
+    return SCOUT_ERR_INVALID_ARG;
+  if (!valid_P(P) || B > kMaxBatch || nblk_cap > kMaxNblk || n_slots > 0x7fffffffLL ||
+      (int64_t)B * nblk_cap * P > 0x7fffffffLL || (int64_t)B * Hkv * nblk_cap > 0x7fffffffLL ||
+      (reinterpret_cast<uintptr_t>(block_list) & 7u) || (reinterpret_cast<uintptr_t>(slot_map) & 7u))
+    return SCOUT_ERR_UNSUPPORTED;
+  TabArgs a;
+  a.prev_len = prev_len;
+  a.seq_len = seq_len;
+  a.free_slots = free_slots;
+  a.n_free = n_free;
+  a.n_slots = n_slots;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.P = P;
+  a.nblk_cap = nblk_cap;
+  a.words = (nblk_cap + 31) / 32;
+  a.page_table = page_table;
+  a.bits = resident_bits;
+  a.cu_tokens = cu_tokens;
+  a.slot_map = slot_map;
+  a.max_tokens = max_tokens;
+  a.block_list = block_list;
+  a.max_list = max_list;
+  a.counts = counts;
+  a.status = dev_status;
+  const int64_t warps = (int64_t)B * Hkv * a.words + max_tokens / P + B + max_list / 32 + 1;
+  const int64_t want = (warps + kTabWarps - 1) / kTabWarps;
+  const int grid = (int)(want < sm_count() * 4 ? want : sm_count() * 4);
+  const size_t smem = (size_t)(5 * B + 3) * sizeof(int);
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem) != cudaSuccess)
+    return SCOUT_ERR_CUDA;
+  tables_kernel<<<grid, kTabWarps * 32, smem, stream>>>(a);
+  return launch_status();
+}
+
+extern "C" int scout_append_kv(const void* K_new, int64_t ld_k, const void* V_new, int64_t ld_v,
+                               const int64_t* slot_map, int n_tokens, int Hkv, int D, int P, void* K_pool,
+                               void* V_pool, int64_t n_slots, int32_t* dev_status, cudaStream_t stream) {
+  using namespace scout;
+  if (K_new == nullptr || V_new == nullptr || slot_map == nullptr || K_pool == nullptr || V_pool == nullptr)
+    return SCOUT_ERR_INVALID_ARG;
+  if (n_tokens < 0 || Hkv <= 0 || n_slots <= 0 || ld_k < (int64_t)Hkv * D || ld_v < (int64_t)Hkv * D)
+    return SCOUT_ERR_INVALID_ARG;
+  if (D != kD || !valid_P(P) || !aligned16(K_new) || !aligned16(V_new) || !aligned16(K_pool) || !aligned16(V_pool) ||
+      ld_k % 8 != 0 || ld_v % 8 != 0 || (reinterpret_cast<uintptr_t>(slot_map) & 7u) || n_slots > 0x7fffffffLL)
+    return SCOUT_ERR_UNSUPPORTED;
+  const int64_t items = (int64_t)n_tokens * Hkv;
+  if (items == 0) return SCOUT_OK;
+  constexpr int kPerCta = kAppThreads / 16 * kAppRows;
+  const int64_t grid = (items + kPerCta - 1) / kPerCta;
+  if (grid > 0x7fffffffLL) return SCOUT_ERR_UNSUPPORTED;
+  append_kernel<<<(unsigned)grid, kAppThreads, 0, stream>>>(
+      static_cast<const __nv_bfloat16*>(K_new), static_cast<const __nv_bfloat16*>(V_new), ld_k, ld_v, slot_map, items,
+      Hkv, static_cast<__nv_bfloat16*>(K_pool), static_cast<__nv_bfloat16*>(V_pool), n_slots * P, dev_status);
+  return launch_status();
+}

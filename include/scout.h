@@ -321,6 +321,134 @@ int scout_merge(const float* O_a, const float* lse_a, const float* O_b, const fl
                 void* O_out, float* lse_out, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ *
+ * Page table, residency bits and slot map of a batch from its request lengths.
+ * The pages take the paged KV cache as given (ScoutAttention (arXiv HTML), section
+ * 3.2); these are the tables the entry points above and below read.
+ *
+ * Sequence b grows from prev_len[b] to seq_len[b] tokens (prev_len NULL: from 0, and
+ * its rows are made anew).  Its new blocks are j in [ceil(prev / P), ceil(seq / P)), its
+ * touched blocks (those that receive a token) j in [floor(prev / P), ceil(seq / P)) when
+ * seq > prev.  The new blocks of the batch, in (b, kvh, j) order, take the entries of
+ * free_slots in order: the i-th takes free_slots[i] (NULL: slot i).
+ *
+ * prev_len, seq_len int32 [B]; free_slots int32 [n_free]
+ * page_table   int32 [B][Hkv][nblk_cap]: the new blocks' slots.  Without prev_len every
+ *              other entry becomes -1; with it every other entry stays.
+ * resident_bits uint32 [B][Hkv][ceil(nblk_cap/32)]: the new blocks' bits set; without
+ *              prev_len the words are written whole.
+ * cu_tokens    int32 [B + 1]: new tokens before sequence b (rows of the packed new K/V), or NULL
+ * slot_map     int64 [max_tokens][Hkv], or NULL: pool row (slot * P + t % P) of every new
+ *              token and KV head; -1 where it has no slot, and in the rows past the last
+ *              new token (a padded batch's rows).
+ * block_list   int32 [max_list][2], or NULL: the touched blocks as (unit, block) pairs in
+ *              (b, kvh, j) order, as the digest builders take them; then (-1, -1).
+ * counts       int32 [3], or NULL: new tokens, touched blocks (of all KV heads), new blocks.
+ * dev_status   may be NULL.  SCOUT_DEV_OVERFLOW: more new blocks than n_free (their entries
+ *              are -1), a length above nblk_cap * P (it counts as that), or more tokens or
+ *              list entries than max_tokens or max_list (the rest is left out).
+ *              SCOUT_DEV_BAD_INDEX: a free slot outside the pool (-1 is entered), a last
+ *              block without a valid entry (its tokens map to -1), a negative length (0) or
+ *              prev_len above seq_len (no new tokens).
+ * No workspace; the result does not depend on the order of execution.
+ * Requires B <= 4096, nblk_cap <= 8192, B * nblk_cap * max(P, Hkv) < 2^31, n_slots < 2^31,
+ * 8-byte aligned slot_map and block_list.
+ * ------------------------------------------------------------------------ */
+int scout_build_tables(const int32_t* prev_len, const int32_t* seq_len, const int32_t* free_slots, int n_free,
+                       int64_t n_slots, int B, int Hkv, int P, int nblk_cap, int32_t* page_table,
+                       uint32_t* resident_bits, int32_t* cu_tokens, int64_t* slot_map, int max_tokens,
+                       int32_t* block_list, int max_list, int32_t* counts, int32_t* dev_status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * New K/V rows into a bf16 paged cache.
+ *
+ * K_new, V_new bf16: row (i, kvh) of D values at i * ld_k (ld_v) + kvh * D elements, so that
+ *              they may be slices of a fused projection's output
+ * slot_map     int64 [n_tokens][Hkv] as scout_build_tables writes it: row (i, kvh) goes to
+ *              pool row slot_map[i][kvh]; a negative entry skips it, one at or above
+ *              n_slots * P is skipped and SCOUT_DEV_BAD_INDEX set in dev_status (may be NULL).
+ *              Entries that are not skipped must be distinct.
+ * K_pool, V_pool bf16 [n_slots][P][D]; rows that no entry names are left as they were.
+ * Requires ld >= Hkv * D, ld % 8 == 0, 16-byte aligned tensors, n_slots < 2^31.
+ * ------------------------------------------------------------------------ */
+int scout_append_kv(const void* K_new, int64_t ld_k, const void* V_new, int64_t ld_v, const int64_t* slot_map,
+                    int n_tokens, int Hkv, int D, int P, void* K_pool, void* V_pool, int64_t n_slots,
+                    int32_t* dev_status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * 8-bit paged caches.
+ *
+ * A pool holds one byte per value, [n_slots][P][D], with one fp32 scale per slot (a block of
+ * one KV head) in K_scale / V_scale [n_slots]: code c of slot s stands for c * scale[s].
+ * Scales are finite and not negative; the writer below makes powers of two, the readers take
+ * any.  The codes are one of two floating-point formats:
+ * ------------------------------------------------------------------------ */
+typedef enum scout_fp8 {
+  SCOUT_FP8_E4M3 = 0, /* 4 exponent bits, 3 of significand, largest 448, no infinities */
+  SCOUT_FP8_E5M2 = 1  /* 5 exponent bits, 2 of significand, largest 57344 */
+} scout_fp8;
+
+/* New K/V rows into an 8-bit paged cache, quantised as they are written.
+ *
+ * Sequence b grows from prev_len[b] (NULL: 0) to seq_len[b] tokens; K_new / V_new hold the new
+ * rows packed by sequence (n_tokens of them; strides as for scout_append_kv), page_table int32
+ * [B][Hkv][nblk_cap] the slots of every touched block (scout_build_tables).  For each touched
+ * block, K and V apart, with F the format's largest value:
+ *   need  = the smallest power of two >= 2^-126 with |x| <= F * need for the finite new values
+ *           x of the block
+ *   scale = need for a block without cached tokens, else max(its scale, need)
+ *   code  = x * (1 / scale) rounded to nearest even (infinities to +-F, NaN to NaN);
+ *           the cached tokens' codes become code * (old scale / scale), rounded, when the
+ *           scale grew, and stay as they are otherwise.
+ * Everything else in the pools and scales is left as it was: rows at and past seq_len too.
+ * Running it again on the same rows changes nothing.  The scales of blocks with cached tokens must be
+ * positive.  Every touched block needs a slot of its own.
+ * dev_status (may be NULL): SCOUT_DEV_BAD_INDEX for a touched block whose slot is not in the
+ * pool or whose rows are not in K_new (it is skipped), a negative length or prev_len above
+ * seq_len (no new tokens); SCOUT_DEV_OVERFLOW for a length above nblk_cap * P (it counts as that).
+ * No workspace.  Requires B <= 4096, nblk_cap <= 8192, B * nblk_cap * P < 2^31, n_slots < 2^31,
+ * ld >= Hkv * D, ld % 8 == 0, and 16-byte aligned rows and pools. */
+int scout_append_kv8(int fmt, const void* K_new, int64_t ld_k, const void* V_new, int64_t ld_v, int n_tokens,
+                     const int32_t* prev_len, const int32_t* seq_len, const int32_t* page_table, int B, int Hkv,
+                     int D, int P, int nblk_cap, void* K_pool, void* V_pool, float* K_scale, float* V_scale,
+                     int64_t n_slots, int32_t* dev_status, cudaStream_t stream);
+
+/* Block digests of an 8-bit cache: scout_build_digest over the values code * scale, with the
+ * same outputs, so that scout_score_topk selects from either cache.  The minima are rounded
+ * down and the maxima up to bf16, so that a digest bounds every score of its block whatever
+ * the scale (with power-of-two scales both are exact).  Mean: a compensated fp32 sum of codes,
+ * scaled and divided by the count.  NaN codes are passed over by the minima and maxima.
+ * A (-1, -1) entry of block_list is padding and skipped; any other entry outside the tables
+ * sets SCOUT_DEV_BAD_INDEX. */
+int scout_build_digest8(int kind, int fmt, const void* K_pool, const float* K_scale, int64_t n_slots,
+                        const int32_t* page_table, const int32_t* seq_len, int B, int Hkv, int D, int P, int nblk_cap,
+                        const int32_t* block_list, int n_list, void* digest, int32_t* dev_status,
+                        cudaStream_t stream);
+
+/* Attention over the listed blocks of an 8-bit cache: scout_sparse_attn and
+ * scout_sparse_attn_merge with K and V read as code * scale; outputs, conventions, work
+ * split and early starts as theirs (it waits before its first global read).  The
+ * probabilities keep about 22 bits and the queries all of theirs, so the fp32 outputs are
+ * good to fp32 rounding.  Listed blocks outside the tables, the pool or the sequence are
+ * skipped and SCOUT_DEV_BAD_INDEX set.
+ * workspace: scout_sparse_attn8_workspace_bytes() bytes, 16-byte aligned; its first 4 * B * Hkv
+ * bytes must be zero before the first use and are left zero by every call.  Calls that may
+ * overlap (streams, graphs) need a workspace each.
+ * Requires G <= 8, B * Hkv <= 4096, B * Hkv * k <= 2^28, n_slots * P < 2^31, pools 16-byte
+ * aligned, q, O_part and O_cpu 8-byte and O_out 4-byte aligned. */
+size_t scout_sparse_attn8_workspace_bytes(int B, int Hq, int Hkv, int D, int P);
+int scout_sparse_attn8(int fmt, const void* q, const void* K_pool, const void* V_pool, const float* K_scale,
+                       const float* V_scale, int64_t n_slots, const int32_t* page_table, const int32_t* seq_len,
+                       const int32_t* res_list, const int32_t* res_count, int B, int Hq, int Hkv, int D, int P,
+                       int nblk_cap, int k, float scale, float* O_part, float* lse_part, void* workspace,
+                       size_t workspace_bytes, int32_t* dev_status, const scout_launch* launch, cudaStream_t stream);
+int scout_sparse_attn8_merge(int fmt, const void* q, const void* K_pool, const void* V_pool, const float* K_scale,
+                             const float* V_scale, int64_t n_slots, const int32_t* page_table, const int32_t* seq_len,
+                             const int32_t* res_list, const int32_t* res_count, int B, int Hq, int Hkv, int D, int P,
+                             int nblk_cap, int k, float scale, const float* O_cpu, const float* lse_cpu, void* O_out,
+                             float* lse_out, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                             const scout_launch* launch, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ *
  * Asynchronous periodic recall (host side).
  * ScoutAttention (arXiv HTML), section 3.4: important blocks are periodically
  * copied from host memory back into GPU memory, off the critical path; the
