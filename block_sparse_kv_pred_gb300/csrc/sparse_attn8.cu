@@ -13,6 +13,10 @@
 // the plain running maximum.  Weights are split into an f16 high and low part (22 bits), as one
 // f16 would be worse than the fp32 partial that is handed on.
 //
+// Streaming.  Each warp keeps a ring of three halves (K or V of a step, 4 KB, one TMA box) and
+// reloads a half as soon as it has read it: 16 warps an SM hold up to 128 KB in flight.  The places of its steps are resolved 16 steps at a time, a
+// tile a lane, one batch ahead.
+//
 // Tiles.  With at most eight query heads a product's free sides are tokens (scores) and channels
 // (output), so both are computed transposed: S^T = K Q^T (16 tokens x 8 heads), O^T += V^T W^T (16
 // channels x 8 heads).  The contraction order of the first and the row order of the second are
@@ -29,15 +33,24 @@ namespace {
 constexpr int kNW = 8;                 // warps of a CTA
 constexpr int kThreads8 = kNW * 32;
 constexpr int kCtasPerSm = 2;
+constexpr int kUnitSteps = 8;          // steps a warp at most when CTAs take whole units
 constexpr int kMaxUnits8 = 4096;
 constexpr int kMaxGrid8 = 1024;
 constexpr int64_t kMaxSteps = (int64_t)1 << 29;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWBoost = 14;            // weights are kept as 2^14 w, so that their low parts stay normal f16
-// A warp's output state in shared memory: channel 16 g + x of head h at h * kHS + 18 g + x, which
-// spreads the eight-byte stores of a half-warp over all banks.
-constexpr int kHS = 148;
+constexpr int kHalf = 4096;            // K or V of a step: 32 tokens x 128 bytes
+constexpr int kHalves = 3;             // of a warp's ring
+constexpr int kBatch = 16;             // steps whose tiles are resolved together (32 tiles, one a lane)
+constexpr int kRingBytes8 = kNW * kHalves * kHalf;
+constexpr int kTileBytes = kNW * 2 * 2 * kBatch * 16;
+
+// A warp's output state in one half of its ring: channel pair md of group g (channels 16 g + 2 md,
+// + 1) of head h, in units of float2; the XOR spreads the stores of a half-warp over all banks.
+__device__ __forceinline__ int state_at(int h, int g, int md) {
+  return h * 64 + 8 * g + (md ^ ((h >> 1) + 4 * ((g >> 1) & 1)));
+}
 
 struct Attn8Args {
   const __nv_bfloat16* q;
@@ -89,11 +102,12 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Where a 16-token tile lies: its first pool row (0 tokens: nothing there), and its scales.
+// Where a 16-token tile lies: its first pool row and its tokens (0: nothing there), and its scales.
 struct Tile {
   int row, nt;
   float ks, vs;
 };
+static_assert(sizeof(Tile) == 16, "a tile is one 16-byte shared-memory access");
 
 struct State {
   float m[2], l[2];  // of heads 2t, 2t+1: running max of s, this lane's running sum of 2^(s - m)
@@ -101,15 +115,14 @@ struct State {
   float o[8][4];     // O^T: channels 16g + 2md (+1) x heads 2t, 2t+1
 };
 
-// Q^T fragments of unit u: head g, channels 64 i + 16 t + 4 w .. +3 for k-step 4 i + w, scaled by
-// a power of two of the head; qf: that factor undone and the softmax scale, for heads 2t, 2t+1.
+// Q^T fragments of unit u: head g, channels 32 t + 4 w .. +3 for k-step w, scaled by a power of two of the head; qf: that factor undone and the softmax scale, for heads 2t, 2t+1.
 __device__ __forceinline__ void load_q8(const Attn8Args& a, int u, int lane, uint32_t (&qb)[8][2], float (&qf)[2]) {
   const int g = lane >> 2, t = lane & 3;
-  const __nv_bfloat16* row = a.q + ((int64_t)u * a.G + g) * kD + 16 * t;
+  const __nv_bfloat16* row = a.q + ((int64_t)u * a.G + g) * kD + 32 * t;
   uint32_t w[16];
 #pragma unroll
   for (int ks = 0; ks < 8; ++ks) {
-    const uint2 v = g < a.G ? *reinterpret_cast<const uint2*>(row + 64 * (ks >> 2) + 4 * (ks & 3)) : make_uint2(0u, 0u);
+    const uint2 v = g < a.G ? *reinterpret_cast<const uint2*>(row + 4 * ks) : make_uint2(0u, 0u);
     w[2 * ks] = v.x;
     w[2 * ks + 1] = v.y;
   }
@@ -131,24 +144,33 @@ __device__ __forceinline__ void load_q8(const Attn8Args& a, int u, int lane, uin
   qf[1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
 }
 
-// K of one tile: lane (g, t) holds bytes 16 t .. +15 and 64 + 16 t .. +15 of rows g and g + 8.
-// V of one tile: bytes 16 g .. +15 of rows 2t, 2t+1, 2t+8, 2t+9.  Rows past the tile's tokens read
-// as zero (a stale V code could be NaN; its weight of zero would not hide it).
-__device__ __forceinline__ void load_k(const uint8_t* pool, const Tile& tl, int lane, uint4 (&k)[4]) {
+// A half stage holds 32 rows of 128 bytes as TMA writes them with its 128-byte swizzle: 16-byte
+// piece c of row r lies at piece c ^ (r & 7).  A lane reads whole pieces, and the pieces that eight
+// neighbouring lanes read lie in eight different bank groups, for K and for V.
+// K of one tile: lane (g, t) takes pieces 2t, 2t + 1 of rows g and g + 8: k[2 x + i] = row g + 8 x.
+// V of one tile: piece g of rows 2t, 2t+1, 2t+8, 2t+9.
+struct LaneOffsets {
+  uint32_t k[2], v[2];  // bytes from the tile's start; row + 8 lies 1024 bytes on
+};
+__device__ __forceinline__ LaneOffsets lane_offsets(int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const uint8_t* p = pool + (int64_t)(tl.row + g) * kD + 16 * t;
+  LaneOffsets o;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    o.k[i] = (uint32_t)(g * 128 + (((2 * t + i) ^ g) << 4));
+    o.v[i] = (uint32_t)((2 * t + i) * 128 + ((g ^ (2 * t + i)) << 4));
+  }
+  return o;
+}
+__device__ __forceinline__ void read_pieces(const uint8_t* tile, const uint32_t (&off)[2], uint4 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(tile + off[i & 1] + 1024 * (i >> 1));
+}
+// Rows past the tile's tokens: a stale V code could be NaN, which its weight of zero would not hide.
+__device__ __forceinline__ void clear_past(uint4 (&v)[4], int nt, int lane) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    k[i] = g + 8 * (i >> 1) < tl.nt ? ldg_stream(p + 8 * (i >> 1) * kD + 64 * (i & 1)) : make_uint4(0u, 0u, 0u, 0u);
-}
-__device__ __forceinline__ void load_v(const uint8_t* pool, const Tile& tl, int lane, uint4 (&v)[4]) {
-  const int g = lane >> 2, t = lane & 3;
-  const uint8_t* p = pool + (int64_t)(tl.row + 2 * t) * kD + 16 * g;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (i & 1) + 8 * (i >> 1);
-    v[i] = 2 * t + r < tl.nt ? ldg_stream(p + r * kD) : make_uint4(0u, 0u, 0u, 0u);
-  }
+    if (2 * (lane & 3) + (i & 1) + 8 * (i >> 1) >= nt) v[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // Scores of one tile: s[0], s[1] = token g, heads 2t, 2t+1; s[2], s[3] = token g + 8.
@@ -204,52 +226,106 @@ __device__ __forceinline__ float split_scale(float vs, float& e) {
   return be <= 1 ? vs * 0x1p126f : __uint_as_float((__float_as_uint(vs) & 0x807fffffu) | 0x3f800000u);
 }
 
-// Softmax update of one step (two tiles) and its output.
-template <int F>
-__device__ __forceinline__ void step_output(float (&s)[2][4], const Tile (&tl)[2], const uint4 (&v)[2][4], State& st) {
-  float e[2], f[2];
+// 2^x, results below the normal range as zero (weights and probabilities are relative to 1)
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The sums move only when some head's reference rose (rarely, after the first steps).
+__device__ __forceinline__ void rescale(State& st, const float (&al)[2]) {
+  if (__all_sync(0xffffffffu, al[0] == 1.f && al[1] == 1.f)) return;
 #pragma unroll
-  for (int x = 0; x < 2; ++x) f[x] = split_scale(tl[x].vs, e[x]);
+  for (int md = 0; md < 8; ++md) {
+    st.o[md][0] *= al[0];
+    st.o[md][1] *= al[1];
+    st.o[md][2] *= al[0];
+    st.o[md][3] *= al[1];
+  }
+}
+
+// Softmax update of one step: the products s become weights, the sums move to the new references.
+// Which path is taken is the same for the whole warp.
+//
+// The usual step: 32 tokens of one page, scales of ordinary size.  One exponential a score gives
+// its weight f 2^(s + e + boost - M); the softmax's sum takes the weights' sum times one factor.
+__device__ __forceinline__ bool step_weights_page(float (&s)[2][4], const float (&kf)[2], float vs, State& st) {
+  float e;
+  const float f = split_scale(vs, e);
+  float N[2], n[2], shift[2];
+  bool near = f != 0.f;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    float b = fmaxf(fmaxf(s[0][c], s[0][2 + c]), fmaxf(s[1][c], s[1][2 + c]));
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+    b *= kf[c];
+    n[c] = fmaxf(st.m[c], b);
+    N[c] = fmaxf(st.M[c], b + (e + 1.f));
+    shift[c] = (e + (float)kWBoost) - N[c];       // weight = f 2^(s + shift)
+    near = near && fabsf(n[c] + shift[c]) < 64.f;  // false for NaN and infinities too
+  }
+  if (!__all_sync(0xffffffffu, near)) return false;
   float al[2];
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    float b0 = fmaxf(s[0][c], s[0][2 + c]), b1 = fmaxf(s[1][c], s[1][2 + c]);
+    al[c] = fast_exp2(st.M[c] - N[c]);
+    float sum = 0.f;
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, o));
-      b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, o));
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float w = fast_exp2(fmaf(s[x][2 * r + c], kf[c], shift[c]));
+        sum += w;
+        s[x][2 * r + c] = w * f;
+      }
+    // p = 2^(s - n) = 2^(s + shift) 2^-(n + shift)
+    st.l[c] = st.l[c] * fast_exp2(st.m[c] - n[c]) + sum * fast_exp2(-(n[c] + shift[c]));
+    st.m[c] = n[c];
+    st.M[c] = N[c];
+  }
+  rescale(st, al);
+  return true;
+}
+
+// Any step: two tiles of different pages and scales, tokens g, g + 8 of tile x past nt[x] masked.
+__device__ __forceinline__ void step_weights_any(float (&s)[2][4], const float (&kf)[2][2], int nt0, int nt1, float vs0,
+                                              float vs1, int g, State& st) {
+  const int nt[2] = {nt0, nt1};
+  float e[2], f[2], al[2];
+  f[0] = split_scale(vs0, e[0]);
+  f[1] = split_scale(vs1, e[1]);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    float b[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) s[x][2 * r + c] = g + 8 * r < nt[x] ? s[x][2 * r + c] * kf[x][c] : -INFINITY;
+      b[x] = fmaxf(s[x][c], s[x][2 + c]);
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) b[x] = fmaxf(b[x], __shfl_xor_sync(0xffffffffu, b[x], o));
     }
-    const float n = fmaxf(st.m[c], fmaxf(b0, b1));
-    const float N = fmaxf(st.M[c], fmaxf(b0 + (e[0] + 1.f), b1 + (e[1] + 1.f)));
+    const float n = fmaxf(st.m[c], fmaxf(b[0], b[1]));
+    const float N = fmaxf(st.M[c], fmaxf(b[0] + (e[0] + 1.f), b[1] + (e[1] + 1.f)));
     const float base = n == -INFINITY ? 0.f : n, Base = N == -INFINITY ? 0.f : N;  // no finite score yet
-    st.l[c] *= exp2f(st.m[c] - base);
-    al[c] = exp2f(st.M[c] - Base);
+    st.l[c] *= fast_exp2(st.m[c] - base);
+    al[c] = fast_exp2(st.M[c] - Base);
     st.m[c] = n;
     st.M[c] = N;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const float ew = (e[x] + (float)kWBoost) - Base;
+      const float shift = (e[x] + (float)kWBoost) - Base;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float sc = s[x][2 * r + c];
-        st.l[c] += exp2f(sc - base);
-        s[x][2 * r + c] = exp2f(sc + ew) * f[x];
+        st.l[c] += fast_exp2(sc - base);
+        s[x][2 * r + c] = fast_exp2(sc + shift) * f[x];
       }
     }
   }
-  // the sums move only when some head's reference rose (rarely, after the first steps)
-  if (!__all_sync(0xffffffffu, al[0] == 1.f && al[1] == 1.f)) {
-#pragma unroll
-    for (int md = 0; md < 8; ++md) {
-      st.o[md][0] *= al[0];
-      st.o[md][1] *= al[1];
-      st.o[md][2] *= al[0];
-      st.o[md][3] *= al[1];
-    }
-  }
-#pragma unroll
-  for (int x = 0; x < 2; ++x)
-    if (tl[x].nt > 0) tile_output<F>(v[x], s[x], st);
+  rescale(st, al);
 }
 
 __device__ __forceinline__ int64_t first_of(int c, int64_t N, int Gp) { return (int64_t)c * N / Gp; }
@@ -281,19 +357,40 @@ __device__ __forceinline__ void write_unit(const Attn8Args& a, int u, int h, int
 }
 
 template <int P, int F>
-__global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const Attn8Args a) {
-  extern __shared__ __align__(16) float sm8[];
-  __shared__ int partial[32];
+__global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __grid_constant__ CUtensorMap tmK,
+                                                                          const __grid_constant__ CUtensorMap tmV,
+                                                                          const Attn8Args a) {
+  extern __shared__ uint8_t smem_raw8[];
+  // [ring, 1024-byte aligned for the swizzle][tiles][prefix]
+  uint8_t* sm8 = smem_raw8 + ((1024u - (smem_u32(smem_raw8) & 1023u)) & 1023u);
+  __shared__ uint64_t full[kNW][kHalves];  // a half has landed
+  __shared__ int partial[32], longest[kNW], state_half[kNW];
   __shared__ float wm[kMaxG][kNW], wl[kMaxG][kNW], wM[kMaxG][kNW], ww[kMaxG][kNW], own_lse[kMaxG], unit_pow[kMaxG];
   __shared__ int last_piece;
-  float* wo = sm8;                                                   // [kNW][G][kHS]
-  int* prefix = reinterpret_cast<int*>(sm8 + kNW * a.G * kHS);       // [units + 1] steps before a unit
+  int* prefix = reinterpret_cast<int*>(sm8 + kRingBytes8 + kTileBytes);  // [units + 1] steps before a unit
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
+  if (tid < kNW * kHalves) mbar_init(&full[0][0] + tid, 1);
+  if (tid < kNW * kHalves) fence_mbar_init();
+  if (tid == 64) {
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
   wait_prerequisites();
-  for (int u = tid; u < a.units; u += kThreads8) prefix[u] = steps_of<P>(min(max(a.res_count[u], 0), a.k));
+  int most = 0;
+  for (int u = tid; u < a.units; u += kThreads8) {
+    const int n = steps_of<P>(min(max(a.res_count[u], 0), a.k));
+    prefix[u] = n;
+    most = max(most, n);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) {
+    longest[warp] = most;
+    state_half[warp] = warp * (kHalves * kHalf);  // read (times NaN) even where the warp has no step
+  }
   __syncthreads();
   cta_exclusive_prefix(prefix, a.units, partial);
+  for (int w = 0; w < kNW; ++w) most = max(most, longest[w]);
   const int64_t N = prefix[a.units];
   // units with no listed block: O = 0, lse = -inf
   for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
@@ -301,15 +398,114 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const Attn
     for (int i = tid; i < a.G * (kD / 2); i += kThreads8)
       write_unit(a, u, i >> 6, i & 63, -INFINITY, make_float2(0.f, 0.f));
   }
-  const int Gp = (int)min((int64_t)gridDim.x, (N + kNW - 1) / kNW);
+  // With every unit short and the grid covering them, CTA c takes unit c whole: nothing is cut, so
+  // no merge of pieces (two more round trips) ends the launch.  Otherwise CTA c takes steps
+  // [c N / Gp, (c + 1) N / Gp) of all units.
+  const bool by_unit = a.units <= (int)gridDim.x && most <= kUnitSteps * kNW;
+  const int Gp = by_unit ? a.units : (int)min((int64_t)gridDim.x, (N + kNW - 1) / kNW);
   const int c = blockIdx.x;
   if (c >= Gp) return;
-  const int64_t start = first_of(c, N, Gp), end = first_of(c + 1, N, Gp);
-  int u = owner_of(prefix, a.units, (int)start);
+  const int64_t start = by_unit ? prefix[c] : first_of(c, N, Gp), end = by_unit ? prefix[c + 1] : first_of(c + 1, N, Gp);
+  if (start == end) return;
+  // this warp's steps: start + warp + kNW i, i < n_mine
+  const int n_mine = (int)((end - start - warp + kNW - 1) / kNW);
+  uint8_t* ring = sm8 + warp * (kHalves * kHalf);
+  const LaneOffsets off = lane_offsets(lane);
+  Tile* tiles = reinterpret_cast<Tile*>(sm8 + kRingBytes8) + warp * (4 * kBatch);  // two batches
+
+  // Tile 2 kBatch b + lane of this warp, resolved in three dependent reads that lie apart: the
+  // list entry, the page-table slot, the scales.
+  int ru = 0, rj = -1, rlen = 0, rslot = -1, rrow = 0, rnt = 0;
+  float rks = 0.f, rvs = 0.f;
+  auto resolve_entry = [&](int batch) {
+    const int i = batch * kBatch + (lane >> 1), y = lane & 1;
+    rj = -1;
+    rlen = 0;
+    rrow = P == 16 ? 0 : P == 32 ? 16 * y : 16 * y;  // first token of the tile in its page
+    if (i < n_mine) {
+      const int x = (int)start + warp + kNW * i;
+      ru = owner_of(prefix, a.units, x);
+      const int step = x - prefix[ru];
+      const int entry = P == 16 ? 2 * step + y : P == 32 ? step : step >> 1;
+      if (P == 64) rrow += 32 * (step & 1);
+      if (P != 16 || entry < min(max(a.res_count[ru], 0), a.k)) {
+        rj = a.res_list[(int64_t)ru * a.k + entry];
+        rlen = a.seq_len[ru / a.Hkv];
+        if (rj < 0 || rj >= a.nblk_cap) rj = -2;
+      }
+    }
+  };
+  auto resolve_slot = [&]() {
+    rslot = rj >= 0 ? a.page_table[(int64_t)ru * a.nblk_cap + rj] : -1;
+  };
+  auto resolve_tile = [&]() {
+    const int nv = rj >= 0 ? min(P, rlen - rj * P) : 0;
+    const bool ok = nv > 0 && rslot >= 0 && rslot < a.n_slots;
+    if (!ok && rj != -1) report(a.status, SCOUT_DEV_BAD_INDEX);
+    rnt = ok ? min(max(nv - rrow, 0), 16) : 0;
+    rrow = ok ? rslot * P + rrow : 0;
+    rks = ok ? __ldg(a.K_scale + rslot) : 0.f;
+    rvs = ok ? __ldg(a.V_scale + rslot) : 0.f;
+  };
+  auto tile_of = [&](int i, int y) -> Tile* { return tiles + ((i / kBatch) & 1) * (2 * kBatch) + 2 * (i % kBatch) + y; };
+
+  // Half h of this warp: K (even) or V (odd) of its step h / 2, into half `at` = h % 3 of the ring.
+  // One lane; every lane has read what was there.  The box starts at a whole row (x = 0).
+  int issued = 0, landed_n = 0;  // halves
+  bool ok = true;  // false once a bounded wait ran out: nothing more is issued or computed
+  auto issue = [&](int h, int at) {
+    const int i = h >> 1;
+    if (i >= n_mine || !ok) return;
+    issued = h + 1;
+    if (lane != 0) return;
+    uint64_t* bar = &full[warp][at];
+    uint8_t* dst = ring + at * kHalf;
+    const CUtensorMap* map = h & 1 ? &tmV : &tmK;
+    const int2 w0 = *reinterpret_cast<const int2*>(tile_of(i, 0));
+    if (P != 16) {
+      if (w0.y > 0) {
+        mbar_arrive_tx(bar, kHalf);
+        tma_load_2d(dst, map, 0, w0.x, bar);
+      } else {
+        mbar_arrive(bar);
+      }
+      return;
+    }
+    const int2 w1 = *reinterpret_cast<const int2*>(tile_of(i, 1));
+    const uint32_t bytes = (w0.y > 0 ? 2048u : 0u) + (w1.y > 0 ? 2048u : 0u);
+    if (bytes == 0u) {
+      mbar_arrive(bar);
+      return;
+    }
+    mbar_arrive_tx(bar, bytes);
+    if (w0.y > 0) tma_load_2d(dst, map, 0, w0.x, bar);
+    if (w1.y > 0) tma_load_2d(dst + 2048, map, 0, w1.x, bar);
+  };
+  auto landed = [&](int at, uint32_t phase) {
+    if (ok && !mbar_wait(&full[warp][at], phase)) {
+      if (lane == 0) report(a.status, SCOUT_DEV_TIMEOUT);
+      ok = false;
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    landed_n += ok;
+  };
+  resolve_entry(0);
+  resolve_slot();
+  resolve_tile();
+  *reinterpret_cast<int2*>(&tiles[lane].row) = make_int2(rrow, rnt);
+  __syncwarp();
+  issue(0, 0);
+  issue(1, 1);
+  issue(2, 2);
+  *reinterpret_cast<float2*>(&tiles[lane].ks) = make_float2(rks, rvs);
+  __syncwarp();
+
+  int u = by_unit ? c : owner_of(prefix, a.units, (int)start);
+  int i = 0, at = 0;   // this warp's next step, and the ring half of its K
+  uint32_t phase = 0;  // of that half's barrier
   for (int64_t pos = start; pos < end;) {
     while (prefix[u + 1] <= pos) ++u;  // the next unit with steps
     const int64_t hi = min(end, (int64_t)prefix[u + 1]);
-    const int b = u / a.Hkv, len = a.seq_len[b], n = min(max(a.res_count[u], 0), a.k);
     uint32_t qb[8][2];
     float qf[2];
     load_q8(a, u, lane, qb, qf);
@@ -318,42 +514,75 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const Attn
     st.l[0] = st.l[1] = 0.f;
 #pragma unroll
     for (int md = 0; md < 8; ++md) st.o[md][0] = st.o[md][1] = st.o[md][2] = st.o[md][3] = 0.f;
-    for (int64_t x = pos + warp; x < hi; x += kNW) {
-      const int step = (int)(x - prefix[u]);
-      Tile tl[2];
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int entry = P == 16 ? 2 * step + y : P == 32 ? step : step >> 1;
-        const int off = P == 16 ? 0 : P == 32 ? 16 * y : 32 * (step & 1) + 16 * y;  // first token in the page
-        tl[y] = Tile{0, 0, 0.f, 0.f};
-        if (entry < n) {
-          const int j = a.res_list[(int64_t)u * a.k + entry];
-          const int nv = j >= 0 && j < a.nblk_cap ? min(P, len - j * P) : 0;
-          const int slot = nv > 0 ? a.page_table[(int64_t)u * a.nblk_cap + j] : -1;
-          if (slot < 0 || slot >= a.n_slots) {
-            if (lane == 0) report(a.status, SCOUT_DEV_BAD_INDEX);
-          } else {
-            tl[y].row = slot * P + off;
-            tl[y].nt = min(max(nv - off, 0), 16);
-            tl[y].ks = a.K_scale[slot];
-            tl[y].vs = a.V_scale[slot];
-          }
+    bool held = false;  // the V half of the segment's last step takes the warp's state
+    // this warp's steps before hi
+    const int i_end = min(n_mine, max(0, ((int)(hi - start) - warp + kNW - 1) / kNW));
+    while (i < i_end) {
+      const int ib = i % kBatch;  // the next batch is resolved while this one runs
+      if ((i / kBatch + 1) * kBatch < n_mine) {
+        if (ib == 0) resolve_entry(i / kBatch + 1);
+        if (ib == 4) resolve_slot();
+        if (ib == 8) resolve_tile();
+        if (ib == 12) {
+          tiles[(((i / kBatch) + 1) & 1) * (2 * kBatch) + lane] = Tile{rrow, rnt, rks, rvs};
+          __syncwarp();
         }
       }
-      if (tl[0].nt + tl[1].nt == 0) continue;
-      uint4 kk[4], vv[2][4];
+      const Tile t0 = *tile_of(i, 0), t1 = *tile_of(i, 1);
+      const float kf[2][2] = {{t0.ks * qf[0], t0.ks * qf[1]}, {t1.ks * qf[0], t1.ks * qf[1]}};
       float s[2][4];
+      const bool any = t0.nt + t1.nt > 0;
+      landed(at, phase);
+      if (any && ok) {
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        load_k(a.K_pool, tl[y], lane, kk);
-        tile_scores<F>(kk, qb, s[y]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s[y][e] = g + 8 * (e >> 1) < tl[y].nt ? s[y][e] * (tl[y].ks * qf[e & 1]) : -INFINITY;
+        for (int y = 0; y < 2; ++y) {
+          uint4 k[4];
+          read_pieces(ring + at * kHalf + y * 2048, off.k, k);
+          tile_scores<F>(k, qb, s[y]);
+        }
       }
+      // the reads above have returned: the products that use them have been issued
+      __syncwarp();
+      issue(2 * i + kHalves, at);
+      if (++at == kHalves) {
+        at = 0;
+        phase ^= 1u;
+      }
+      if (any && ok) {
+        if (!(P != 16 && t1.nt == 16 && step_weights_page(s, kf[0], t0.vs, st)))
+          step_weights_any(s, kf, t0.nt, t1.nt, t0.vs, t1.vs, g, st);
+      }
+      landed(at, phase);
+      if (any && ok) {
 #pragma unroll
-      for (int y = 0; y < 2; ++y) load_v(a.V_pool, tl[y], lane, vv[y]);
-      step_output<F>(s, tl, vv, st);
+        for (int y = 0; y < 2; ++y) {
+          uint4 v[4];
+          const int nt = y ? t1.nt : t0.nt;
+          read_pieces(ring + at * kHalf + y * 2048, off.v, v);
+          if (nt < 16) clear_past(v, nt, lane);
+          tile_output<F>(v, s[y], st);
+        }
+      }
+      held = i + 1 == i_end;
+      __syncwarp();  // every lane has read its V
+      if (!held) issue(2 * i + 1 + kHalves, at);
+      if (held && lane == 0) state_half[warp] = (warp * kHalves + at) * kHalf;
+      const int was = at;
+      if (++at == kHalves) {
+        at = 0;
+        phase ^= 1u;
+      }
+      ++i;
+      if (held) {
+        float2* dst = reinterpret_cast<float2*>(ring + was * kHalf);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int h = 2 * t + x;
+#pragma unroll
+          for (int md = 0; md < 8; ++md)
+            if (h < a.G) dst[state_at(h, g, md)] = make_float2(st.o[md][x], st.o[md][2 + x]);
+        }
+      }
     }
     // the warps' states of this segment, through shared memory
 #pragma unroll
@@ -370,9 +599,6 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const Attn
         wl[h][warp] = st.l[x];
         wM[h][warp] = st.M[x];
       }
-      float2* dst = reinterpret_cast<float2*>(wo + (warp * a.G + h) * kHS + 18 * g);
-#pragma unroll
-      for (int md = 0; md < 8; ++md) dst[md] = make_float2(st.o[md][x], st.o[md][2 + x]);
     }
     __syncthreads();
     if (tid < a.G) {
@@ -394,14 +620,16 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const Attn
     __syncthreads();
     const bool whole = pos == prefix[u] && hi == prefix[u + 1];
     const int64_t piece = (int64_t)c * 2 + (prefix[u] <= start ? 0 : 1);
-    for (int i = tid; i < a.G * (kD / 2); i += kThreads8) {
-      const int h = i >> 6, d2 = i & 63;
+    for (int e = tid; e < a.G * (kD / 2); e += kThreads8) {
+      const int h = e >> 6, d2 = e & 63;
       float2 o = make_float2(0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kNW; ++w) {
-        const float2 v = reinterpret_cast<const float2*>(wo + (w * a.G + h) * kHS + 18 * (d2 >> 3))[d2 & 7];
-        o.x += ww[h][w] * v.x;
-        o.y += ww[h][w] * v.y;
+        const float f = ww[h][w];
+        if (f == 0.f) continue;  // a warp without a step of the segment has no state
+        const float2 v = reinterpret_cast<const float2*>(sm8 + state_half[w])[state_at(h, d2 >> 3, d2 & 7)];
+        o.x += f * v.x;
+        o.y += f * v.y;
       }
       o.x *= unit_pow[h];
       o.y *= unit_pow[h];
@@ -421,8 +649,8 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const Attn
       __syncthreads();
       if (last_piece) {
         __threadfence();
-        for (int i = tid; i < a.G * (kD / 2); i += kThreads8) {
-          const int h = i >> 6, d2 = i & 63;
+        for (int e = tid; e < a.G * (kD / 2); e += kThreads8) {
+          const int h = e >> 6, d2 = e & 63;
           float m = -INFINITY, L = 0.f;
           float2 o = make_float2(0.f, 0.f);
           for (int cc = c0; cc <= c1; ++cc) {
@@ -443,24 +671,47 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const Attn
       }
     }
     __syncthreads();  // the shared state may be written again
+    if (held) {
+      fence_proxy_async();  // the state was written and read by ordinary accesses, the copy is not one
+      issue(2 * (i - 1) + 1 + kHalves, at == 0 ? kHalves - 1 : at - 1);
+    }
     pos = hi;
   }
+  // given up: let the copies that were started land (again for a bounded time) before leaving
+  for (int h = landed_n; !ok && h < issued; ++h) mbar_wait(&full[warp][h % kHalves], (uint32_t)(h / kHalves) & 1u);
   release_dependents();
 }
 
 inline size_t counters8_bytes(int64_t units) { return (size_t)((units * 4 + 255) / 256 * 256); }
+constexpr size_t kSmSmem = 228 * 1024;       // shared memory of an SM
+constexpr size_t kStaticSmem = 1024 + 2048;  // of a CTA besides the dynamic part: the system's and the arrays'
 constexpr size_t kSlotLse8 = (size_t)kMaxGrid8 * 2 * kMaxG * sizeof(float);
 constexpr size_t kSlotO8 = (size_t)kMaxGrid8 * 2 * kMaxG * kD * sizeof(float);
+
+// The pool as rows of 128 bytes; a box is the rows of a step that lie in one page.
+bool make_rows_map(CUtensorMap* map, const void* pool, int64_t rows, int box_rows) {
+  const cuuint64_t dims[2] = {kD, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {kD};
+  const cuuint32_t box[2] = {kD, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(pool), dims, strides, box, estr,
+                      CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+}
 
 template <int P, int F>
 int launch_attn8(const Attn8Args& a, const scout_launch* launch, cudaStream_t stream) {
   auto kern = attn8_kernel<P, F>;
-  const size_t smem = (size_t)kNW * a.G * kHS * sizeof(float) + (size_t)(a.units + 1) * 4;
-  if (smem > 32 * 1024 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  CUtensorMap tmK, tmV;
+  constexpr int kBox = P == 16 ? 16 : 32;
+  if (!make_rows_map(&tmK, a.K_pool, a.n_slots * P, kBox) || !make_rows_map(&tmV, a.V_pool, a.n_slots * P, kBox))
+    return SCOUT_ERR_UNSUPPORTED;
+  const size_t smem = 1024 + (size_t)kRingBytes8 + kTileBytes + (size_t)(a.units + 1) * 4;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return SCOUT_ERR_CUDA;
+  // two CTAs an SM as long as the prefix over the units leaves room for both
+  const int per_sm = 2 * (smem + kStaticSmem) <= kSmSmem ? kCtasPerSm : 1;
   const int max_ctas = launch != nullptr ? launch->max_ctas : 0;
-  const int grid = min(kMaxGrid8, max_ctas > 0 ? max_ctas : sm_count() * kCtasPerSm);
+  const int grid = min(kMaxGrid8, max_ctas > 0 ? max_ctas : sm_count() * per_sm);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads8);
@@ -469,7 +720,7 @@ int launch_attn8(const Attn8Args& a, const scout_launch* launch, cudaStream_t st
   cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
   cfg.numAttrs = early_start_attrs(launch, attr, 0);
-  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kern, tmK, tmV, a) != cudaSuccess) {
     cudaGetLastError();
     return SCOUT_ERR_CUDA;
   }
