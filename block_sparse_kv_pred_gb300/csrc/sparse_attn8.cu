@@ -13,8 +13,8 @@
 // the plain running maximum.  Weights are split into an f16 high and low part (22 bits), as one
 // f16 would be worse than the fp32 partial that is handed on.
 //
-// Streaming.  Each warp keeps a ring of three halves (K or V of a step, 4 KB, one TMA box) and
-// reloads a half as soon as it has read it: 16 warps an SM hold up to 128 KB in flight.  The places of its steps are resolved 16 steps at a time, a
+// Streaming.  Each warp keeps a ring of two halves (K or V of a step, 4 KB, one TMA box) and
+// reloads a half as soon as it has read it.  The places of its steps are resolved 16 steps at a time, a
 // tile a lane, one batch ahead.
 //
 // Tiles.  With at most eight query heads a product's free sides are tokens (scores) and channels
@@ -23,8 +23,10 @@
 // free, so a lane takes 16-byte pieces of rows and uses every byte where it lies: no shared memory
 // transposes.  A step is 32 tokens: two 16-token tiles, each inside one page.
 //
-// Split.  The steps of all units are dealt as contiguous ranges to CTAs; a range's steps go round
-// its warps.  Whole units are finished by their CTA, cut ones by the last CTA to arrive.
+// Split.  The steps of all units are dealt as contiguous ranges to CTAs, and a CTA's to its warps.
+// A warp finishes the units inside its part alone; units that a warp boundary cuts are joined in
+// shared memory when the CTA's warps are done, and units that a CTA boundary cuts by the last CTA to
+// count itself.  While it streams, a warp waits for nothing but its own copies.
 #include "fp8.cuh"
 
 namespace scout {
@@ -33,15 +35,23 @@ namespace {
 constexpr int kNW = 8;                 // warps of a CTA
 constexpr int kThreads8 = kNW * 32;
 constexpr int kCtasPerSm = 2;
-constexpr int kUnitSteps = 8;          // steps a warp at most when CTAs take whole units
+// A CTA takes whole units when its warps then have at most this many steps more than with an even
+// split, which pays for the even split's merge of pieces across CTAs.  Measured on GB300, whole | even,
+// lists of 58 blocks of 32 tokens, 8 KV heads: 1 sequence (7 steps more) 18.3 | 11.3 us, 16 (4 more)
+// 25.7 | 22.2 us, 32 (1 more) 29.3 | 31.6 us.
+constexpr int kWholeSteps = 2;
+constexpr int kPieces = 16;            // of a cut unit, merged at a time
 constexpr int kMaxUnits8 = 4096;
-constexpr int kMaxGrid8 = 1024;
+constexpr int kMaxGrid8 = 512;
 constexpr int64_t kMaxSteps = (int64_t)1 << 29;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWBoost = 14;            // weights are kept as 2^14 w, so that their low parts stay normal f16
 constexpr int kHalf = 4096;            // K or V of a step: 32 tokens x 128 bytes
-constexpr int kHalves = 3;             // of a warp's ring
+// Halves of a warp's ring.  Two, so that an SM has at most 128 KB in flight: with three it had 192
+// KB, which bought no bandwidth but longer queues for every other access (40 sequences of 2,048
+// listed tokens, 8 KV heads: 42.8 us with two, 46.5 with three; 4 x 128K tokens: 176 and 189 us).
+constexpr int kHalves = 2;
 constexpr int kBatch = 16;             // steps whose tiles are resolved together (32 tiles, one a lane)
 constexpr int kRingBytes8 = kNW * kHalves * kHalf;
 constexpr int kTileBytes = kNW * 2 * 2 * kBatch * 16;
@@ -72,9 +82,10 @@ struct Attn8Args {
   const float* lse_cpu;
   __nv_bfloat16* O_out;
   float* lse_out;
-  int32_t* counters;  // [units]
+  int32_t* counters;  // [units][kMaxG]
   float* slot_lse;    // [kMaxGrid8][2][kMaxG]
-  float* slot_O;      // [kMaxGrid8][2][kMaxG][kD]
+  float* slot_O;      // [kMaxGrid8][2][kMaxG][kD] a CTA's pieces of units it shares with others
+  float* piece_O;     // [kMaxGrid8][kNW][kMaxG][kD] a warp's first piece, while it goes on
   int32_t* status;
 };
 
@@ -328,32 +339,104 @@ __device__ __forceinline__ void step_weights_any(float (&s)[2][4], const float (
   rescale(st, al);
 }
 
-__device__ __forceinline__ int64_t first_of(int c, int64_t N, int Gp) { return (int64_t)c * N / Gp; }
-// the CTA whose range holds step x
-__device__ __forceinline__ int holder_of(int64_t x, int64_t N, int Gp) { return (int)(((x + 1) * Gp + N - 1) / N) - 1; }
+// N steps dealt to Gp CTAs: CTA c takes [first(c), first(c + 1)), first(c) = floor(c N / Gp), written
+// with 32-bit arithmetic (c < 2^9, so c (N mod Gp) < 2^18).
+struct Ranges {
+  int Gp, each, rest;
+  float inv;
+  __device__ __forceinline__ Ranges(int N, int grid) : Gp(grid) {
+    each = N / grid;
+    rest = N - each * grid;
+    inv = (float)grid / (float)N;
+  }
+  __device__ __forceinline__ int first(int c) const { return c * each + (int)((unsigned)(c * rest) / (unsigned)Gp); }
+  // the CTA whose range holds step x: the estimate is off by one at most
+  __device__ __forceinline__ int holder(int x) const {
+    int c = min((int)((float)x * inv), Gp - 1);
+    if (first(c) > x) --c;
+    else if (first(c + 1) <= x) ++c;
+    return c;
+  }
+};
 
-// Final rows of unit u from (fin lse, normalised output): thread d2 of 64 holds channels 2 d2, +1.
-__device__ __forceinline__ void write_unit(const Attn8Args& a, int u, int h, int d2, float lse, float2 o) {
+// One head's result, two channel pairs a lane: d2 = lane and lane + 32.  The CPU partial it is merged
+// with (merge mode) is loaded ahead of its use.
+struct CpuPart8 {
+  float2 o[2];
+  float lse;
+};
+__device__ __forceinline__ CpuPart8 load_cpu8(const Attn8Args& a, int u, int h, int lane) {
+  CpuPart8 c;
+  c.lse = -INFINITY;
+  c.o[0] = c.o[1] = make_float2(0.f, 0.f);
+  if (a.O_out != nullptr) {
+    const int64_t row = (int64_t)u * a.G + h;
+    c.lse = a.lse_cpu[row];
+    c.o[0] = reinterpret_cast<const float2*>(a.O_cpu + row * kD)[lane];
+    c.o[1] = reinterpret_cast<const float2*>(a.O_cpu + row * kD)[lane + 32];
+  }
+  return c;
+}
+__device__ __forceinline__ void write_head(const Attn8Args& a, int u, int h, int lane, float lse, const float2 (&o)[2],
+                                           const CpuPart8& c) {
   const int64_t row = (int64_t)u * a.G + h;
   if (a.O_out == nullptr) {
-    reinterpret_cast<float2*>(a.O_part + row * kD)[d2] = o;
-    if (d2 == 0) a.lse_part[row] = lse;
+    reinterpret_cast<float2*>(a.O_part + row * kD)[lane] = o[0];
+    reinterpret_cast<float2*>(a.O_part + row * kD)[lane + 32] = o[1];
+    if (lane == 0) a.lse_part[row] = lse;
     return;
   }
-  const float lc = a.lse_cpu[row];
-  const float2 oc = reinterpret_cast<const float2*>(a.O_cpu + row * kD)[d2];
-  const float m = fmaxf(lse, lc);
+  const float m = fmaxf(lse, c.lse);
   float wg = 0.f, wc = 0.f, out = -INFINITY;
   if (m != -INFINITY) {
     wg = expf(lse - m);
-    wc = expf(lc - m);
+    wc = expf(c.lse - m);
     const float sum = wg + wc;
     out = m + logf(sum);
     wg /= sum;
     wc /= sum;
   }
-  reinterpret_cast<uint32_t*>(a.O_out + row * kD)[d2] = pack_bf16(wg * o.x + wc * oc.x, wg * o.y + wc * oc.y);
-  if (d2 == 0 && a.lse_out != nullptr) a.lse_out[row] = out;
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    reinterpret_cast<uint32_t*>(a.O_out + row * kD)[lane + 32 * x] =
+        pack_bf16(wg * o[x].x + wc * c.o[x].x, wg * o[x].y + wc * c.o[x].y);
+  if (lane == 0 && a.lse_out != nullptr) a.lse_out[row] = out;
+}
+
+// The weight f of a lane's piece (m, l, M) in the join of all lanes' pieces: output = pow * sum f o.
+// The power of two of the result's size is kept apart, so that no factor leaves the normal range
+// while the result lies in it.  A NaN in any piece makes every weight NaN: it is passed on, not
+// taken for an empty set.
+struct Joined {
+  float f, pow, lse;
+};
+__device__ __forceinline__ Joined join_at(bool has, float m, float l, float M, float top_m, float top_M, float L,
+                                          float base) {
+  const float E = top_M == -INFINITY ? 0.f : fminf(fmaxf(rintf(top_M - base), -100.f), 100.f);
+  const bool none = L == 0.f;
+  Joined j;
+  j.f = none || !has ? 0.f : __fdividef(fast_exp2(M - base - E), L);
+  j.pow = fast_exp2(E - (float)kWBoost);
+  j.lse = none ? -INFINITY : (top_m + __log2f(L)) * kLn2;
+  return j;
+}
+// lanes 8 i + w, w < 8: piece w
+__device__ __forceinline__ Joined join(bool has, float m, float l, float M) {
+  float top_m = m, top_M = M;
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    top_m = fmaxf(top_m, __shfl_xor_sync(0xffffffffu, top_m, o));
+    top_M = fmaxf(top_M, __shfl_xor_sync(0xffffffffu, top_M, o));
+  }
+  const float base = top_m == -INFINITY ? 0.f : top_m;
+  float L = has ? l * fast_exp2(m - base) : 0.f;
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  return join_at(has, m, l, M, top_m, top_M, L, base);
+}
+__device__ __forceinline__ Joined join_one(float m, float l, float M) {
+  const float base = m == -INFINITY ? 0.f : m;
+  return join_at(true, m, l, M, m, M, l * fast_exp2(m - base), base);
 }
 
 template <int P, int F>
@@ -364,9 +447,9 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __gr
   // [ring, 1024-byte aligned for the swizzle][tiles][prefix]
   uint8_t* sm8 = smem_raw8 + ((1024u - (smem_u32(smem_raw8) & 1023u)) & 1023u);
   __shared__ uint64_t full[kNW][kHalves];  // a half has landed
-  __shared__ int partial[32], longest[kNW], state_half[kNW];
-  __shared__ float wm[kMaxG][kNW], wl[kMaxG][kNW], wM[kMaxG][kNW], ww[kMaxG][kNW], own_lse[kMaxG], unit_pow[kMaxG];
-  __shared__ int last_piece;
+  __shared__ int partial[kNW], longest[kNW];
+  __shared__ const float2* state_ptr[kNW][2];  // a warp's pieces: in its ring or the workspace
+  __shared__ float pm[kNW][2][kMaxG], pl[kNW][2][kMaxG], pM[kNW][2][kMaxG];  // m, l, M of a warp's pieces
   int* prefix = reinterpret_cast<int*>(sm8 + kRingBytes8 + kTileBytes);  // [units + 1] steps before a unit
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -377,38 +460,67 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __gr
     prefetch_tmap(&tmV);
   }
   wait_prerequisites();
+  // exclusive prefix of the units' steps, a run of units a thread: the counts are read twice, the
+  // second time from L1, so that all of a thread's first reads are in flight together
   int most = 0;
-  for (int u = tid; u < a.units; u += kThreads8) {
-    const int n = steps_of<P>(min(max(a.res_count[u], 0), a.k));
-    prefix[u] = n;
-    most = max(most, n);
+  {
+    const int per = (a.units + kThreads8 - 1) / kThreads8, u0 = tid * per, u1 = min(a.units, u0 + per);
+    int sum = 0;
+#pragma unroll 4
+    for (int u = u0; u < u1; ++u) {
+      const int n = steps_of<P>(min(max(a.res_count[u], 0), a.k));
+      sum += n;
+      most = max(most, n);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    int run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += x;
+    }
+    if (lane == 31) {
+      partial[warp] = run;
+      longest[warp] = most;
+    }
+    __syncthreads();
+    run -= sum;
+#pragma unroll
+    for (int w = 0; w < kNW; ++w) {
+      run += w < warp ? partial[w] : 0;
+      most = max(most, longest[w]);
+    }
+    for (int u = u0; u < u1; ++u) {
+      prefix[u] = run;
+      run += steps_of<P>(min(max(a.res_count[u], 0), a.k));
+    }
+    if (tid == kThreads8 - 1) prefix[a.units] = run;
+    __syncthreads();
   }
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 0) {
-    longest[warp] = most;
-    state_half[warp] = warp * (kHalves * kHalf);  // read (times NaN) even where the warp has no step
-  }
-  __syncthreads();
-  cta_exclusive_prefix(prefix, a.units, partial);
-  for (int w = 0; w < kNW; ++w) most = max(most, longest[w]);
-  const int64_t N = prefix[a.units];
+  const int N = prefix[a.units];
   // units with no listed block: O = 0, lse = -inf
   for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
     if (prefix[u + 1] != prefix[u]) continue;
-    for (int i = tid; i < a.G * (kD / 2); i += kThreads8)
-      write_unit(a, u, i >> 6, i & 63, -INFINITY, make_float2(0.f, 0.f));
+    const float2 none[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    if (warp < a.G) write_head(a, u, warp, lane, -INFINITY, none, load_cpu8(a, u, warp, lane));
   }
-  // With every unit short and the grid covering them, CTA c takes unit c whole: nothing is cut, so
-  // no merge of pieces (two more round trips) ends the launch.  Otherwise CTA c takes steps
-  // [c N / Gp, (c + 1) N / Gp) of all units.
-  const bool by_unit = a.units <= (int)gridDim.x && most <= kUnitSteps * kNW;
-  const int Gp = by_unit ? a.units : (int)min((int64_t)gridDim.x, (N + kNW - 1) / kNW);
+  // CTA c takes steps [c N / Gp, (c + 1) N / Gp) of all units, or unit c whole: nothing is cut then,
+  // and no merge of pieces (three more round trips) ends the launch.
+  const int even = min((int)gridDim.x, (N + kNW - 1) / kNW);
+  const bool by_unit = a.units <= (int)gridDim.x &&
+                       (most + kNW - 1) / kNW <= (N + even * kNW - 1) / max(even * kNW, 1) + kWholeSteps;
+  const int Gp = by_unit ? a.units : even;
   const int c = blockIdx.x;
   if (c >= Gp) return;
-  const int64_t start = by_unit ? prefix[c] : first_of(c, N, Gp), end = by_unit ? prefix[c + 1] : first_of(c + 1, N, Gp);
+  const Ranges ranges(max(N, 1), Gp);
+  const int start = by_unit ? prefix[c] : ranges.first(c), end = by_unit ? prefix[c + 1] : ranges.first(c + 1);
   if (start == end) return;
-  // this warp's steps: start + warp + kNW i, i < n_mine
-  const int n_mine = (int)((end - start - warp + kNW - 1) / kNW);
+  // A warp's steps are a contiguous part of its CTA's: units that lie inside it are finished by the
+  // warp alone, and what a boundary cuts is joined once, when all warps are done.
+  const int len = end - start;
+  auto part = [&](int w) { return start + (int)(((int64_t)len * w) >> 3); };
+  static_assert(kNW == 8, "parts are eighths");
+  const int wlo = part(warp), whi = part(warp + 1), n_mine = whi - wlo;
   uint8_t* ring = sm8 + warp * (kHalves * kHalf);
   const LaneOffsets off = lane_offsets(lane);
   Tile* tiles = reinterpret_cast<Tile*>(sm8 + kRingBytes8) + warp * (4 * kBatch);  // two batches
@@ -423,7 +535,7 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __gr
     rlen = 0;
     rrow = P == 16 ? 0 : P == 32 ? 16 * y : 16 * y;  // first token of the tile in its page
     if (i < n_mine) {
-      const int x = (int)start + warp + kNW * i;
+      const int x = wlo + i;
       ru = owner_of(prefix, a.units, x);
       const int step = x - prefix[ru];
       const int entry = P == 16 ? 2 * step + y : P == 32 ? step : step >> 1;
@@ -494,18 +606,16 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __gr
   resolve_tile();
   *reinterpret_cast<int2*>(&tiles[lane].row) = make_int2(rrow, rnt);
   __syncwarp();
-  issue(0, 0);
-  issue(1, 1);
-  issue(2, 2);
+  for (int h = 0; h < kHalves; ++h) issue(h, h);
   *reinterpret_cast<float2*>(&tiles[lane].ks) = make_float2(rks, rvs);
   __syncwarp();
 
-  int u = by_unit ? c : owner_of(prefix, a.units, (int)start);
+  int u = n_mine > 0 ? owner_of(prefix, a.units, wlo) : 0;
   int i = 0, at = 0;   // this warp's next step, and the ring half of its K
   uint32_t phase = 0;  // of that half's barrier
-  for (int64_t pos = start; pos < end;) {
+  for (int pos = wlo; pos < whi;) {
     while (prefix[u + 1] <= pos) ++u;  // the next unit with steps
-    const int64_t hi = min(end, (int64_t)prefix[u + 1]);
+    const int hi = min(whi, prefix[u + 1]), i_end = hi - wlo;
     uint32_t qb[8][2];
     float qf[2];
     load_q8(a, u, lane, qb, qf);
@@ -514,10 +624,8 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __gr
     st.l[0] = st.l[1] = 0.f;
 #pragma unroll
     for (int md = 0; md < 8; ++md) st.o[md][0] = st.o[md][1] = st.o[md][2] = st.o[md][3] = 0.f;
-    bool held = false;  // the V half of the segment's last step takes the warp's state
-    // this warp's steps before hi
-    const int i_end = min(n_mine, max(0, ((int)(hi - start) - warp + kNW - 1) / kNW));
-    while (i < i_end) {
+    int was = 0;  // ring half of the last V read
+    while (true) {
       const int ib = i % kBatch;  // the next batch is resolved while this one runs
       if ((i / kBatch + 1) * kBatch < n_mine) {
         if (ib == 0) resolve_entry(i / kBatch + 1);
@@ -563,130 +671,217 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __gr
           tile_output<F>(v, s[y], st);
         }
       }
-      held = i + 1 == i_end;
       __syncwarp();  // every lane has read its V
-      if (!held) issue(2 * i + 1 + kHalves, at);
-      if (held && lane == 0) state_half[warp] = (warp * kHalves + at) * kHalf;
-      const int was = at;
+      was = at;
       if (++at == kHalves) {
         at = 0;
         phase ^= 1u;
       }
-      ++i;
-      if (held) {
-        float2* dst = reinterpret_cast<float2*>(ring + was * kHalf);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int h = 2 * t + x;
-#pragma unroll
-          for (int md = 0; md < 8; ++md)
-            if (h < a.G) dst[state_at(h, g, md)] = make_float2(st.o[md][x], st.o[md][2 + x]);
-        }
-      }
+      if (++i == i_end) break;
+      issue(2 * i - 1 + kHalves, was);
     }
-    // the warps' states of this segment, through shared memory
+    // the segment's state goes into the half that its last V left
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], o);
       st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], o);
     }
+    float2* own = reinterpret_cast<float2*>(ring + was * kHalf);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int h = 2 * t + x;
-      if (h >= a.G) continue;
-      if (g == 0) {
-        wm[h][warp] = st.m[x];
-        wl[h][warp] = st.l[x];
-        wM[h][warp] = st.M[x];
-      }
-    }
-    __syncthreads();
-    if (tid < a.G) {
-      float m = -INFINITY, L = 0.f;
-      for (int w = 0; w < kNW; ++w) m = fmaxf(m, wm[tid][w]);
-      const float base = m == -INFINITY ? 0.f : m;
-      for (int w = 0; w < kNW; ++w) L += wl[tid][w] * exp2f(wm[tid][w] - base);
-      // a NaN anywhere makes L NaN: it is passed on, not taken for an empty set
-      const bool none = L == 0.f;
-      // the power of two of the result's size is kept apart, so that no factor leaves the normal
-      // range while the result lies in it
-      float top = -INFINITY;
-      for (int w = 0; w < kNW; ++w) top = fmaxf(top, wM[tid][w]);
-      const float E = top == -INFINITY ? 0.f : fminf(fmaxf(rintf(top - base), -100.f), 100.f);
-      for (int w = 0; w < kNW; ++w) ww[tid][w] = none ? 0.f : exp2f(wM[tid][w] - base - E) / L;
-      unit_pow[tid] = exp2f(E - (float)kWBoost);
-      own_lse[tid] = none ? -INFINITY : (m + log2f(L)) * kLn2;
-    }
-    __syncthreads();
-    const bool whole = pos == prefix[u] && hi == prefix[u + 1];
-    const int64_t piece = (int64_t)c * 2 + (prefix[u] <= start ? 0 : 1);
-    for (int e = tid; e < a.G * (kD / 2); e += kThreads8) {
-      const int h = e >> 6, d2 = e & 63;
-      float2 o = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kNW; ++w) {
-        const float f = ww[h][w];
-        if (f == 0.f) continue;  // a warp without a step of the segment has no state
-        const float2 v = reinterpret_cast<const float2*>(sm8 + state_half[w])[state_at(h, d2 >> 3, d2 & 7)];
-        o.x += f * v.x;
-        o.y += f * v.y;
-      }
-      o.x *= unit_pow[h];
-      o.y *= unit_pow[h];
-      if (whole) {
-        write_unit(a, u, h, d2, own_lse[h], o);
-      } else {
-        reinterpret_cast<float2*>(a.slot_O + (piece * kMaxG + h) * kD)[d2] = o;
-        if (d2 == 0) a.slot_lse[piece * kMaxG + h] = own_lse[h];
+      for (int md = 0; md < 8; ++md)
+        if (h < a.G) own[state_at(h, g, md)] = make_float2(st.o[md][x], st.o[md][2 + x]);
+    }
+    const bool whole = pos == prefix[u] && hi == prefix[u + 1];
+    if (!whole && g == 0) {
+      const int slot = pos == wlo ? 0 : 1;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        pm[warp][slot][2 * t + x] = st.m[x];
+        pl[warp][slot][2 * t + x] = st.l[x];
+        pM[warp][slot][2 * t + x] = st.M[x];
       }
     }
-    if (!whole) {
-      // the last CTA to count itself merges the pieces, in the order of the ranges
-      const int c0 = holder_of(prefix[u], N, Gp), c1 = holder_of(prefix[u + 1] - 1, N, Gp);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) last_piece = atomicAdd(&a.counters[u], 1) == c1 - c0;
-      __syncthreads();
-      if (last_piece) {
-        __threadfence();
-        for (int e = tid; e < a.G * (kD / 2); e += kThreads8) {
-          const int h = e >> 6, d2 = e & 63;
-          float m = -INFINITY, L = 0.f;
-          float2 o = make_float2(0.f, 0.f);
-          for (int cc = c0; cc <= c1; ++cc) {
-            const int64_t pc = (int64_t)cc * 2 + (prefix[u] <= first_of(cc, N, Gp) ? 0 : 1);
-            const float lse = __ldcg(a.slot_lse + pc * kMaxG + h);
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(a.slot_O + (pc * kMaxG + h) * kD) + d2);
-            if (lse == -INFINITY) continue;  // a piece without tokens weighs nothing
-            const float n = fmaxf(m, lse), keep = expf(m - n), w = expf(lse - n);
-            o.x = o.x * keep + w * v.x;
-            o.y = o.y * keep + w * v.y;
-            L = L * keep + w;
-            m = n;
-          }
-          const float r = L == 0.f ? 0.f : 1.f / L;
-          write_unit(a, u, h, d2, L == 0.f ? -INFINITY : m + logf(L), make_float2(o.x * r, o.y * r));
+    __syncwarp();
+    if (whole) {
+      CpuPart8 next = load_cpu8(a, u, 0, lane);
+      for (int h = 0; h < a.G; ++h) {
+        const float m0 = __shfl_sync(0xffffffffu, st.m[0], h >> 1), m1 = __shfl_sync(0xffffffffu, st.m[1], h >> 1);
+        const float l0 = __shfl_sync(0xffffffffu, st.l[0], h >> 1), l1 = __shfl_sync(0xffffffffu, st.l[1], h >> 1);
+        const float M0 = __shfl_sync(0xffffffffu, st.M[0], h >> 1), M1 = __shfl_sync(0xffffffffu, st.M[1], h >> 1);
+        const Joined j = join_one(h & 1 ? m1 : m0, h & 1 ? l1 : l0, h & 1 ? M1 : M0);
+        float2 o[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float2 v = own[state_at(h, (lane + 32 * x) >> 3, lane & 7)];
+          o[x] = make_float2(j.f * v.x * j.pow, j.f * v.y * j.pow);
         }
-        if (tid == 0) a.counters[u] = 0;  // ready for the next call
+        const CpuPart8 cpu = next;
+        if (h + 1 < a.G) next = load_cpu8(a, u, h + 1, lane);
+        write_head(a, u, h, lane, j.lse, o, cpu);
       }
+    } else {
+      const float2* where = own;
+      if (hi < whi) {  // a first piece with more to come: out of the ring's way
+        float4* dst = reinterpret_cast<float4*>(a.piece_O + ((int64_t)c * kNW + warp) * (kMaxG * kD));
+        for (int e = lane; e < a.G * (kD / 4); e += 32) dst[e] = reinterpret_cast<const float4*>(own)[e];
+        where = reinterpret_cast<const float2*>(dst);
+      }
+      if (lane == 0) state_ptr[warp][pos == wlo ? 0 : 1] = where;
     }
-    __syncthreads();  // the shared state may be written again
-    if (held) {
-      fence_proxy_async();  // the state was written and read by ordinary accesses, the copy is not one
-      issue(2 * (i - 1) + 1 + kHalves, at == 0 ? kHalves - 1 : at - 1);
+    if (hi < whi) {
+      __syncwarp();
+      fence_proxy_async();  // the state was written and read by ordinary accesses, the next copy is not one
+      issue(2 * i - 1 + kHalves, was);
     }
     pos = hi;
   }
   // given up: let the copies that were started land (again for a bounded time) before leaving
   for (int h = landed_n; !ok && h < issued; ++h) mbar_wait(&full[warp][h % kHalves], (uint32_t)(h / kHalves) & 1u);
   release_dependents();
+  __syncthreads();
+
+  // What boundaries cut, a (unit, head) a warp.  First the units cut by the CTA's ends (at most two):
+  // their pieces go to the workspace, and after one fence they are counted; while the answers
+  // come back, the units inside that only warp boundaries cut are joined (phase 1).
+  const int v0 = owner_of(prefix, a.units, start), v1 = owner_of(prefix, a.units, end - 1);
+  const bool cut0 = prefix[v0] < start || prefix[v0 + 1] > end, cut1 = v1 != v0 && prefix[v1 + 1] > end;
+  const int n_cut = ((int)cut0 + (int)cut1) * a.G;
+  auto cut_unit = [&](int q) { return q < a.G && cut0 ? v0 : v1; };  // of task q: unit, then q % G the head
+  auto piece_of = [&](int v, int h, int cc) {
+    return (int64_t)((cc * 2 + (prefix[v] <= ranges.first(cc) ? 0 : 1)) * kMaxG + h);
+  };
+  int arrived = -1;  // of lane k: the count before it of this warp's k-th task
+#pragma unroll 1
+  for (int phase1 = 0; phase1 < 2; ++phase1) {
+    const int tasks = phase1 ? (v1 - v0 + 1) * a.G : n_cut;
+#pragma unroll 1
+    for (int q = warp; q < tasks; q += kNW) {
+      const int h = q % a.G, v = phase1 ? v0 + q / a.G : cut_unit(q);
+      const int plo = max(start, prefix[v]), phi = min(end, prefix[v + 1]);
+      if (plo >= phi) continue;
+      // the warps whose parts hold its ends here
+      const int wl = lane & (kNW - 1), lo_w = part(wl);
+      const int w0 = __popc(__ballot_sync(0xffffffffu, lane < kNW && lo_w <= plo)) - 1;
+      const int w1 = __popc(__ballot_sync(0xffffffffu, lane < kNW && lo_w < phi)) - 1;
+      // phase 1: not the cut ones again, nor those that one warp has finished
+      if (phase1 && (prefix[v] < start || prefix[v + 1] > end || w0 == w1)) continue;
+      CpuPart8 cpu;
+      if (phase1) cpu = load_cpu8(a, v, h, lane);
+      const bool has = wl >= w0 && wl <= w1 && lo_w < part(wl + 1);
+      const int slot = lo_w >= plo ? 0 : 1;
+      const Joined j = join(has, has ? pm[wl][slot][h] : -INFINITY, has ? pl[wl][slot][h] : 0.f,
+                            has ? pM[wl][slot][h] : -INFINITY);
+      float2 p[kNW][2];
+      float f[kNW];
+#pragma unroll
+      for (int w = 0; w < kNW; ++w) {
+        f[w] = __shfl_sync(0xffffffffu, j.f, w);
+        p[w][0] = p[w][1] = make_float2(0.f, 0.f);
+        if (f[w] != 0.f) {
+          const float2* src = state_ptr[w][part(w) >= plo ? 0 : 1];
+          p[w][0] = src[state_at(h, lane >> 3, lane & 7)];
+          p[w][1] = src[state_at(h, (lane + 32) >> 3, lane & 7)];
+        }
+      }
+      float2 o[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int w = 0; w < kNW; ++w)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          o[x].x += f[w] * p[w][x].x;
+          o[x].y += f[w] * p[w][x].y;
+        }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        o[x].x *= j.pow;
+        o[x].y *= j.pow;
+      }
+      if (phase1) {
+        write_head(a, v, h, lane, j.lse, o, cpu);
+      } else {
+        const int64_t mine = piece_of(v, h, c);
+        reinterpret_cast<float2*>(a.slot_O + mine * kD)[lane] = o[0];
+        reinterpret_cast<float2*>(a.slot_O + mine * kD)[lane + 32] = o[1];
+        if (lane == 0) a.slot_lse[mine] = j.lse;
+      }
+    }
+    if (phase1 == 0 && warp < n_cut) {
+      __threadfence();
+      __syncwarp();
+      const int q = warp + kNW * lane;  // two tasks a warp at most
+      if (lane < 2 && q < n_cut) arrived = atomicAdd(a.counters + (int64_t)cut_unit(q) * kMaxG + q % a.G, 1);
+    }
+  }
+  // a unit of several CTAs: the last to count itself merges the pieces, in the order of the ranges
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    const int q = warp + kNW * k;
+    if (q >= n_cut) break;
+    const int v = cut_unit(q), h = q % a.G;
+    const CpuPart8 cpu = load_cpu8(a, v, h, lane);
+    const int c0 = ranges.holder(prefix[v]), c1 = ranges.holder(prefix[v + 1] - 1);
+    if (__shfl_sync(0xffffffffu, arrived, k) != c1 - c0) continue;
+    __threadfence();
+    float m = -INFINITY, L = 0.f;
+    float2 o[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    for (int b0 = c0; b0 <= c1; b0 += kPieces) {  // all loads of a batch together
+      const int nb = min(kPieces, c1 - b0 + 1);
+      const float lse = (lane & (kPieces - 1)) < nb ? __ldcg(a.slot_lse + piece_of(v, h, b0 + (lane & (kPieces - 1)))) : -INFINITY;
+      float2 p[kPieces][2];
+#pragma unroll
+      for (int e = 0; e < kPieces; ++e) {
+        p[e][0] = p[e][1] = make_float2(0.f, 0.f);
+        if (e < nb) {
+          const float2* src = reinterpret_cast<const float2*>(a.slot_O + piece_of(v, h, b0 + e) * kD);
+          p[e][0] = __ldcg(src + lane);
+          p[e][1] = __ldcg(src + lane + 32);
+        }
+      }
+      float n = fmaxf(m, lse);
+#pragma unroll
+      for (int x = kPieces / 2; x > 0; x >>= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, x));
+      const float base = n == -INFINITY ? 0.f : n;
+      const float keep = expf(m - base), wt = expf(lse - base);
+      float sum = wt;
+#pragma unroll
+      for (int x = kPieces / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      L = L * keep + sum;
+      m = n;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        o[x].x *= keep;
+        o[x].y *= keep;
+      }
+#pragma unroll
+      for (int e = 0; e < kPieces; ++e) {
+        const float w = __shfl_sync(0xffffffffu, wt, e);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          o[x].x += w * p[e][x].x;
+          o[x].y += w * p[e][x].y;
+        }
+      }
+    }
+    const float r = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      o[x].x *= r;
+      o[x].y *= r;
+    }
+    write_head(a, v, h, lane, L == 0.f ? -INFINITY : m + logf(L), o, cpu);
+    if (lane == 0) a.counters[(int64_t)v * kMaxG + h] = 0;  // ready for the next call
+  }
 }
 
-inline size_t counters8_bytes(int64_t units) { return (size_t)((units * 4 + 255) / 256 * 256); }
+inline size_t counters8_bytes(int64_t units) { return (size_t)((units * kMaxG * 4 + 255) / 256 * 256); }
 constexpr size_t kSmSmem = 228 * 1024;       // shared memory of an SM
 constexpr size_t kStaticSmem = 1024 + 2048;  // of a CTA besides the dynamic part: the system's and the arrays'
 constexpr size_t kSlotLse8 = (size_t)kMaxGrid8 * 2 * kMaxG * sizeof(float);
 constexpr size_t kSlotO8 = (size_t)kMaxGrid8 * 2 * kMaxG * kD * sizeof(float);
+constexpr size_t kPieceO8 = (size_t)kMaxGrid8 * kNW * kMaxG * kD * sizeof(float);
 
 // The pool as rows of 128 bytes; a box is the rows of a step that lie in one page.
 bool make_rows_map(CUtensorMap* map, const void* pool, int64_t rows, int box_rows) {
@@ -789,6 +984,7 @@ int attn8_entry(int fmt, const void* q, const void* K_pool, const void* V_pool, 
   a.counters = reinterpret_cast<int32_t*>(ws);
   a.slot_lse = reinterpret_cast<float*>(ws + counters8_bytes(units));
   a.slot_O = reinterpret_cast<float*>(ws + counters8_bytes(units) + kSlotLse8);
+  a.piece_O = reinterpret_cast<float*>(ws + counters8_bytes(units) + kSlotLse8 + kSlotO8);
   a.status = dev_status;
   return fmt == SCOUT_FP8_E4M3 ? attn8_by_P<SCOUT_FP8_E4M3>(P, a, launch, stream)
                                : attn8_by_P<SCOUT_FP8_E5M2>(P, a, launch, stream);
@@ -802,7 +998,7 @@ extern "C" size_t scout_sparse_attn8_workspace_bytes(int B, int Hq, int Hkv, int
   (void)D;
   (void)P;
   if (B <= 0 || Hkv <= 0) return 0;
-  return scout::counters8_bytes((int64_t)B * Hkv) + scout::kSlotLse8 + scout::kSlotO8;
+  return scout::counters8_bytes((int64_t)B * Hkv) + scout::kSlotLse8 + scout::kSlotO8 + scout::kPieceO8;
 }
 
 extern "C" int scout_sparse_attn8(int fmt, const void* q, const void* K_pool, const void* V_pool,

@@ -430,7 +430,7 @@ int scout_build_digest8(int kind, int fmt, const void* K_pool, const float* K_sc
  * probabilities keep about 22 bits and the queries all of theirs, so the fp32 outputs are
  * good to fp32 rounding.  Listed blocks outside the tables, the pool or the sequence are
  * skipped and SCOUT_DEV_BAD_INDEX set.
- * workspace: scout_sparse_attn8_workspace_bytes() bytes, 16-byte aligned; its first 4 * B * Hkv
+ * workspace: scout_sparse_attn8_workspace_bytes() bytes, 16-byte aligned; its first 32 * B * Hkv
  * bytes must be zero before the first use and are left zero by every call.  Calls that may
  * overlap (streams, graphs) need a workspace each.
  * Requires G <= 8, B * Hkv <= 4096, B * Hkv * k <= 2^28, n_slots * P < 2^31, pools 16-byte

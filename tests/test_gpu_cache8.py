@@ -407,7 +407,7 @@ class Attn:
         Om, lm = bs.sparse_attn8_merge(*t, ws, dev(self.O_cpu), dev(self.lse_cpu), status=st, **kw)
         self.check(Om, lm, merged=True)
         assert int(st) == 0
-        assert int(ws[: 4 * self.B * self.Hkv].view(torch.int32).abs().sum()) == 0
+        assert int(ws[: 32 * self.B * self.Hkv].view(torch.int32).abs().sum()) == 0
         return O_, l
 
 
