@@ -318,20 +318,19 @@ def merge(O_a, lse_a, O_b, lse_b, O_out=None, lse_out=None, stream=None):
 # tables, cache writes and 8-bit caches
 # ---------------------------------------------------------------------------
 _FP8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+_I32, _I64, _F32, _BF16, _U8 = torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.uint8
 
 
 def _sized(t, dtype, numel, name: str, device: int) -> int:
     """Device pointer of a contiguous tensor of this type and size on the call's device."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
-        have = f"{t.dtype} of {tuple(t.shape)}" if isinstance(t, torch.Tensor) else type(t).__name__
-        raise ScoutError(f"{name} must be a contiguous {dtype} tensor of {numel} elements, got {have}")
-    if t.get_device() != device:
-        raise ScoutError(f"{name} must be on the call's CUDA device, got {t.device}")
-    return t.data_ptr()
-
-
-def _opt_sized(t, dtype, numel, name, device):
-    return None if t is None else _sized(t, dtype, numel, name, device)
+    try:
+        if t.dtype is dtype and t.numel() == numel and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+        have = f"{t.dtype} of {tuple(t.shape)} on {t.device}"
+    except AttributeError:
+        have = type(t).__name__
+    where = f"cuda:{device}" if device >= 0 else "the call's device"
+    raise ScoutError(f"{name} must be a contiguous {dtype} tensor of {numel} elements on {where}, got {have}")
 
 
 def _here(t, name: str) -> int:
@@ -342,19 +341,27 @@ def _here(t, name: str) -> int:
     return d
 
 
+def _stream_on(stream, device: int) -> int:
+    """The handle of ``stream``, or of the device's current one."""
+    if stream is None:
+        return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream
+
+
 def _pool8(K_pool, V_pool, P):
-    """(format, slots) of an 8-bit pool or pair of pools [n_slots][P][128]."""
+    """(format, slots) of an 8-bit pool or pair of pools [n_slots][P][D]."""
     fmt = _FP8.get(K_pool.dtype)
     if fmt is None:
         raise ScoutError(f"an 8-bit pool must be float8_e4m3fn or float8_e5m2, got {K_pool.dtype}")
-    if K_pool.dim() != 3 or K_pool.shape[1] != P or (V_pool is not None and V_pool.shape != K_pool.shape):
-        raise ScoutError(f"the pools must be [n_slots][{P}][D] alike, got {tuple(K_pool.shape)}")
-    return fmt, K_pool.shape[0]
+    shape = K_pool.shape
+    if len(shape) != 3 or shape[1] != P or (V_pool is not None and V_pool.shape != shape):
+        raise ScoutError(f"the pools must be [n_slots][{P}][D] alike, got {tuple(shape)}")
+    return fmt, shape[0]
 
 
 def _rows(t, Hkv, D, name, device):
     """(pointer, token stride) of new rows [n_tokens][Hkv][D], each token's heads contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (Hkv, D):
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.dim() != 3 or t.shape[1:] != (Hkv, D):
         raise ScoutError(f"{name} must be a bf16 tensor [n_tokens][{Hkv}][{D}]")
     if t.get_device() != device:
         raise ScoutError(f"{name} must be on the call's CUDA device, got {t.device}")
@@ -378,19 +385,19 @@ def build_tables(seq_len, free_slots, n_slots, B, Hkv, P, page_table, resident_b
     something did not fit and SCOUT_DEV_BAD_INDEX (1) for a bad slot or length."""
     d = _here(page_table, "page_table")
     cap = page_table.shape[-1]
-    i32, L = torch.int32, lib()
     n_free = n_slots if free_slots is None else free_slots.numel()
     max_tokens = 0 if slot_map is None else slot_map.shape[0]
     max_list = 0 if block_list is None else block_list.shape[0]
-    _check(L.scout_build_tables(
-        _opt_sized(prev_len, i32, B, "prev_len", d), _sized(seq_len, i32, B, "seq_len", d),
-        _opt_sized(free_slots, i32, n_free, "free_slots", d), n_free, n_slots, B, Hkv, P, cap,
-        _sized(page_table, i32, B * Hkv * cap, "page_table", d),
-        _sized(resident_bits, i32, B * Hkv * (-(-cap // 32)), "resident_bits", d),
-        _opt_sized(cu_tokens, i32, B + 1, "cu_tokens", d),
-        _opt_sized(slot_map, torch.int64, max_tokens * Hkv, "slot_map", d), max_tokens,
-        _opt_sized(block_list, i32, max_list * 2, "block_list", d), max_list, _opt_sized(counts, i32, 3, "counts", d),
-        _opt_sized(status, i32, 1, "status", d), _stream(stream)), "scout_build_tables")
+    _check(lib().scout_build_tables(
+        None if prev_len is None else _sized(prev_len, _I32, B, "prev_len", d), _sized(seq_len, _I32, B, "seq_len", d),
+        None if free_slots is None else _sized(free_slots, _I32, n_free, "free_slots", d), n_free, n_slots, B, Hkv, P, cap,
+        _sized(page_table, _I32, B * Hkv * cap, "page_table", d),
+        _sized(resident_bits, _I32, B * Hkv * (-(-cap // 32)), "resident_bits", d),
+        None if cu_tokens is None else _sized(cu_tokens, _I32, B + 1, "cu_tokens", d),
+        None if slot_map is None else _sized(slot_map, _I64, max_tokens * Hkv, "slot_map", d), max_tokens,
+        None if block_list is None else _sized(block_list, _I32, max_list * 2, "block_list", d), max_list,
+        None if counts is None else _sized(counts, _I32, 3, "counts", d),
+        None if status is None else _sized(status, _I32, 1, "status", d), _stream_on(stream, d)), "scout_build_tables")
     return page_table, resident_bits
 
 
@@ -406,10 +413,9 @@ def append_kv(K_new, V_new, slot_map, Hkv, P, K_pool, V_pool, status=None, strea
     if n == 0:
         return K_pool, V_pool
     _check(lib().scout_append_kv(
-        kp, ld_k, vp, ld_v, _sized(slot_map, torch.int64, n * Hkv, "slot_map", d), n, Hkv, D, P,
-        _sized(K_pool, torch.bfloat16, n_slots * P * D, "K_pool", d),
-        _sized(V_pool, torch.bfloat16, n_slots * P * D, "V_pool", d), n_slots,
-        _opt_sized(status, torch.int32, 1, "status", d), _stream(stream)), "scout_append_kv")
+        kp, ld_k, vp, ld_v, _sized(slot_map, _I64, n * Hkv, "slot_map", d), n, Hkv, D, P,
+        _sized(K_pool, _BF16, n_slots * P * D, "K_pool", d), _sized(V_pool, _BF16, n_slots * P * D, "V_pool", d), n_slots,
+        None if status is None else _sized(status, _I32, 1, "status", d), _stream_on(stream, d)), "scout_append_kv")
     return K_pool, V_pool
 
 
@@ -428,13 +434,13 @@ def append_kv8(K_new, V_new, page_table, seq_len, B, Hkv, P, K_pool, V_pool, K_s
         raise ScoutError("K_new and V_new must hold the same tokens")
     if n == 0:
         return K_pool, V_pool
-    i32, f32, pool = torch.int32, torch.float32, n_slots * P * D
+    pool, dtype = n_slots * P * D, K_pool.dtype
     _check(lib().scout_append_kv8(
-        fmt, kp, ld_k, vp, ld_v, n, _opt_sized(prev_len, i32, B, "prev_len", d), _sized(seq_len, i32, B, "seq_len", d),
-        _sized(page_table, i32, B * Hkv * cap, "page_table", d), B, Hkv, D, P, cap,
-        _sized(K_pool, K_pool.dtype, pool, "K_pool", d), _sized(V_pool, K_pool.dtype, pool, "V_pool", d),
-        _sized(K_scale, f32, n_slots, "K_scale", d), _sized(V_scale, f32, n_slots, "V_scale", d), n_slots,
-        _opt_sized(status, i32, 1, "status", d), _stream(stream)), "scout_append_kv8")
+        fmt, kp, ld_k, vp, ld_v, n, None if prev_len is None else _sized(prev_len, _I32, B, "prev_len", d),
+        _sized(seq_len, _I32, B, "seq_len", d), _sized(page_table, _I32, B * Hkv * cap, "page_table", d), B, Hkv, D, P, cap,
+        _sized(K_pool, dtype, pool, "K_pool", d), _sized(V_pool, dtype, pool, "V_pool", d),
+        _sized(K_scale, _F32, n_slots, "K_scale", d), _sized(V_scale, _F32, n_slots, "V_scale", d), n_slots,
+        None if status is None else _sized(status, _I32, 1, "status", d), _stream_on(stream, d)), "scout_append_kv8")
     return K_pool, V_pool
 
 
@@ -445,16 +451,16 @@ def build_digest8(kind, K_pool, K_scale, page_table, seq_len, B, Hkv, P, digest,
     kind = _KIND[kind]
     d = _here(K_pool, "K_pool")
     fmt, n_slots = _pool8(K_pool, None, P)
-    D, cap, i32 = K_pool.shape[-1], page_table.shape[-1], torch.int32
+    D, cap = K_pool.shape[-1], page_table.shape[-1]
     n_list = 0 if block_list is None else block_list.shape[0]
-    ddt, per = (torch.bfloat16, 2 * D) if kind == MINMAX else (torch.float32, D)
+    ddt, per = (_BF16, 2 * D) if kind == MINMAX else (_F32, D)
     _check(lib().scout_build_digest8(
         kind, fmt, _sized(K_pool, K_pool.dtype, n_slots * P * D, "K_pool", d),
-        _sized(K_scale, torch.float32, n_slots, "K_scale", d), n_slots,
-        _sized(page_table, i32, B * Hkv * cap, "page_table", d), _sized(seq_len, i32, B, "seq_len", d), B, Hkv, D, P, cap,
-        _opt_sized(block_list, i32, n_list * 2, "block_list", d), n_list,
-        _sized(digest, ddt, B * Hkv * cap * per, "digest", d), _opt_sized(status, i32, 1, "status", d),
-        _stream(stream)), "scout_build_digest8")
+        _sized(K_scale, _F32, n_slots, "K_scale", d), n_slots, _sized(page_table, _I32, B * Hkv * cap, "page_table", d),
+        _sized(seq_len, _I32, B, "seq_len", d), B, Hkv, D, P, cap,
+        None if block_list is None else _sized(block_list, _I32, n_list * 2, "block_list", d), n_list,
+        _sized(digest, ddt, B * Hkv * cap * per, "digest", d),
+        None if status is None else _sized(status, _I32, 1, "status", d), _stream_on(stream, d)), "scout_build_digest8")
     return digest
 
 
@@ -463,56 +469,51 @@ def sparse_attn8_workspace(B, Hq, Hkv, P, D=128, device="cuda") -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _attn8_args(q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq, Hkv, P, k, scale):
-    """The arguments both 8-bit attention calls begin with."""
+def _attn8(what, merge, q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq, Hkv, P, k,
+           scale, workspace, cpu, O, lse, status, max_ctas, stream):
+    """Both 8-bit attention calls: ``cpu`` is the (O, lse) partial to merge, or None."""
     d = _here(q, "q")
     fmt, n_slots = _pool8(K_pool, V_pool, P)
-    D, cap, i32, f32 = K_pool.shape[-1], page_table.shape[-1], torch.int32, torch.float32
-    pool = n_slots * P * D
-    return d, D, (
-        fmt, _sized(q, torch.bfloat16, B * Hq * D, "q", d), _sized(K_pool, K_pool.dtype, pool, "K_pool", d),
-        _sized(V_pool, K_pool.dtype, pool, "V_pool", d), _sized(K_scale, f32, n_slots, "K_scale", d),
-        _sized(V_scale, f32, n_slots, "V_scale", d), n_slots, _sized(page_table, i32, B * Hkv * cap, "page_table", d),
-        _sized(seq_len, i32, B, "seq_len", d), _sized(res_list, i32, B * Hkv * k, "res_list", d),
-        _sized(res_count, i32, B * Hkv, "res_count", d), B, Hq, Hkv, D, P, cap, k, float(scale))
+    D, cap, dtype, rows = K_pool.shape[2], page_table.shape[-1], K_pool.dtype, B * Hq
+    odt = _BF16 if merge else _F32
+    if O is None:
+        O = torch.empty((B, Hq, D), dtype=odt, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=_F32, device=q.device)
+    pool, units, wsb = n_slots * P * D, B * Hkv, workspace.numel()
+    head = (fmt, _sized(q, _BF16, rows * D, "q", d), _sized(K_pool, dtype, pool, "K_pool", d),
+            _sized(V_pool, dtype, pool, "V_pool", d), _sized(K_scale, _F32, n_slots, "K_scale", d),
+            _sized(V_scale, _F32, n_slots, "V_scale", d), n_slots, _sized(page_table, _I32, units * cap, "page_table", d),
+            _sized(seq_len, _I32, B, "seq_len", d), _sized(res_list, _I32, units * k, "res_list", d),
+            _sized(res_count, _I32, units, "res_count", d), B, Hq, Hkv, D, P, cap, k, scale)
+    tail = (_sized(O, odt, rows * D, "O", d), _sized(lse, _F32, rows, "lse", d), _sized(workspace, _U8, wsb, "workspace", d),
+            wsb, None if status is None else _sized(status, _I32, 1, "status", d),
+            None if max_ctas is None else _launch(max_ctas), _stream_on(stream, d))
+    if merge:
+        rc = lib().scout_sparse_attn8_merge(*head, _sized(cpu[0], _F32, rows * D, "O_cpu", d),
+                                            _sized(cpu[1], _F32, rows, "lse_cpu", d), *tail)
+    else:
+        rc = lib().scout_sparse_attn8(*head, *tail)
+    if rc != 0:
+        _check(rc, what)
+    return O, lse
 
 
 def sparse_attn8(q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq, Hkv, P, k, scale,
                  workspace, O=None, lse=None, status=None, max_ctas=None, stream=None):
     """Partial attention over the listed blocks of an 8-bit cache (float8 pools [n_slots][P][D], fp32
     scales [n_slots]) -> (O fp32 [B][Hq][D], lse fp32 [B][Hq])."""
-    d, D, args = _attn8_args(q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq, Hkv,
-                             P, k, scale)
-    if O is None:
-        O = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    f32 = torch.float32
-    _check(lib().scout_sparse_attn8(
-        *args, _sized(O, f32, B * Hq * D, "O", d), _sized(lse, f32, B * Hq, "lse", d),
-        _sized(workspace, torch.uint8, workspace.numel(), "workspace", d), workspace.numel(),
-        _opt_sized(status, torch.int32, 1, "status", d), _launch(max_ctas), _stream(stream)), "scout_sparse_attn8")
-    return O, lse
+    return _attn8("scout_sparse_attn8", False, q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list,
+                  res_count, B, Hq, Hkv, P, k, scale, workspace, None, O, lse, status, max_ctas, stream)
 
 
 def sparse_attn8_merge(q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq, Hkv, P, k,
                        scale, workspace, O_cpu, lse_cpu, O_out=None, lse_out=None, status=None, max_ctas=None,
                        stream=None):
     """The same merged with the CPU partial -> (O bf16 [B][Hq][D], lse fp32 [B][Hq])."""
-    d, D, args = _attn8_args(q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq, Hkv,
-                             P, k, scale)
-    if O_out is None:
-        O_out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
-    if lse_out is None:
-        lse_out = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    f32 = torch.float32
-    _check(lib().scout_sparse_attn8_merge(
-        *args, _sized(O_cpu, f32, B * Hq * D, "O_cpu", d), _sized(lse_cpu, f32, B * Hq, "lse_cpu", d),
-        _sized(O_out, torch.bfloat16, B * Hq * D, "O_out", d), _sized(lse_out, f32, B * Hq, "lse_out", d),
-        _sized(workspace, torch.uint8, workspace.numel(), "workspace", d), workspace.numel(),
-        _opt_sized(status, torch.int32, 1, "status", d), _launch(max_ctas), _stream(stream)),
-        "scout_sparse_attn8_merge")
-    return O_out, lse_out
+    return _attn8("scout_sparse_attn8_merge", True, q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list,
+                  res_count, B, Hq, Hkv, P, k, scale, workspace, (O_cpu, lse_cpu), O_out, lse_out, status, max_ctas,
+                  stream)
 
 
 def recall_async(ops, host_K, host_V, K_pool, V_pool, B, Hkv, P, nblk_cap, side_stream, wait_event=None,

@@ -18,10 +18,10 @@ namespace {
 constexpr int kA8Warps = 8;
 
 struct App8Args {
-  const __nv_bfloat16* src[2];  // K, V rows
-  int64_t ld[2];                // elements from a token to the next
-  uint8_t* pool[2];
-  float* scale[2];
+  const __nv_bfloat16 *K, *V;  // new rows
+  int64_t ld_k, ld_v;          // elements from a token to the next
+  uint8_t *K_pool, *V_pool;
+  float *K_scale, *V_scale;
   const int32_t* prev_len;
   const int32_t* seq_len;
   const int32_t* page_table;
@@ -30,18 +30,15 @@ struct App8Args {
   int32_t* status;
 };
 
-// largest finite |x| of the eight bf16 of v, into the running pair maximum m (packed magnitudes):
-// bf16 magnitudes order as integers; infinities and NaN count as zero
-__device__ __forceinline__ uint32_t finite_max(uint32_t m, const uint4& v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t a = w[i] & 0x7fff7fffu;
-    a = __vminu2(a, 0x7f807f80u);            // NaN magnitudes become infinity's
-    a &= ~__vcmpeq2(a, 0x7f807f80u);         // and those zero
-    m = __vmaxu2(m, a);
-  }
-  return m;
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t x) {
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                   __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x)));  // passes over NaN
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// the same with infinities (and NaN) as zero
+__device__ __forceinline__ uint32_t finite2(uint32_t x) {
+  return (((x & 0x7f80u) == 0x7f80u) ? 0u : (x & 0xffffu)) |
+         (((x & 0x7f800000u) == 0x7f800000u) ? 0u : (x & 0xffff0000u));
 }
 
 template <int F>
@@ -66,26 +63,25 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
 template <int P, int F>
 __global__ void __launch_bounds__(kA8Warps * 32) append8_kernel(const App8Args a) {
   extern __shared__ int sm[];
-  __shared__ int partial[32];
+  __shared__ int partial[2 * 32];
   const int B = a.B;
   int* tok = sm;            // [B + 1] new tokens before sequence b
   int* tou = sm + (B + 1);  // [B + 1] touched blocks (of one KV head) before it
   const int tid = threadIdx.x, lane = tid & 31;
   const int cap_tokens = a.nblk_cap * P;
-  for (int b = tid; b < B; b += blockDim.x) {
+  int* const out[2] = {tok, tou};
+  cta_prefixes<2>(B, out, partial, [&](int b, int (&x)[2]) {
     const SeqSpan s = seq_span(a.prev_len, a.seq_len, b, cap_tokens);
-    tok[b] = s.seq - s.prev;
-    tou[b] = s.seq > s.prev ? (s.seq + P - 1) / P - s.prev / P : 0;
-    if (blockIdx.x == 0) report_span(a.status, a.prev_len, a.seq_len, b, cap_tokens);
-  }
-  __syncthreads();
-  cta_exclusive_prefix(tok, B, partial);
-  cta_exclusive_prefix(tou, B, partial);
+    x[0] = s.seq - s.prev;
+    x[1] = s.seq > s.prev ? (s.seq + P - 1) / P - s.prev / P : 0;
+  });
+  if (blockIdx.x == 0)
+    for (int b = tid; b < B; b += blockDim.x) report_span(a.status, a.prev_len, a.seq_len, b, cap_tokens);
   const int64_t items = (int64_t)tou[B] * a.Hkv * 2;
   const int half = lane >> 4, chunk = lane & 15;
   const int64_t wn = (int64_t)gridDim.x * kA8Warps;
   for (int64_t it = (int64_t)blockIdx.x * kA8Warps + (tid >> 5); it < items; it += wn) {
-    const int which = (int)(it & 1);
+    const bool is_v = (it & 1) != 0;
     const int64_t bh = it >> 1;
     const int blk = (int)(bh / a.Hkv), h = (int)(bh - (int64_t)blk * a.Hkv);
     const int b = owner_of(tou, B, blk);
@@ -93,36 +89,46 @@ __global__ void __launch_bounds__(kA8Warps * 32) append8_kernel(const App8Args a
     const int j = s.prev / P + blk - tou[b];
     const int r0 = max(s.prev - j * P, 0), r1 = min(s.seq - j * P, P);  // the block's new rows
     const int64_t i0 = (int64_t)tok[b] + (j * P - s.prev);              // token row of its row 0
-    const int slot = a.page_table[((int64_t)b * a.Hkv + h) * a.nblk_cap + j];
-    if (slot < 0 || slot >= a.n_slots || i0 + r1 > a.n_tokens) {
-      if (lane == 0) report(a.status, SCOUT_DEV_BAD_INDEX);
-      continue;
-    }
-    const __nv_bfloat16* src = a.src[which] + i0 * a.ld[which] + h * kD + chunk * 8;
-    uint8_t* page = a.pool[which] + (int64_t)slot * (P * kD) + chunk * 8;
-    const float old = r0 > 0 ? a.scale[which][slot] : 0.f;
+    const int slot = a.page_table[((int64_t)b * a.Hkv + h) * a.nblk_cap + j];  // in flight with the rows
+    const int64_t ld = is_v ? a.ld_v : a.ld_k;
+    const bool rows_ok = i0 + r1 <= a.n_tokens;
+    const __nv_bfloat16* src = (is_v ? a.V : a.K) + i0 * ld + h * kD + chunk * 8;
     uint4 v[P / 2];
-    uint32_t m = 0u;
 #pragma unroll
     for (int i = 0; i < P / 2; ++i) {
       const int r = 2 * i + half;
-      v[i] = r >= r0 && r < r1 ? ldg_stream(src + (int64_t)r * a.ld[which]) : make_uint4(0u, 0u, 0u, 0u);
+      v[i] = r >= r0 && r < r1 && rows_ok ? ldg_stream(src + (int64_t)r * ld) : make_uint4(0u, 0u, 0u, 0u);
     }
+    if (slot < 0 || slot >= a.n_slots || !rows_ok) {
+      if (lane == 0) report(a.status, SCOUT_DEV_BAD_INDEX);
+      continue;
+    }
+    uint8_t* page = (is_v ? a.V_pool : a.K_pool) + (int64_t)slot * (P * kD) + chunk * 8;
+    float* scale_at = (is_v ? a.V_scale : a.K_scale) + slot;
+    const float old = r0 > 0 ? *scale_at : 0.f;
+    uint32_t m = 0u;
 #pragma unroll
-    for (int i = 0; i < P / 2; ++i) m = finite_max(m, v[i]);
-    const uint32_t big = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-    const uint32_t e = scale_exponent<F>(__uint_as_float(big << 16));
-    const float need = pow2_biased(e);
+    for (int i = 0; i < P / 2; ++i) m = max_abs2(max_abs2(max_abs2(max_abs2(m, v[i].x), v[i].y), v[i].z), v[i].w);
+    uint32_t big = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+    if (big == 0x7f80u) {  // an infinity among them: the largest of the others (rare)
+      m = 0u;
+#pragma unroll 1
+      for (int r = r0 + half; r < r1; r += 2) {  // the same rows, from memory (L2)
+        const uint4 x = ldg_stream(src + (int64_t)r * ld);
+        m = max_abs2(max_abs2(max_abs2(max_abs2(m, finite2(x.x)), finite2(x.y)), finite2(x.z)), finite2(x.w));
+      }
+      big = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+    }
+    const float need = pow2_biased(scale_exponent<F>(__uint_as_float(big << 16)));
     // the scale of a block with cached tokens never shrinks
     const bool grows = r0 > 0 && need > old;
     const float scale = r0 > 0 && !grows ? old : need;
-    // both factors are exact where the scales are powers of two (1 / 2^-126 = 2^126 is finite)
+    // exact where the scale is a power of two (1 / 2^-126 = 2^126 is finite)
     const float inv = 1.f / scale;
     if (grows) {
       const float ratio = old / need;
-      for (int i = 0; i < P / 2; ++i) {
-        const int r = 2 * i + half;
-        if (r >= r0) continue;
+#pragma unroll 1
+      for (int r = half; r < r0; r += 2) {
         uint2* at = reinterpret_cast<uint2*>(page + r * kD);
         const uint2 c = *at;
         *at = make_uint2(recode4<F>(c.x, ratio), recode4<F>(c.y, ratio));
@@ -133,7 +139,7 @@ __global__ void __launch_bounds__(kA8Warps * 32) append8_kernel(const App8Args a
       const int r = 2 * i + half;
       if (r >= r0 && r < r1) *reinterpret_cast<uint2*>(page + r * kD) = encode8<F>(v[i], inv);
     }
-    if (lane == 0 && (r0 == 0 || grows)) a.scale[which][slot] = scale;
+    if (lane == 0 && (r0 == 0 || grows)) *scale_at = scale;
   }
 }
 
@@ -176,14 +182,14 @@ extern "C" int scout_append_kv8(int fmt, const void* K_new, int64_t ld_k, const 
     return SCOUT_ERR_UNSUPPORTED;
   if (n_tokens == 0) return SCOUT_OK;
   App8Args a;
-  a.src[0] = static_cast<const __nv_bfloat16*>(K_new);
-  a.src[1] = static_cast<const __nv_bfloat16*>(V_new);
-  a.ld[0] = ld_k;
-  a.ld[1] = ld_v;
-  a.pool[0] = static_cast<uint8_t*>(K_pool);
-  a.pool[1] = static_cast<uint8_t*>(V_pool);
-  a.scale[0] = K_scale;
-  a.scale[1] = V_scale;
+  a.K = static_cast<const __nv_bfloat16*>(K_new);
+  a.V = static_cast<const __nv_bfloat16*>(V_new);
+  a.ld_k = ld_k;
+  a.ld_v = ld_v;
+  a.K_pool = static_cast<uint8_t*>(K_pool);
+  a.V_pool = static_cast<uint8_t*>(V_pool);
+  a.K_scale = K_scale;
+  a.V_scale = V_scale;
   a.prev_len = prev_len;
   a.seq_len = seq_len;
   a.page_table = page_table;

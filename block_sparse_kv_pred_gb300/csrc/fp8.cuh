@@ -89,29 +89,49 @@ __device__ __forceinline__ void report_span(int32_t* status, const int32_t* prev
   if (n < 0 || p < 0 || p > max(n, 0)) report(status, SCOUT_DEV_BAD_INDEX);
 }
 
-// In-place exclusive prefix over v[0 .. B), v[B] = the total, by all threads of a CTA (a multiple
-// of 32, at most 1024); partial[] holds 32 ints.  Ends with a barrier.
-__device__ __forceinline__ void cta_exclusive_prefix(int* v, int B, int* partial) {
+// K exclusive prefixes over b < B at once: f(b, x) gives the K values of b, out[k][b] the sum of those
+// before it and out[k][B] the total.  By all threads of a CTA (a multiple of 32, at most 1024), a run
+// of b a thread; f is called twice, so that a thread's first reads are all in flight together and
+// the second ones hit L1.  partial: K * 32 ints.  Ends with a barrier.
+template <int K, class F>
+__device__ __forceinline__ void cta_prefixes(int B, int* const (&out)[K], int* partial, F f) {
   const int tid = threadIdx.x, n = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int per = (B + n - 1) / n, lo = min(B, tid * per), hi = min(B, lo + per);
-  int sum = 0;
-  for (int i = lo; i < hi; ++i) sum += v[i];
-  int inc = sum;
+  int sum[K], run[K], x[K];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
+  for (int k = 0; k < K; ++k) sum[k] = 0;
+#pragma unroll 4
+  for (int b = lo; b < hi; ++b) {
+    f(b, x);
+#pragma unroll
+    for (int k = 0; k < K; ++k) sum[k] += x[k];
   }
-  if (lane == 31) partial[warp] = inc;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    run[k] = sum[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, run[k], o);
+      if (lane >= o) run[k] += y;
+    }
+    if (lane == 31) partial[k * 32 + warp] = run[k];
+    run[k] -= sum[k];
+  }
   __syncthreads();
-  int run = inc - sum;
-  for (int w = 0; w < warp; ++w) run += partial[w];
-  for (int i = lo; i < hi; ++i) {
-    const int x = v[i];
-    v[i] = run;
-    run += x;
+  for (int w = 0; w < warp; ++w)
+#pragma unroll
+    for (int k = 0; k < K; ++k) run[k] += partial[k * 32 + w];
+  for (int b = lo; b < hi; ++b) {
+    f(b, x);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      out[k][b] = run[k];
+      run[k] += x[k];
+    }
   }
-  if (tid == n - 1) v[B] = run;
+  if (tid == n - 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) out[k][B] = run[k];
   __syncthreads();
 }
 

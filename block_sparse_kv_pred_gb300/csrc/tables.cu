@@ -33,23 +33,26 @@ struct TabArgs {
   int32_t* status;
 };
 
-// Slot of the i-th new block of the batch: -1 (reported) past the free list or outside the pool.
+constexpr int kBatch = 4;
+
+// Slot of the i-th new block of the batch (kNoSlot past the free list), unchecked: the read is in
+// flight when this returns.
+constexpr int kNoSlot = -2;
 __device__ __forceinline__ int take_slot(const TabArgs& a, int i) {
-  if (i >= a.n_free) {
-    report(a.status, SCOUT_DEV_OVERFLOW);
-    return -1;
-  }
-  const int s = a.free_slots != nullptr ? a.free_slots[i] : i;
-  if (s < 0 || s >= a.n_slots) {
-    report(a.status, SCOUT_DEV_BAD_INDEX);
-    return -1;
-  }
-  return s;
+  if (i >= a.n_free) return kNoSlot;
+  return a.free_slots != nullptr ? max(a.free_slots[i], -1) : i;
+}
+// The slot of a lane that has one, -1 (reported) where it is none of the pool's.
+__device__ __forceinline__ int checked(const TabArgs& a, bool has, int s) {
+  if (!has) return -1;
+  if (s >= 0 && s < a.n_slots) return s;
+  report(a.status, s == kNoSlot ? SCOUT_DEV_OVERFLOW : SCOUT_DEV_BAD_INDEX);
+  return -1;
 }
 
 __global__ void __launch_bounds__(kTabWarps * 32) tables_kernel(const TabArgs a) {
   extern __shared__ int sm[];
-  __shared__ int partial[32];
+  __shared__ int partial[3 * 32];
   const int B = a.B, P = a.P;
   int* tok = sm;              // [B + 1] new tokens before sequence b
   int* tou = sm + (B + 1);    // [B + 1] touched blocks (of one KV head)
@@ -58,20 +61,19 @@ __global__ void __launch_bounds__(kTabWarps * 32) tables_kernel(const TabArgs a)
   int* seq = prv + B;         // [B] clamped lengths
   const int tid = threadIdx.x, lane = tid & 31;
   const int cap_tokens = a.nblk_cap * P;
-  for (int b = tid; b < B; b += blockDim.x) {
+  const int lg = P == 16 ? 4 : P == 32 ? 5 : 6;  // P = 2^lg
+  int* const out[3] = {tok, tou, neu};
+  cta_prefixes<3>(B, out, partial, [&](int b, int (&x)[3]) {
     const SeqSpan s = seq_span(a.prev_len, a.seq_len, b, cap_tokens);
     prv[b] = s.prev;
     seq[b] = s.seq;
-    const int nb = (s.seq + P - 1) / P;
-    tok[b] = s.seq - s.prev;
-    tou[b] = s.seq > s.prev ? nb - s.prev / P : 0;
-    neu[b] = nb - (s.prev + P - 1) / P;
-    if (blockIdx.x == 0) report_span(a.status, a.prev_len, a.seq_len, b, cap_tokens);
-  }
-  __syncthreads();
-  cta_exclusive_prefix(tok, B, partial);
-  cta_exclusive_prefix(tou, B, partial);
-  cta_exclusive_prefix(neu, B, partial);
+    const int nb = (s.seq + P - 1) >> lg;
+    x[0] = s.seq - s.prev;
+    x[1] = s.seq > s.prev ? nb - (s.prev >> lg) : 0;
+    x[2] = nb - ((s.prev + P - 1) >> lg);
+  });
+  if (blockIdx.x == 0)
+    for (int b = tid; b < B; b += blockDim.x) report_span(a.status, a.prev_len, a.seq_len, b, cap_tokens);
   const int n_tok = tok[B], n_tou = tou[B];
   const int64_t n_list = (int64_t)n_tou * a.Hkv;
   if (blockIdx.x == 0) {
@@ -89,56 +91,95 @@ __global__ void __launch_bounds__(kTabWarps * 32) tables_kernel(const TabArgs a)
   }
   const int64_t w0 = (int64_t)blockIdx.x * kTabWarps + (tid >> 5), wn = (int64_t)gridDim.x * kTabWarps;
 
-  // rows of the page table, a word of 32 blocks at a time; a grown row gets its new blocks only
+  // rows of the page table, a word of 32 blocks at a time; a grown row gets its new blocks only.
+  // kBatch items of a warp together: their free slots are all in flight before the first is stored.
   const int64_t n_words = (int64_t)B * a.Hkv * a.words;
-  for (int64_t it = w0; it < n_words; it += wn) {
-    const int64_t u = it / a.words;
-    const int w = (int)(it - u * a.words);
-    const int b = (int)(u / a.Hkv), h = (int)(u - (int64_t)b * a.Hkv);
-    const int j0 = (prv[b] + P - 1) / P, j1 = (seq[b] + P - 1) / P;  // new blocks
-    if (a.prev_len != nullptr && (w * 32 + 32 <= j0 || w * 32 >= j1)) continue;
-    const int j = w * 32 + lane;
-    int s = -1;
-    const bool fresh = j >= j0 && j < j1;
-    if (fresh) s = take_slot(a, neu[b] * a.Hkv + h * (j1 - j0) + (j - j0));
-    if (j < a.nblk_cap && (fresh || a.prev_len == nullptr)) a.page_table[u * a.nblk_cap + j] = s;
-    const uint32_t m = __ballot_sync(0xffffffffu, s >= 0);
-    if (lane == 0) {
-      if (a.prev_len == nullptr) a.bits[it] = m;
-      else if (m != 0u) atomicOr(&a.bits[it], m);
+  for (int64_t it0 = w0; it0 < n_words; it0 += kBatch * wn) {
+    int slot[kBatch];
+    bool fresh[kBatch], mine[kBatch];
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      const int64_t it = it0 + y * wn;
+      fresh[y] = mine[y] = false;
+      slot[y] = -1;
+      if (it >= n_words) continue;
+      const int u = (int)((unsigned)it / (unsigned)a.words), w = (int)it - u * a.words;
+      const int b = u / a.Hkv, h = u - b * a.Hkv;
+      const int j0 = (prv[b] + P - 1) >> lg, j1 = (seq[b] + P - 1) >> lg;  // new blocks
+      mine[y] = a.prev_len == nullptr || (w * 32 + 32 > j0 && w * 32 < j1);
+      const int j = w * 32 + lane;
+      fresh[y] = j >= j0 && j < j1;
+      if (fresh[y]) slot[y] = take_slot(a, neu[b] * a.Hkv + h * (j1 - j0) + (j - j0));
+    }
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      const int64_t it = it0 + y * wn;
+      const int u = (int)((unsigned)it / (unsigned)a.words), j = ((int)it - u * a.words) * 32 + lane;
+      slot[y] = checked(a, fresh[y], slot[y]);
+      const uint32_t m = __ballot_sync(0xffffffffu, slot[y] >= 0);
+      if (!mine[y]) continue;
+      if (j < a.nblk_cap && (fresh[y] || a.prev_len == nullptr)) a.page_table[(int64_t)u * a.nblk_cap + j] = slot[y];
+      if (lane == 0) {
+        if (a.prev_len == nullptr) a.bits[it] = m;
+        else if (m != 0u) atomicOr(&a.bits[it], m);
+      }
     }
   }
 
-  // slot map: the tokens of one touched block of a sequence, all heads
+  // slot map: the tokens of one touched block of a sequence, all heads: one contiguous piece, 32
+  // entries at a time; (r, hh) = (token, head) of a lane's entry, stepped without a division
   if (a.slot_map != nullptr) {
-    for (int64_t it = w0; it < n_tou; it += wn) {
-      const int b = owner_of(tou, B, (int)it);
-      const int j = prv[b] / P + ((int)it - tou[b]);
-      const int t0 = max(j * P, prv[b]), t1 = min((j + 1) * P, seq[b]);
-      const int j0 = (prv[b] + P - 1) / P, nb = (seq[b] + P - 1) / P - j0;
-      const int i0 = tok[b] + t0 - prv[b];  // first of its tokens
-      const int rows = min(t1 - t0, a.max_tokens - i0);
-      for (int h0 = 0; h0 < a.Hkv && rows > 0; h0 += 32) {
-        const int hn = min(32, a.Hkv - h0);
-        int s = -1;
-        if (lane < hn) {
+    const bool aligned = (reinterpret_cast<uintptr_t>(a.slot_map) & 15u) == 0;
+    for (int h0 = 0; h0 < a.Hkv; h0 += 32) {
+      const int hn = min(32, a.Hkv - h0), dr = 32 / hn, dh = 32 - dr * hn;
+      const int r_first = lane / hn, h_first = lane - r_first * hn;
+      const bool pairs = hn == a.Hkv && hn >= 2 && (hn & (hn - 1)) == 0 && aligned;
+      for (int64_t it0 = w0; it0 < n_tou; it0 += kBatch * wn) {
+        int slot[kBatch], off[kBatch], i0[kBatch], rows[kBatch];
+#pragma unroll
+        for (int y = 0; y < kBatch; ++y) {
+          const int64_t it = it0 + y * wn;
+          rows[y] = 0;
+          if (it >= n_tou) continue;
+          const int b = owner_of(tou, B, (int)it);
+          const int p = prv[b], j = (p >> lg) + ((int)it - tou[b]);
+          const int t0 = max(j << lg, p), t1 = min((j + 1) << lg, seq[b]);
+          const int j0 = (p + P - 1) >> lg, nb = ((seq[b] + P - 1) >> lg) - j0;
+          i0[y] = tok[b] + t0 - p;  // first of its tokens
+          rows[y] = min(t1 - t0, a.max_tokens - i0[y]);
+          off[y] = t0 - (j << lg);
           const int h = h0 + lane;
-          if (j >= j0) {
-            s = take_slot(a, neu[b] * a.Hkv + h * nb + (j - j0));
-          } else {  // the partly filled last block of the previous length
-            s = a.page_table[((int64_t)b * a.Hkv + h) * a.nblk_cap + j];
-            if (s < 0 || s >= a.n_slots) {
-              s = -1;
-              report(a.status, SCOUT_DEV_BAD_INDEX);
+          if (lane < hn)  // a new block's slot, or that of the partly filled last block
+            slot[y] = j >= j0 ? take_slot(a, neu[b] * a.Hkv + h * nb + (j - j0))
+                              : max(a.page_table[((int64_t)b * a.Hkv + h) * a.nblk_cap + j], -1);
+        }
+#pragma unroll
+        for (int y = 0; y < kBatch; ++y) {
+          if (rows[y] <= 0) continue;
+          const int s = checked(a, lane < hn, slot[y]);
+          const int64_t first = s < 0 ? -1 : ((int64_t)s << lg) + off[y];  // pool row of its first token
+          int64_t* dst = a.slot_map + (int64_t)i0[y] * a.Hkv + h0;
+          if (pairs) {  // 32 entry pairs at a time, always the same two heads a lane
+            const int64_t f0 = __shfl_sync(0xffffffffu, first, (2 * lane) & (hn - 1));
+            const int64_t f1 = __shfl_sync(0xffffffffu, first, (2 * lane + 1) & (hn - 1));
+            longlong2* d2 = reinterpret_cast<longlong2*>(dst) + lane;
+            const int dr2 = 64 / hn;
+#pragma unroll 4
+            for (int r = 2 * lane / hn; r < rows[y]; r += dr2, d2 += 32)
+              *d2 = make_longlong2(f0 < 0 ? -1 : f0 + r, f1 < 0 ? -1 : f1 + r);
+            continue;
+          }
+          int r = r_first, hh = h_first;
+          for (int e = 0; e < rows[y] * hn; e += 32) {
+            const int64_t f = __shfl_sync(0xffffffffu, first, hh);
+            if (r < rows[y]) dst[(int64_t)r * a.Hkv + hh] = f < 0 ? -1 : f + r;
+            r += dr;
+            hh += dh;
+            if (hh >= hn) {
+              hh -= hn;
+              ++r;
             }
           }
-        }
-        for (int e0 = 0; e0 < rows * hn; e0 += 32) {
-          const int e = e0 + lane;
-          const int r = e / hn, hh = e - r * hn;
-          const int se = __shfl_sync(0xffffffffu, s, hh);
-          if (e < rows * hn)
-            a.slot_map[(int64_t)(i0 + r) * a.Hkv + h0 + hh] = se < 0 ? -1 : (int64_t)se * P + (t0 + r) % P;
         }
       }
     }
@@ -152,11 +193,11 @@ __global__ void __launch_bounds__(kTabWarps * 32) tables_kernel(const TabArgs a)
     for (int64_t i = w0 * 32 + lane; i < a.max_list; i += wn * 32) {
       int u = -1, j = -1;
       if (i < n_list) {
-        const int b = owner_of(tou, B, (int)(i / a.Hkv));
+        const int b = owner_of(tou, B, (int)((unsigned)i / (unsigned)a.Hkv));
         const int nt = tou[b + 1] - tou[b], r = (int)(i - (int64_t)tou[b] * a.Hkv);
         const int h = r / nt;
         u = b * a.Hkv + h;
-        j = prv[b] / P + (r - h * nt);
+        j = (prv[b] >> lg) + (r - h * nt);
       }
       reinterpret_cast<int2*>(a.block_list)[i] = make_int2(u, j);
     }

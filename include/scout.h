@@ -415,8 +415,9 @@ int scout_append_kv8(int fmt, const void* K_new, int64_t ld_k, const void* V_new
 /* Block digests of an 8-bit cache: scout_build_digest over the values code * scale, with the
  * same outputs, so that scout_score_topk selects from either cache.  The minima are rounded
  * down and the maxima up to bf16, so that a digest bounds every score of its block whatever
- * the scale (with power-of-two scales both are exact).  Mean: a compensated fp32 sum of codes,
- * scaled and divided by the count.  NaN codes are passed over by the minima and maxima.
+ * the scale (with power-of-two scales both are exact).  Mean: the codes' fp32 sum (exact for
+ * e4m3, at most seven roundings deep for e5m2) times scale / count.  NaN codes are passed over by
+ * the minima and maxima.  Requires n_slots < 2^31.
  * A (-1, -1) entry of block_list is padding and skipped; any other entry outside the tables
  * sets SCOUT_DEV_BAD_INDEX. */
 int scout_build_digest8(int kind, int fmt, const void* K_pool, const float* K_scale, int64_t n_slots,

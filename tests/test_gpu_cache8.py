@@ -2,8 +2,9 @@
 oracle (oracle/cache8_oracle.py).
 
 Tolerances.  Tables, bf16 writes, codes and scales are bit-exact; min/max digests are the exact
-value rounded down and up; a mean is a compensated fp32 sum, scaled and divided (each rounding at
-most 2^-24 relative; 2^-22 of the mean magnitude is allowed).  Attention, per head, with A = scale *
+value rounded down and up; a mean passes each value through at most seven roundings of its sum and
+two more (scale / count, and the product), so it is off by at most 9 * 2^-24 of the mean magnitude
+(10 are allowed, for the products of the roundings).  Attention, per head, with A = scale *
 max_t sum_c |q_c k_tc| and n tokens: a score is 16 accumulations (two of them joined) of exact
 products, each off by at most 2^-23 A, and two fp32 products, so it is off by at most
 es = 17 * 2^-23 A + 2^-22 A; the weights are off by 2 es (numerator and sum), 2^-20 (exp2, the split
@@ -279,7 +280,7 @@ def finite_codes(rng, shape, fmt):
     return c
 
 
-def check_digest(got, exp, kind, written):
+def check_digest(got, exp, kind, written, mag=None):
     if kind == "minmax":
         lo, hi = got[..., 0, :].astype(np.float64)[written], got[..., 1, :].astype(np.float64)[written]
         elo, ehi = exp[..., 0, :][written], exp[..., 1, :][written]
@@ -291,7 +292,7 @@ def check_digest(got, exp, kind, written):
             f = b(e.astype(np.float32)).to(torch.bfloat16).double().numpy()
             assert (x == e)[f == e].all()
     else:
-        assert (np.abs(got.astype(np.float64) - exp)[written] <= 2.0 ** -22 * np.abs(exp).max()).all()
+        assert (np.abs(got.astype(np.float64) - exp)[written] <= 10 * 2.0 ** -24 * mag[written]).all()
     assert (got[~written] == 4096.0).all()
 
 
@@ -310,12 +311,13 @@ def test_digest8(kind, fmt, B, Hkv, P, top, pow2):
     shape = (B, Hkv, cap, 2, D) if kind == "minmax" else (B, Hkv, cap, D)
     ddt = torch.bfloat16 if kind == "minmax" else torch.float32
     exp = C8.digest8(kind, codes, scales, table, seq, fmt, P, np.full(shape, 4096.0))
+    mag = C8.digest8(kind, codes & 0x7F, scales, table, seq, fmt, P, np.full(shape, 4096.0))  # of the magnitudes
     written = np.broadcast_to((np.arange(cap) * P < seq[:, None])[:, None, :], (B, Hkv, cap))
     dg = torch.full(shape, 4096.0, dtype=ddt, device="cuda")
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     args = (kind, pool8(codes, fmt), dev(scales), i32(table), i32(seq), B, Hkv, P)
     bs.build_digest8(*args, dg, status=status)
-    check_digest(dg.float().cpu().numpy(), exp, kind, written)
+    check_digest(dg.float().cpu().numpy(), exp, kind, written, mag)
     assert int(status) == 0
     # by list: padding is skipped, the rest of the digest stays
     pick = [(u, j) for u in range(B * Hkv) for j in range(cap) if written.reshape(-1, cap)[u, j]][::2]
@@ -325,7 +327,7 @@ def test_digest8(kind, fmt, B, Hkv, P, top, pow2):
     bs.build_digest8(*args, dg, block_list=i32(lst), status=status)
     sel = np.zeros((B * Hkv, cap), bool)
     sel[tuple(np.array(pick).T)] = True
-    check_digest(dg.float().cpu().numpy(), exp, kind, sel.reshape(B, Hkv, cap))
+    check_digest(dg.float().cpu().numpy(), exp, kind, sel.reshape(B, Hkv, cap), mag)
     assert int(status) == 0
     bs.build_digest8(*args, dg, block_list=i32([[B * Hkv, 0], [0, -1], [-1, 0], [0, cap]]), status=status)
     assert int(status) == 1
