@@ -40,7 +40,7 @@ constexpr int kCtasPerSm = 2;
 // lists of 58 blocks of 32 tokens, 8 KV heads: 1 sequence (7 steps more) 18.3 | 11.3 us, 16 (4 more)
 // 25.7 | 22.2 us, 32 (1 more) 29.3 | 31.6 us.
 constexpr int kWholeSteps = 2;
-constexpr int kPieces = 16;            // of a cut unit, merged at a time
+constexpr int kPieces = 8;             // of a cut unit, merged at a time
 constexpr int kMaxUnits8 = 4096;
 constexpr int kMaxGrid8 = 512;
 constexpr int64_t kMaxSteps = (int64_t)1 << 29;
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __gr
   const int n_cut = ((int)cut0 + (int)cut1) * a.G;
   auto cut_unit = [&](int q) { return q < a.G && cut0 ? v0 : v1; };  // of task q: unit, then q % G the head
   auto piece_of = [&](int v, int h, int cc) {
-    return (int64_t)((cc * 2 + (prefix[v] <= ranges.first(cc) ? 0 : 1)) * kMaxG + h);
+    return (cc * 2 + (prefix[v] <= ranges.first(cc) ? 0 : 1)) * kMaxG + h;
   };
   int arrived = -1;  // of lane k: the count before it of this warp's k-th task
 #pragma unroll 1
@@ -835,13 +835,15 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __gr
     float2 o[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     for (int b0 = c0; b0 <= c1; b0 += kPieces) {  // all loads of a batch together
       const int nb = min(kPieces, c1 - b0 + 1);
-      const float lse = (lane & (kPieces - 1)) < nb ? __ldcg(a.slot_lse + piece_of(v, h, b0 + (lane & (kPieces - 1)))) : -INFINITY;
+      const int e_lane = lane & (kPieces - 1), at_lane = piece_of(v, h, b0 + min(e_lane, nb - 1));
+      const float lse = e_lane < nb ? __ldcg(a.slot_lse + at_lane) : -INFINITY;
       float2 p[kPieces][2];
 #pragma unroll
       for (int e = 0; e < kPieces; ++e) {
         p[e][0] = p[e][1] = make_float2(0.f, 0.f);
+        const int64_t at_piece = __shfl_sync(0xffffffffu, at_lane, e);
         if (e < nb) {
-          const float2* src = reinterpret_cast<const float2*>(a.slot_O + piece_of(v, h, b0 + e) * kD);
+          const float2* src = reinterpret_cast<const float2*>(a.slot_O + at_piece * kD);
           p[e][0] = __ldcg(src + lane);
           p[e][1] = __ldcg(src + lane + 32);
         }
