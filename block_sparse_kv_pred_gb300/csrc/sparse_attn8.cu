@@ -51,6 +51,12 @@ constexpr int kCtasPerSm = 2;
 // 25.7 | 22.2 us, 32 (1 more) 29.3 | 31.6 us.
 constexpr int kWholeSteps = 2;
 constexpr int kPieces = 8;             // of a cut unit, merged at a time
+#ifndef SCOUT_CS
+#define SCOUT_CS 4
+#define SCOUT_MC 8
+#endif
+constexpr int kMaxCluster = SCOUT_MC;
+constexpr int kClusterSteps = SCOUT_CS;
 constexpr int kMaxUnits8 = 4096;
 constexpr int kMaxGrid8 = 512;
 constexpr int64_t kMaxSteps = (int64_t)1 << 29;
@@ -455,6 +461,321 @@ __device__ __forceinline__ Joined join_one(float m, float l, float M) {
   return join_at(true, m, l, M, m, M, l * fast_exp2(m - base), base);
 }
 
+// One warp's steps, streamed through its ring.  MAP: map(x, unit, step) gives the unit of step x of
+// the CTA's numbering, and its number in the unit.
+template <int P, int F, class MAP>
+struct WarpStream {
+  const Attn8Args& a;
+  const CUtensorMap *tmK, *tmV;
+  uint8_t* ring;     // this warp's halves
+  Tile* tiles;       // two batches
+  uint64_t* full;    // a half has landed
+  const MAP& map;
+  int lane, wlo, n_mine;  // its steps: wlo + i, i < n_mine
+  LaneOffsets off;
+  int i, at;         // the next step, and the ring half of its K
+  uint32_t phase;    // of that half's barrier
+  int issued, landed_n;  // halves
+  bool ok;           // false once a bounded wait ran out: nothing more is issued or computed
+  // a tile on its way through the three dependent reads: list entry, page-table slot, scales
+  int ru, rj, rlen, rslot, rrow, rnt;
+  float rks, rvs;
+
+  __device__ __forceinline__ WarpStream(const Attn8Args& args, const CUtensorMap* k, const CUtensorMap* v, uint8_t* sm,
+                                        uint64_t* bars, const MAP& mp, int warp, int ln, int lo, int n)
+      : a(args), tmK(k), tmV(v), ring(sm + warp * (kHalves * kHalf)),
+        tiles(reinterpret_cast<Tile*>(sm + kRingBytes8) + warp * (4 * kBatch)), full(bars + warp * kHalves), map(mp),
+        lane(ln), wlo(lo), n_mine(n), off(lane_offsets(ln)), i(0), at(0), phase(0), issued(0), landed_n(0), ok(true),
+        ru(0), rj(-1), rlen(0), rslot(-1), rrow(0), rnt(0), rks(0.f), rvs(0.f) {}
+
+  // Tile 2 kBatch b + lane of this warp.
+  __device__ __forceinline__ void resolve_entry(int batch) {
+    const int k = batch * kBatch + (lane >> 1), y = lane & 1;
+    rj = -1;
+    rlen = 0;
+    rrow = P == 16 ? 0 : 16 * y;  // first token of the tile in its page
+    if (k < n_mine) {
+      int step;
+      map(wlo + k, ru, step);
+      const int entry = P == 16 ? 2 * step + y : P == 32 ? step : step >> 1;
+      if (P == 64) rrow += 32 * (step & 1);
+      if (P != 16 || entry < min(max(a.res_count[ru], 0), a.k)) {
+        rj = a.res_list[(int64_t)ru * a.k + entry];
+        rlen = a.seq_len[ru / a.Hkv];
+        if (rj < 0 || rj >= a.nblk_cap) rj = -2;
+      }
+    }
+  }
+  __device__ __forceinline__ void resolve_slot() {
+    rslot = rj >= 0 ? a.page_table[(int64_t)ru * a.nblk_cap + rj] : -1;
+  }
+  __device__ __forceinline__ void resolve_tile() {
+    const int nv = rj >= 0 ? min(P, rlen - rj * P) : 0;
+    const bool fine = nv > 0 && rslot >= 0 && rslot < a.n_slots;
+    if (!fine && rj != -1) report(a.status, SCOUT_DEV_BAD_INDEX);
+    rnt = fine ? min(max(nv - rrow, 0), 16) : 0;
+    rrow = fine ? rslot * P + rrow : 0;
+    rks = fine ? __ldg(a.K_scale + rslot) : 0.f;
+    rvs = fine ? __ldg(a.V_scale + rslot) : 0.f;
+  }
+  __device__ __forceinline__ Tile* tile_of(int k, int y) {
+    return tiles + ((k / kBatch) & 1) * (2 * kBatch) + 2 * (k % kBatch) + y;
+  }
+
+  // Half h: K (even) or V (odd) of step h / 2, into ring half `to` = h % kHalves.  One lane; every
+  // lane has read what was there.  The box starts at a whole row (x = 0).
+  __device__ __forceinline__ void issue(int h, int to) {
+    const int k = h >> 1;
+    if (k >= n_mine || !ok) return;
+    issued = h + 1;
+    if (lane != 0) return;
+    uint64_t* bar = full + to;
+    uint8_t* dst = ring + to * kHalf;
+    const CUtensorMap* m = h & 1 ? tmV : tmK;
+    const int2 w0 = *reinterpret_cast<const int2*>(tile_of(k, 0));
+    if (P != 16) {
+      if (w0.y > 0) {
+        mbar_arrive_tx(bar, kHalf);
+        tma_load_2d(dst, m, 0, w0.x, bar);
+      } else {
+        mbar_arrive(bar);
+      }
+      return;
+    }
+    const int2 w1 = *reinterpret_cast<const int2*>(tile_of(k, 1));
+    const uint32_t bytes = (w0.y > 0 ? 2048u : 0u) + (w1.y > 0 ? 2048u : 0u);
+    if (bytes == 0u) {
+      mbar_arrive(bar);
+      return;
+    }
+    mbar_arrive_tx(bar, bytes);
+    if (w0.y > 0) tma_load_2d(dst, m, 0, w0.x, bar);
+    if (w1.y > 0) tma_load_2d(dst + 2048, m, 0, w1.x, bar);
+  }
+  __device__ __forceinline__ void landed() {
+    if (ok && !mbar_wait(full + at, phase)) {
+      if (lane == 0) report(a.status, SCOUT_DEV_TIMEOUT);
+      ok = false;
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    landed_n += ok;
+  }
+  __device__ __forceinline__ void next_half() {
+    if (++at == kHalves) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
+
+  __device__ __forceinline__ void begin() {
+    resolve_entry(0);
+    resolve_slot();
+    resolve_tile();
+    *reinterpret_cast<int2*>(&tiles[lane].row) = make_int2(rrow, rnt);
+    __syncwarp();
+    for (int h = 0; h < kHalves; ++h) issue(h, h);
+    *reinterpret_cast<float2*>(&tiles[lane].ks) = make_float2(rks, rvs);
+    __syncwarp();
+  }
+
+  // Steps i .. i_end - 1 (at least one), all of one unit, into its state; leaves the state in the
+  // ring half that the last V left, which is not reloaded before release().
+  __device__ __forceinline__ float2* run(int i_end, const uint32_t (&qb)[8][2], const float (&qf)[2], State& st) {
+    const int g = lane >> 2, t = lane & 3;
+    st.m[0] = st.m[1] = st.M[0] = st.M[1] = -INFINITY;
+    st.l[0] = st.l[1] = 0.f;
+#pragma unroll
+    for (int md = 0; md < 8; ++md) st.o[md][0] = st.o[md][1] = st.o[md][2] = st.o[md][3] = 0.f;
+    int was;
+    while (true) {
+      const int ib = i % kBatch;  // the next batch is resolved while this one runs
+      if ((i / kBatch + 1) * kBatch < n_mine) {
+        if (ib == 0) resolve_entry(i / kBatch + 1);
+        if (ib == 4) resolve_slot();
+        if (ib == 8) resolve_tile();
+        if (ib == 12) {
+          tiles[(((i / kBatch) + 1) & 1) * (2 * kBatch) + lane] = Tile{rrow, rnt, rks, rvs};
+          __syncwarp();
+        }
+      }
+      const Tile t0 = *tile_of(i, 0), t1 = *tile_of(i, 1);
+      const float kf[2][2] = {{t0.ks * qf[0], t0.ks * qf[1]}, {t1.ks * qf[0], t1.ks * qf[1]}};
+      float s[2][4];
+      const bool any = t0.nt + t1.nt > 0;
+      landed();
+      if (any && ok) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          uint4 k[4];
+          read_pieces(ring + at * kHalf + y * 2048, off.k, k);
+          tile_scores<F>(k, qb, s[y]);
+        }
+      }
+      // the reads above have returned: the products that use them have been issued
+      __syncwarp();
+      issue(2 * i + kHalves, at);
+      next_half();
+      if (any && ok) {
+        if (!(P != 16 && t1.nt == 16 && step_weights_page(s, kf[0], t0.vs, st)))
+          step_weights_any(s, kf, t0.nt, t1.nt, t0.vs, t1.vs, g, st);
+      }
+      landed();
+      if (any && ok) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          uint4 v[4];
+          const int nt = y ? t1.nt : t0.nt;
+          read_pieces(ring + at * kHalf + y * 2048, off.v, v);
+          if (nt < 16) clear_past(v, nt, lane);
+          tile_output<F>(v, s[y], st);
+        }
+      }
+      __syncwarp();  // every lane has read its V
+      was = at;
+      next_half();
+      if (++i == i_end) break;
+      issue(2 * i - 1 + kHalves, was);
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], o);
+      st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], o);
+    }
+    float2* own = reinterpret_cast<float2*>(ring + was * kHalf);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int h = 2 * t + x;
+#pragma unroll
+      for (int md = 0; md < 8; ++md)
+        if (h < a.G) own[state_at(h, g, md)] = make_float2(st.o[md][x], st.o[md][2 + x]);
+    }
+    return own;
+  }
+  // The state has been read: the half that held it goes on.
+  __device__ __forceinline__ void release(const float2* own) {
+    __syncwarp();
+    fence_proxy_async();  // the state was written and read by ordinary accesses, the next copy is not one
+    issue(2 * i - 1 + kHalves, (int)((reinterpret_cast<const uint8_t*>(own) - ring) / kHalf));
+  }
+  // Given up: let the copies that were started land (again for a bounded time) before leaving.
+  __device__ __forceinline__ void drain() {
+    for (int h = landed_n; !ok && h < issued; ++h) mbar_wait(full + h % kHalves, (uint32_t)(h / kHalves) & 1u);
+  }
+};
+
+// A head's join of the pieces of a CTA's warps w0 .. w1 (those that have steps), for the whole warp that
+// calls it: weights in every lane group of kNW, output in o (channel pairs lane and lane + 32).  lo: where
+// warp w's part begins; from: where the unit's begins.
+struct Pieces {
+  const float2* at[kNW][2];  // a warp's first piece, and its other one: in its ring or the workspace
+  float m[kNW][2][kMaxG], l[kNW][2][kMaxG], M[kNW][2][kMaxG];
+  __device__ __forceinline__ void put(int warp, int slot, int lane, const float2* where, const State& st) {
+    if (lane < 4) {  // row g = 0 of the layout: heads 2t, 2t + 1
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        m[warp][slot][2 * lane + x] = st.m[x];
+        l[warp][slot][2 * lane + x] = st.l[x];
+        M[warp][slot][2 * lane + x] = st.M[x];
+      }
+    }
+    if (lane == 0) at[warp][slot] = where;
+  }
+  // has, slot: of warp lane % kNW; slot_of(w): the same slot, for any w
+  template <class SLOT>
+  __device__ __forceinline__ float join_head(int h, int lane, bool has, SLOT slot_of, float2 (&o)[2]) const {
+    const int wl = lane & (kNW - 1), slot = slot_of(wl);
+    const Joined j = join(has, has ? m[wl][slot][h] : -INFINITY, has ? l[wl][slot][h] : 0.f,
+                          has ? M[wl][slot][h] : -INFINITY);
+    float2 p[kNW][2];
+    float f[kNW];
+#pragma unroll
+    for (int w = 0; w < kNW; ++w) {
+      f[w] = __shfl_sync(0xffffffffu, j.f, w);
+      p[w][0] = p[w][1] = make_float2(0.f, 0.f);
+      if (f[w] != 0.f) {
+        const float2* src = at[w][slot_of(w)];
+        p[w][0] = src[state_at(h, lane >> 3, lane & 7)];
+        p[w][1] = src[state_at(h, (lane + 32) >> 3, lane & 7)];
+      }
+    }
+    o[0] = o[1] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kNW; ++w)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        o[x].x += f[w] * p[w][x].x;
+        o[x].y += f[w] * p[w][x].y;
+      }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      o[x].x *= j.pow;
+      o[x].y *= j.pow;
+    }
+    return j.lse;
+  }
+};
+
+// Weighted sum of np <= kPieces finished parts (their own lse, normalised output): lane e % kPieces
+// holds lse of part e; read(e, x) loads channel pair lane + 32 x of part e.  Added to (m, L, o).
+template <class READ>
+__device__ __forceinline__ void add_parts(float lse, int np, int lane, READ read, float& m, float& L, float2 (&o)[2]) {
+  float2 p[kPieces][2];
+#pragma unroll
+  for (int e = 0; e < kPieces; ++e)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) p[e][x] = e < np ? read(e, x) : make_float2(0.f, 0.f);
+  float n = fmaxf(m, lse);
+#pragma unroll
+  for (int x = kPieces / 2; x > 0; x >>= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, x));
+  const float base = n == -INFINITY ? 0.f : n;
+  const float keep = expf(m - base), wt = expf(lse - base);
+  float sum = wt;
+#pragma unroll
+  for (int x = kPieces / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  L = L * keep + sum;
+  m = n;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    o[x].x *= keep;
+    o[x].y *= keep;
+  }
+#pragma unroll
+  for (int e = 0; e < kPieces; ++e) {
+    const float w = __shfl_sync(0xffffffffu, wt, e);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      o[x].x += w * p[e][x].x;
+      o[x].y += w * p[e][x].y;
+    }
+  }
+}
+__device__ __forceinline__ void write_parts(const Attn8Args& a, int u, int h, int lane, float m, float L, float2 (&o)[2],
+                                            const CpuPart8& cpu) {
+  const float r = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    o[x].x *= r;
+    o[x].y *= r;
+  }
+  write_head(a, u, h, lane, L == 0.f ? -INFINITY : m + logf(L), o, cpu);
+}
+
+struct FlatMap {  // steps of all units in a row
+  const int* prefix;
+  int units;
+  __device__ __forceinline__ void operator()(int x, int& u, int& step) const {
+    u = owner_of(prefix, units, x);
+    step = x - prefix[u];
+  }
+};
+struct UnitMap {  // steps of one unit
+  int unit;
+  __device__ __forceinline__ void operator()(int x, int& u, int& step) const {
+    u = unit;
+    step = x;
+  }
+};
+
 template <int P, int F>
 __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __grid_constant__ CUtensorMap tmK,
                                                                           const __grid_constant__ CUtensorMap tmV,
@@ -464,11 +785,9 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __gr
   uint8_t* sm8 = smem_raw8 + ((1024u - (smem_u32(smem_raw8) & 1023u)) & 1023u);
   __shared__ uint64_t full[kNW][kHalves];  // a half has landed
   __shared__ int partial[kNW], longest[kNW];
-  __shared__ const float2* state_ptr[kNW][2];  // a warp's pieces: in its ring or the workspace
-  __shared__ float pm[kNW][2][kMaxG], pl[kNW][2][kMaxG], pM[kNW][2][kMaxG];  // m, l, M of a warp's pieces
+  __shared__ Pieces pieces;
   int* prefix = reinterpret_cast<int*>(sm8 + kRingBytes8 + kTileBytes);  // [units + 1] steps before a unit
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, t = lane & 3;
   if (tid < kNW * kHalves) mbar_init(&full[0][0] + tid, 1);
   if (tid < kNW * kHalves) fence_mbar_init();
   if (tid == 64) {
@@ -537,191 +856,20 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __gr
   auto part = [&](int w) { return start + (int)(((int64_t)len * w) >> 3); };
   static_assert(kNW == 8, "parts are eighths");
   const int wlo = part(warp), whi = part(warp + 1), n_mine = whi - wlo;
-  uint8_t* ring = sm8 + warp * (kHalves * kHalf);
-  const LaneOffsets off = lane_offsets(lane);
-  Tile* tiles = reinterpret_cast<Tile*>(sm8 + kRingBytes8) + warp * (4 * kBatch);  // two batches
-
-  // Tile 2 kBatch b + lane of this warp, resolved in three dependent reads that lie apart: the
-  // list entry, the page-table slot, the scales.
-  int ru = 0, rj = -1, rlen = 0, rslot = -1, rrow = 0, rnt = 0;
-  float rks = 0.f, rvs = 0.f;
-  auto resolve_entry = [&](int batch) {
-    const int i = batch * kBatch + (lane >> 1), y = lane & 1;
-    rj = -1;
-    rlen = 0;
-    rrow = P == 16 ? 0 : P == 32 ? 16 * y : 16 * y;  // first token of the tile in its page
-    if (i < n_mine) {
-      const int x = wlo + i;
-      ru = owner_of(prefix, a.units, x);
-      const int step = x - prefix[ru];
-      const int entry = P == 16 ? 2 * step + y : P == 32 ? step : step >> 1;
-      if (P == 64) rrow += 32 * (step & 1);
-      if (P != 16 || entry < min(max(a.res_count[ru], 0), a.k)) {
-        rj = a.res_list[(int64_t)ru * a.k + entry];
-        rlen = a.seq_len[ru / a.Hkv];
-        if (rj < 0 || rj >= a.nblk_cap) rj = -2;
-      }
-    }
-  };
-  auto resolve_slot = [&]() {
-    rslot = rj >= 0 ? a.page_table[(int64_t)ru * a.nblk_cap + rj] : -1;
-  };
-  auto resolve_tile = [&]() {
-    const int nv = rj >= 0 ? min(P, rlen - rj * P) : 0;
-    const bool ok = nv > 0 && rslot >= 0 && rslot < a.n_slots;
-    if (!ok && rj != -1) report(a.status, SCOUT_DEV_BAD_INDEX);
-    rnt = ok ? min(max(nv - rrow, 0), 16) : 0;
-    rrow = ok ? rslot * P + rrow : 0;
-    rks = ok ? __ldg(a.K_scale + rslot) : 0.f;
-    rvs = ok ? __ldg(a.V_scale + rslot) : 0.f;
-  };
-  auto tile_of = [&](int i, int y) -> Tile* { return tiles + ((i / kBatch) & 1) * (2 * kBatch) + 2 * (i % kBatch) + y; };
-
-  // Half h of this warp: K (even) or V (odd) of its step h / 2, into half `at` = h % 3 of the ring.
-  // One lane; every lane has read what was there.  The box starts at a whole row (x = 0).
-  int issued = 0, landed_n = 0;  // halves
-  bool ok = true;  // false once a bounded wait ran out: nothing more is issued or computed
-  auto issue = [&](int h, int at) {
-    const int i = h >> 1;
-    if (i >= n_mine || !ok) return;
-    issued = h + 1;
-    if (lane != 0) return;
-    uint64_t* bar = &full[warp][at];
-    uint8_t* dst = ring + at * kHalf;
-    const CUtensorMap* map = h & 1 ? &tmV : &tmK;
-    const int2 w0 = *reinterpret_cast<const int2*>(tile_of(i, 0));
-    if (P != 16) {
-      if (w0.y > 0) {
-        mbar_arrive_tx(bar, kHalf);
-        tma_load_2d(dst, map, 0, w0.x, bar);
-      } else {
-        mbar_arrive(bar);
-      }
-      return;
-    }
-    const int2 w1 = *reinterpret_cast<const int2*>(tile_of(i, 1));
-    const uint32_t bytes = (w0.y > 0 ? 2048u : 0u) + (w1.y > 0 ? 2048u : 0u);
-    if (bytes == 0u) {
-      mbar_arrive(bar);
-      return;
-    }
-    mbar_arrive_tx(bar, bytes);
-    if (w0.y > 0) tma_load_2d(dst, map, 0, w0.x, bar);
-    if (w1.y > 0) tma_load_2d(dst + 2048, map, 0, w1.x, bar);
-  };
-  auto landed = [&](int at, uint32_t phase) {
-    if (ok && !mbar_wait(&full[warp][at], phase)) {
-      if (lane == 0) report(a.status, SCOUT_DEV_TIMEOUT);
-      ok = false;
-    }
-    ok = __all_sync(0xffffffffu, ok);
-    landed_n += ok;
-  };
-  resolve_entry(0);
-  resolve_slot();
-  resolve_tile();
-  *reinterpret_cast<int2*>(&tiles[lane].row) = make_int2(rrow, rnt);
-  __syncwarp();
-  for (int h = 0; h < kHalves; ++h) issue(h, h);
-  *reinterpret_cast<float2*>(&tiles[lane].ks) = make_float2(rks, rvs);
-  __syncwarp();
-
+  const FlatMap map{prefix, a.units};
+  WarpStream<P, F, FlatMap> ws(a, &tmK, &tmV, sm8, &full[0][0], map, warp, lane, wlo, n_mine);
+  ws.begin();
   int u = n_mine > 0 ? owner_of(prefix, a.units, wlo) : 0;
-  int i = 0, at = 0;   // this warp's next step, and the ring half of its K
-  uint32_t phase = 0;  // of that half's barrier
   for (int pos = wlo; pos < whi;) {
     while (prefix[u + 1] <= pos) ++u;  // the next unit with steps
-    const int hi = min(whi, prefix[u + 1]), i_end = hi - wlo;
+    const int hi = min(whi, prefix[u + 1]);
     uint32_t qb[8][2];
     float qf[2];
     load_q8(a, u, lane, qb, qf);
     State st;
-    st.m[0] = st.m[1] = st.M[0] = st.M[1] = -INFINITY;
-    st.l[0] = st.l[1] = 0.f;
-#pragma unroll
-    for (int md = 0; md < 8; ++md) st.o[md][0] = st.o[md][1] = st.o[md][2] = st.o[md][3] = 0.f;
-    int was = 0;  // ring half of the last V read
-    while (true) {
-      const int ib = i % kBatch;  // the next batch is resolved while this one runs
-      if ((i / kBatch + 1) * kBatch < n_mine) {
-        if (ib == 0) resolve_entry(i / kBatch + 1);
-        if (ib == 4) resolve_slot();
-        if (ib == 8) resolve_tile();
-        if (ib == 12) {
-          tiles[(((i / kBatch) + 1) & 1) * (2 * kBatch) + lane] = Tile{rrow, rnt, rks, rvs};
-          __syncwarp();
-        }
-      }
-      const Tile t0 = *tile_of(i, 0), t1 = *tile_of(i, 1);
-      const float kf[2][2] = {{t0.ks * qf[0], t0.ks * qf[1]}, {t1.ks * qf[0], t1.ks * qf[1]}};
-      float s[2][4];
-      const bool any = t0.nt + t1.nt > 0;
-      landed(at, phase);
-      if (any && ok) {
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          uint4 k[4];
-          read_pieces(ring + at * kHalf + y * 2048, off.k, k);
-          tile_scores<F>(k, qb, s[y]);
-        }
-      }
-      // the reads above have returned: the products that use them have been issued
-      __syncwarp();
-      issue(2 * i + kHalves, at);
-      if (++at == kHalves) {
-        at = 0;
-        phase ^= 1u;
-      }
-      if (any && ok) {
-        if (!(P != 16 && t1.nt == 16 && step_weights_page(s, kf[0], t0.vs, st)))
-          step_weights_any(s, kf, t0.nt, t1.nt, t0.vs, t1.vs, g, st);
-      }
-      landed(at, phase);
-      if (any && ok) {
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          uint4 v[4];
-          const int nt = y ? t1.nt : t0.nt;
-          read_pieces(ring + at * kHalf + y * 2048, off.v, v);
-          if (nt < 16) clear_past(v, nt, lane);
-          tile_output<F>(v, s[y], st);
-        }
-      }
-      __syncwarp();  // every lane has read its V
-      was = at;
-      if (++at == kHalves) {
-        at = 0;
-        phase ^= 1u;
-      }
-      if (++i == i_end) break;
-      issue(2 * i - 1 + kHalves, was);
-    }
-    // the segment's state goes into the half that its last V left
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], o);
-      st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], o);
-    }
-    float2* own = reinterpret_cast<float2*>(ring + was * kHalf);
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int h = 2 * t + x;
-#pragma unroll
-      for (int md = 0; md < 8; ++md)
-        if (h < a.G) own[state_at(h, g, md)] = make_float2(st.o[md][x], st.o[md][2 + x]);
-    }
-    const bool whole = pos == prefix[u] && hi == prefix[u + 1];
-    if (!whole && g == 0) {
-      const int slot = pos == wlo ? 0 : 1;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        pm[warp][slot][2 * t + x] = st.m[x];
-        pl[warp][slot][2 * t + x] = st.l[x];
-        pM[warp][slot][2 * t + x] = st.M[x];
-      }
-    }
+    float2* own = ws.run(hi - wlo, qb, qf, st);
     __syncwarp();
-    if (whole) {
+    if (pos == prefix[u] && hi == prefix[u + 1]) {  // whole: finished here
       CpuPart8 next = load_cpu8(a, u, 0, lane);
       for (int h = 0; h < a.G; ++h) {
         const float m0 = __shfl_sync(0xffffffffu, st.m[0], h >> 1), m1 = __shfl_sync(0xffffffffu, st.m[1], h >> 1);
@@ -745,17 +893,12 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __gr
         for (int e = lane; e < a.G * (kD / 4); e += 32) dst[e] = reinterpret_cast<const float4*>(own)[e];
         where = reinterpret_cast<const float2*>(dst);
       }
-      if (lane == 0) state_ptr[warp][pos == wlo ? 0 : 1] = where;
+      pieces.put(warp, pos == wlo ? 0 : 1, lane, where, st);
     }
-    if (hi < whi) {
-      __syncwarp();
-      fence_proxy_async();  // the state was written and read by ordinary accesses, the next copy is not one
-      issue(2 * i - 1 + kHalves, was);
-    }
+    if (hi < whi) ws.release(own);
     pos = hi;
   }
-  // given up: let the copies that were started land (again for a bounded time) before leaving
-  for (int h = landed_n; !ok && h < issued; ++h) mbar_wait(&full[warp][h % kHalves], (uint32_t)(h / kHalves) & 1u);
+  ws.drain();
   release_dependents();
   __syncthreads();
 
@@ -786,42 +929,16 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __gr
       if (phase1 && (prefix[v] < start || prefix[v + 1] > end || w0 == w1)) continue;
       CpuPart8 cpu;
       if (phase1) cpu = load_cpu8(a, v, h, lane);
-      const bool has = wl >= w0 && wl <= w1 && lo_w < part(wl + 1);
-      const int slot = lo_w >= plo ? 0 : 1;
-      const Joined j = join(has, has ? pm[wl][slot][h] : -INFINITY, has ? pl[wl][slot][h] : 0.f,
-                            has ? pM[wl][slot][h] : -INFINITY);
-      float2 p[kNW][2];
-      float f[kNW];
-#pragma unroll
-      for (int w = 0; w < kNW; ++w) {
-        f[w] = __shfl_sync(0xffffffffu, j.f, w);
-        p[w][0] = p[w][1] = make_float2(0.f, 0.f);
-        if (f[w] != 0.f) {
-          const float2* src = state_ptr[w][part(w) >= plo ? 0 : 1];
-          p[w][0] = src[state_at(h, lane >> 3, lane & 7)];
-          p[w][1] = src[state_at(h, (lane + 32) >> 3, lane & 7)];
-        }
-      }
-      float2 o[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int w = 0; w < kNW; ++w)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          o[x].x += f[w] * p[w][x].x;
-          o[x].y += f[w] * p[w][x].y;
-        }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        o[x].x *= j.pow;
-        o[x].y *= j.pow;
-      }
+      float2 o[2];
+      const float lse = pieces.join_head(h, lane, wl >= w0 && wl <= w1 && lo_w < part(wl + 1),
+                                         [&](int w) { return part(w) >= plo ? 0 : 1; }, o);
       if (phase1) {
-        write_head(a, v, h, lane, j.lse, o, cpu);
+        write_head(a, v, h, lane, lse, o, cpu);
       } else {
-        const int64_t mine = piece_of(v, h, c);
-        reinterpret_cast<float2*>(a.slot_O + mine * kD)[lane] = o[0];
-        reinterpret_cast<float2*>(a.slot_O + mine * kD)[lane + 32] = o[1];
-        if (lane == 0) a.slot_lse[mine] = j.lse;
+        const int mine = piece_of(v, h, c);
+        reinterpret_cast<float2*>(a.slot_O + (int64_t)mine * kD)[lane] = o[0];
+        reinterpret_cast<float2*>(a.slot_O + (int64_t)mine * kD)[lane + 32] = o[1];
+        if (lane == 0) a.slot_lse[mine] = lse;
       }
     }
     if (phase1 == 0 && warp < n_cut) {
@@ -843,55 +960,114 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __gr
     __threadfence();
     float m = -INFINITY, L = 0.f;
     float2 o[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
     for (int b0 = c0; b0 <= c1; b0 += kPieces) {  // all loads of a batch together
       const int nb = min(kPieces, c1 - b0 + 1);
       const int e_lane = lane & (kPieces - 1), at_lane = piece_of(v, h, b0 + min(e_lane, nb - 1));
       const float lse = e_lane < nb ? __ldcg(a.slot_lse + at_lane) : -INFINITY;
-      float2 p[kPieces][2];
+      int at_piece[kPieces];
 #pragma unroll
-      for (int e = 0; e < kPieces; ++e) {
-        p[e][0] = p[e][1] = make_float2(0.f, 0.f);
-        const int64_t at_piece = __shfl_sync(0xffffffffu, at_lane, e);
-        if (e < nb) {
-          const float2* src = reinterpret_cast<const float2*>(a.slot_O + at_piece * kD);
-          p[e][0] = __ldcg(src + lane);
-          p[e][1] = __ldcg(src + lane + 32);
-        }
-      }
-      float n = fmaxf(m, lse);
-#pragma unroll
-      for (int x = kPieces / 2; x > 0; x >>= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, x));
-      const float base = n == -INFINITY ? 0.f : n;
-      const float keep = expf(m - base), wt = expf(lse - base);
-      float sum = wt;
-#pragma unroll
-      for (int x = kPieces / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-      L = L * keep + sum;
-      m = n;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        o[x].x *= keep;
-        o[x].y *= keep;
-      }
-#pragma unroll
-      for (int e = 0; e < kPieces; ++e) {
-        const float w = __shfl_sync(0xffffffffu, wt, e);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          o[x].x += w * p[e][x].x;
-          o[x].y += w * p[e][x].y;
-        }
-      }
+      for (int e = 0; e < kPieces; ++e) at_piece[e] = __shfl_sync(0xffffffffu, at_lane, e);
+      add_parts(lse, nb, lane,
+                [&](int e, int x) {
+                  return __ldcg(reinterpret_cast<const float2*>(a.slot_O + (int64_t)at_piece[e] * kD) + lane + 32 * x);
+                },
+                m, L, o);
     }
-    const float r = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      o[x].x *= r;
-      o[x].y *= r;
-    }
-    write_head(a, v, h, lane, L == 0.f ? -INFINITY : m + logf(L), o, cpu);
+    write_parts(a, v, h, lane, m, L, o, cpu);
     if (lane == 0) a.counters[(int64_t)v * kMaxG + h] = 0;  // ready for the next call
   }
+}
+
+// distributed shared memory of a cluster
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t in_rank(uint32_t smem, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Few units with short lists: the CTAs of a cluster take equal parts of one unit and join them through
+// distributed shared memory, which costs one cluster barrier where the even split's pieces take a
+// fence, a count and a read through L2; no prefix over the units is needed either.
+template <int P, int F>
+__global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_cluster_kernel(const __grid_constant__ CUtensorMap tmK,
+                                                                                  const __grid_constant__ CUtensorMap tmV,
+                                                                                  const Attn8Args a, int cs) {
+  extern __shared__ uint8_t smem_raw8[];
+  uint8_t* sm8 = smem_raw8 + ((1024u - (smem_u32(smem_raw8) & 1023u)) & 1023u);
+  __shared__ uint64_t full[kNW][kHalves];
+  __shared__ Pieces pieces;
+  __shared__ __align__(16) float2 part_o[kMaxG][kD / 2];  // this CTA's part, head by head
+  __shared__ float part_lse[kMaxG];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < kNW * kHalves) mbar_init(&full[0][0] + tid, 1);
+  if (tid < kNW * kHalves) fence_mbar_init();
+  if (tid == 64) {
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  wait_prerequisites();
+  const int u = (int)blockIdx.x / cs, rank = (int)cluster_rank();
+  const int n = steps_of<P>(min(max(a.res_count[u], 0), a.k));
+  const int start = (int)((int64_t)n * rank / cs), end = (int)((int64_t)n * (rank + 1) / cs), len = end - start;
+  auto part = [&](int w) { return start + (int)(((int64_t)len * w) >> 3); };
+  const int wlo = part(warp), n_mine = part(warp + 1) - wlo;
+  __syncthreads();  // the barriers are ready
+  const UnitMap map{u};
+  WarpStream<P, F, UnitMap> ws(a, &tmK, &tmV, sm8, &full[0][0], map, warp, lane, wlo, n_mine);
+  ws.begin();
+  if (n_mine > 0) {
+    uint32_t qb[8][2];
+    float qf[2];
+    load_q8(a, u, lane, qb, qf);
+    State st;
+    const float2* own = ws.run(n_mine, qb, qf, st);
+    pieces.put(warp, 0, lane, own, st);
+  }
+  ws.drain();
+  release_dependents();
+  __syncthreads();
+  if (warp < a.G) {  // warp h: head h of this CTA's part
+    const int wl = lane & (kNW - 1);
+    float2 o[2];
+    const float lse = pieces.join_head(warp, lane, part(wl) < part(wl + 1), [](int) { return 0; }, o);
+    part_o[warp][lane] = o[0];
+    part_o[warp][lane + 32] = o[1];
+    if (lane == 0) part_lse[warp] = lse;
+  }
+  // warp w of CTA r finishes head r + cs w
+  const int h = rank + cs * warp;
+  CpuPart8 cpu;
+  if (h < a.G) cpu = load_cpu8(a, u, h, lane);
+  cluster_barrier();
+  if (h < a.G) {
+    float m = -INFINITY, L = 0.f;
+    float2 o[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    const int e_lane = lane & (kPieces - 1);
+    const float lse = e_lane < cs ? ld_cluster(in_rank(smem_u32(&part_lse[h]), (uint32_t)e_lane)) : -INFINITY;
+    add_parts(lse, cs, lane,
+              [&](int e, int x) { return ld_cluster2(in_rank(smem_u32(&part_o[h][lane + 32 * x]), (uint32_t)e)); }, m, L, o);
+    write_parts(a, u, h, lane, m, L, o, cpu);
+  }
+  cluster_barrier();  // no CTA leaves while another reads its part
 }
 
 inline size_t counters8_bytes(int64_t units) { return (size_t)((units * kMaxG * 4 + 255) / 256 * 256); }
@@ -913,27 +1089,44 @@ bool make_rows_map(CUtensorMap* map, const void* pool, int64_t rows, int box_row
 
 template <int P, int F>
 int launch_attn8(const Attn8Args& a, const scout_launch* launch, cudaStream_t stream) {
-  auto kern = attn8_kernel<P, F>;
   CUtensorMap tmK, tmV;
   constexpr int kBox = P == 16 ? 16 : 32;
   if (!make_rows_map(&tmK, a.K_pool, a.n_slots * P, kBox) || !make_rows_map(&tmV, a.V_pool, a.n_slots * P, kBox))
     return SCOUT_ERR_UNSUPPORTED;
-  const size_t smem = 1024 + (size_t)kRingBytes8 + kTileBytes + (size_t)(a.units + 1) * 4;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return SCOUT_ERR_CUDA;
+  const int max_ctas = launch != nullptr ? launch->max_ctas : 0;
+  const int limit = max_ctas > 0 ? max_ctas : sm_count() * kCtasPerSm;
+  // CTAs a unit, for lists as long as they may be: as many as fit (up to 8) and find a step for each warp
+  const int64_t steps = P == 16 ? ((int64_t)a.k + 1) / 2 : P == 32 ? (int64_t)a.k : 2 * (int64_t)a.k;
+  int cs = 1;
+  while (cs < kMaxCluster && (int64_t)a.units * cs * 2 <= limit && steps > cs * kNW) cs *= 2;
+  const bool cluster = cs > 1 && steps <= (int64_t)cs * kNW * kClusterSteps;
+  size_t smem = 1024 + (size_t)kRingBytes8 + kTileBytes;
+  if (!cluster) smem += (size_t)(a.units + 1) * 4;
   // two CTAs an SM as long as the prefix over the units leaves room for both
   const int per_sm = 2 * (smem + kStaticSmem) <= kSmSmem ? kCtasPerSm : 1;
-  const int max_ctas = launch != nullptr ? launch->max_ctas : 0;
-  const int grid = min(kMaxGrid8, max_ctas > 0 ? max_ctas : sm_count() * per_sm);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)(cluster ? a.units * cs : min(kMaxGrid8, max_ctas > 0 ? max_ctas : sm_count() * per_sm)));
   cfg.blockDim = dim3(kThreads8);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[3];
   cfg.attrs = attr;
   cfg.numAttrs = early_start_attrs(launch, attr, 0);
-  if (cudaLaunchKernelEx(&cfg, kern, tmK, tmV, a) != cudaSuccess) {
+  cudaError_t err;
+  if (cluster) {
+    auto kern = attn8_cluster_kernel<P, F>;
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = (unsigned)cs;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err == cudaSuccess) err = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, a, cs);
+  } else {
+    auto kern = attn8_kernel<P, F>;
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err == cudaSuccess) err = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, a);
+  }
+  if (err != cudaSuccess) {
     cudaGetLastError();
     return SCOUT_ERR_CUDA;
   }

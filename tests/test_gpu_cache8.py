@@ -432,6 +432,17 @@ def test_attn8_splits(scales, max_ctas):
     Attn(11, B=3, Hkv=3, G=5, P=32, top=3000, k=70, scales=scales).run(max_ctas=max_ctas)
 
 
+@pytest.mark.parametrize("B,Hkv,k,P", [(1, 1, 9, 32), (1, 3, 40, 16), (2, 5, 33, 32), (7, 4, 100, 16), (9, 8, 17, 64),
+                                       (16, 8, 64, 32), (19, 8, 12, 64), (1, 2, 256, 32), (1, 2, 257, 32)])
+@pytest.mark.parametrize("G", [1, 8])
+def test_attn8_few_units_with_short_lists(B, Hkv, k, P, G):
+    # units shared by several CTAs of a cluster: lists from empty to k, parts without a step
+    a = Attn(B * 100 + k, B=B, Hkv=Hkv, G=G, P=P, top=k * P + 5, k=k, scales="wild" if G == 1 else "mixed")
+    a.counts[0, 0] = 0
+    a.run()
+    a.run(max_ctas=2 * B * Hkv + 1)
+
+
 def test_attn8_long_list_over_the_whole_grid():
     Attn(12, B=1, Hkv=2, G=8, P=16, lens=[20011], k=1300).run()
 
