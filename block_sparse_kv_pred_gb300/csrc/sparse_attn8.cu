@@ -23,20 +23,26 @@
 // free, so a lane takes 16-byte pieces of rows and uses every byte where it lies: no shared memory
 // transposes.  A step is 32 tokens: two 16-token tiles, each inside one page.
 //
-// Split.  The steps of all units are dealt as contiguous ranges to CTAs, and a CTA's to its warps.
-// A warp finishes the units inside its part alone; units that a warp boundary cuts are joined in
-// shared memory when the CTA's warps are done, and units that a CTA boundary cuts by the last CTA to
-// count itself.  While it streams, a warp waits for nothing but its own copies.
+// Split.  A warp gets a contiguous part of the steps of all units, and while it streams it waits for
+// nothing but its own copies.  It finishes the units inside its part alone; units that a boundary
+// between warps cuts are joined when the warps are done: in shared memory within a CTA, in
+// distributed shared memory within a cluster, and across CTAs through the workspace, by the last CTA
+// to count itself.  Which of these occurs is a matter of the split:
+//   few units, short lists    the CTAs of a cluster take equal parts of one unit;
+//   many units                a cluster takes whole units, its steps dealt to its 64 warps;
+//   units nearly as many as CTAs, or a long one among many: whole units, or the even split, by CTA.
 //
 // What bounds it.  mma.sync rather than tcgen05: five to eight query heads fill an eighth of a tcgen05
 // tile, and its operands would need q and the weights in 8 bits or K and V widened in shared
 // memory.  The products take 52 ns of an SM's time a step (48 at 1.08 ns), the conversions about
 // as much; a step's 8 KB take 182 ns of the SM's share of DRAM, so a long launch is bound by DRAM:
-// GB300, 4 x 128K tokens dense, 174 us for 1.08 GB (6.2 TB/s, 0.91 of the measured copy bandwidth;
+// GB300, 4 x 128K tokens dense, 176 us for 1.08 GB (6.1 TB/s, 0.90 of the measured copy bandwidth;
 // the SMs' shares of it differ, and the first are done at 0.75 of the time).  40 sequences of 2,048
-// listed tokens, 8 x 5 heads: 41 us for 152 MB, of which the first 4 go by before the copies start
-// (counts, list, page table), 23 stream at 6.5 TB/s, and the rest is the slowest CTA and the end
-// phase (join, fence, count, merge, each a round trip).  One 4K sequence: 9.1 us, all latency.
+// listed tokens, 8 x 5 heads: 38.6 us for 152 MB, of which the first 4 go by before the copies start
+// (counts, list, page table), 24 stream at 6.3 TB/s, and the rest is the slowest warp and the end
+// phase (barrier, join, barrier).  One 4K sequence: 6.9 us, all latency.
+#include <atomic>
+
 #include "fp8.cuh"
 
 namespace scout {
@@ -46,17 +52,22 @@ constexpr int kNW = 8;                 // warps of a CTA
 constexpr int kThreads8 = kNW * 32;
 constexpr int kCtasPerSm = 2;
 // A CTA takes whole units when its warps then have at most this many steps more than with an even
-// split, which pays for the even split's merge of pieces across CTAs.  Measured on GB300, whole | even,
-// lists of 58 blocks of 32 tokens, 8 KV heads: 1 sequence (7 steps more) 18.3 | 11.3 us, 16 (4 more)
-// 25.7 | 22.2 us, 32 (1 more) 29.3 | 31.6 us.
+// split, which pays for the even split's joins.  Measured on GB300, whole | even, lists of 58 blocks of
+// 32 tokens, 8 KV heads: 1 sequence (7 steps more) 18.3 | 11.3 us, 16 (4 more) 25.7 | 22.2 us, 32 (1
+// more) 29.3 | 31.6 us.
 constexpr int kWholeSteps = 2;
 constexpr int kPieces = 8;             // of a cut unit, merged at a time
-#ifndef SCOUT_CS
-#define SCOUT_CS 4
-#define SCOUT_MC 8
-#endif
-constexpr int kMaxCluster = SCOUT_MC;
-constexpr int kClusterSteps = SCOUT_CS;
+// Clusters.  With few units and lists that give each warp at most kClusterSteps steps, the CTAs of a
+// cluster share one unit.  Measured on GB300, even split | cluster, lists of 58 blocks of 32 tokens, 8
+// KV heads x 4: 1 sequence 11.9 | 7.2 us, 8 17.2 | 11.4, 16 23.3 | 18.4; 4 of 512 blocks (8 steps a
+// warp) 32.3 | 27.8, 1 of 1,024 (16 steps) 27.1 | 33.4.
+constexpr int kMaxCluster = 8;
+constexpr int kClusterSteps = 8;
+// With at least kSnapUnits units for each cluster of kSnap CTAs that the device holds, a cluster takes
+// whole units.  Even split | clusters: 40 sequences of 8 x 5 heads, 58 blocks, 41.4 | 38.6 us; with
+// ragged lists 47.1 | 39.6; 24 sequences 31.3 | 29.5; 64 of 29 blocks 34.5 | 34.0.
+constexpr int kSnap = 8;
+constexpr int kSnapUnits = 4;
 constexpr int kMaxUnits8 = 4096;
 constexpr int kMaxGrid8 = 512;
 constexpr int64_t kMaxSteps = (int64_t)1 << 29;
@@ -442,23 +453,56 @@ __device__ __forceinline__ Joined join_at(bool has, float m, float l, float M, f
   j.lse = none ? -INFINITY : (top_m + __log2f(L)) * kLn2;
   return j;
 }
-// lanes 8 i + w, w < 8: piece w
+// lanes LANES i + w, w < LANES: piece w
+template <int LANES = kNW>
 __device__ __forceinline__ Joined join(bool has, float m, float l, float M) {
   float top_m = m, top_M = M;
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) {
+  for (int o = LANES / 2; o > 0; o >>= 1) {
     top_m = fmaxf(top_m, __shfl_xor_sync(0xffffffffu, top_m, o));
     top_M = fmaxf(top_M, __shfl_xor_sync(0xffffffffu, top_M, o));
   }
   const float base = top_m == -INFINITY ? 0.f : top_m;
   float L = has ? l * fast_exp2(m - base) : 0.f;
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  for (int o = LANES / 2; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   return join_at(has, m, l, M, top_m, top_M, L, base);
 }
 __device__ __forceinline__ Joined join_one(float m, float l, float M) {
   const float base = m == -INFINITY ? 0.f : m;
   return join_at(true, m, l, M, m, M, l * fast_exp2(m - base), base);
+}
+
+// distributed shared memory of a cluster
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t in_rank(uint32_t smem, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+// the same place as p (shared memory of this CTA) in another CTA of the cluster, as a generic address
+template <class T>
+__device__ __forceinline__ const T* in_rank_generic(const T* p, uint32_t rank) {
+  uint64_t r;
+  asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+  return reinterpret_cast<const T*>(r);
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // One warp's steps, streamed through its ring.  MAP: map(x, unit, step) gives the unit of step x of
@@ -760,6 +804,88 @@ __device__ __forceinline__ void write_parts(const Attn8Args& a, int u, int h, in
   write_head(a, u, h, lane, L == 0.f ? -INFINITY : m + logf(L), o, cpu);
 }
 
+// The end of a cluster that has taken the units of steps [lo, lo + len), dealt to its 64 warps: the
+// (unit, head) pairs that boundaries between warps cut are dealt to all of them again, whose steps
+// they ever were.  The pieces lie in the warps' rings, or in the workspace.
+__device__ __forceinline__ void join_in_cluster(const Attn8Args& a, const int* prefix, const Pieces& pieces, int lo,
+                                                int len, int c, int rank, int warp, int lane) {
+  auto part = [&](int w) { return lo + (int)(((int64_t)len * w) >> 6); };  // of the cluster's warp w
+  auto last_part = [&](int x) {  // the last warp whose part begins at or before step x
+    return __popc(__ballot_sync(0xffffffffu, part(lane) <= x)) + __popc(__ballot_sync(0xffffffffu, part(lane + 32) <= x)) - 1;
+  };
+  // lane, and 32 + lane: the unit at the boundary before warp w + 1, if it is cut there for the first time
+  int unit[2];
+  uint32_t cut[2];
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const int w = lane + 32 * y + 1, x = part(w);
+    unit[y] = owner_of(prefix, a.units, min(x, lo + len - 1));
+    cut[y] = __ballot_sync(0xffffffffu, w < 64 && x < lo + len && prefix[unit[y]] < x && part(w - 1) <= prefix[unit[y]]);
+  }
+  cluster_barrier();
+  const int n0 = __popc(cut[0]), tasks = (n0 + __popc(cut[1])) * a.G;
+#pragma unroll 1
+  for (int task = warp * kSnap + rank; task < tasks; task += kSnap * kNW) {
+    const int k = task / a.G, h = task - k * a.G;  // the k-th cut unit
+    const bool low = k < n0;
+    const uint32_t in = low ? cut[0] : cut[1];
+    const int nth = low ? k : k - n0;
+    const int from = __ffs(__ballot_sync(0xffffffffu, ((in >> lane) & 1u) != 0u && __popc(in & ((1u << lane) - 1u)) == nth)) - 1;
+    const int v = __shfl_sync(0xffffffffu, low ? unit[0] : unit[1], from);
+    const CpuPart8 cpu = load_cpu8(a, v, h, lane);
+    // the cluster's warps that have steps of it; lane p: piece p, of warp g0 + p
+    const int g0 = last_part(prefix[v]), np = last_part(prefix[v + 1] - 1) - g0 + 1;
+    const int gw = g0 + min(lane, np - 1), lo_w = part(gw), hi_w = part(gw + 1), w = gw % kNW;
+    const bool has = lane < np && lo_w < hi_w;
+    const int slot = lo_w >= prefix[v] ? 0 : 1;
+    const Pieces* there = in_rank_generic(&pieces, (uint32_t)(gw / kNW));
+    float m = -INFINITY, l = 0.f, M = -INFINITY;
+    const float2* at = nullptr;
+    if (has) {
+      m = there->m[w][slot][h];
+      l = there->l[w][slot][h];
+      M = there->M[w][slot][h];
+      if (min(prefix[v + 1], hi_w) == hi_w)  // the warp's last piece: in its ring
+        at = in_rank_generic(there->at[w][slot], (uint32_t)(gw / kNW));
+      else
+        at = reinterpret_cast<const float2*>(a.piece_O + ((int64_t)(c - rank) * kNW + gw) * (kMaxG * kD));
+    }
+    const Joined j = join<32>(has, m, l, M);
+    float2 o[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+    for (int e0 = 0; e0 < np; e0 += kPieces) {
+      float2 p[kPieces][2];
+      float f[kPieces];
+#pragma unroll
+      for (int e = 0; e < kPieces; ++e) {
+        f[e] = __shfl_sync(0xffffffffu, j.f, (e0 + e) & 31);
+        const float2* src = reinterpret_cast<const float2*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(at), (e0 + e) & 31));
+        p[e][0] = p[e][1] = make_float2(0.f, 0.f);
+        if (e0 + e >= np) f[e] = 0.f;
+        if (f[e] != 0.f) {
+          p[e][0] = src[state_at(h, lane >> 3, lane & 7)];
+          p[e][1] = src[state_at(h, (lane + 32) >> 3, lane & 7)];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kPieces; ++e)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          o[x].x += f[e] * p[e][x].x;
+          o[x].y += f[e] * p[e][x].y;
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      o[x].x *= j.pow;
+      o[x].y *= j.pow;
+    }
+    write_head(a, v, h, lane, j.lse, o, cpu);
+  }
+  cluster_barrier();  // no CTA leaves while another reads its pieces
+}
+
 struct FlatMap {  // steps of all units in a row
   const int* prefix;
   int units;
@@ -776,7 +902,11 @@ struct UnitMap {  // steps of one unit
   }
 };
 
-template <int P, int F>
+// CL: launched in clusters of kSnap CTAs.  As long as no unit is long against a cluster's share, a
+// cluster then takes whole units (its share's ends moved to the nearest unit's), deals their steps to
+// its warps, and joins them through distributed shared memory; nothing is left to be merged
+// through the workspace.
+template <int P, int F, bool CL>
 __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __grid_constant__ CUtensorMap tmK,
                                                                           const __grid_constant__ CUtensorMap tmV,
                                                                           const Attn8Args a) {
@@ -844,17 +974,33 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __gr
   const int even = min((int)gridDim.x, (N + kNW - 1) / kNW);
   const bool by_unit = a.units <= (int)gridDim.x &&
                        (most + kNW - 1) / kNW <= (N + even * kNW - 1) / max(even * kNW, 1) + kWholeSteps;
-  const int Gp = by_unit ? a.units : even;
+  const int clusters = (int)gridDim.x / kSnap;
+  // a unit then lies in at most 32 of the cluster's warps
+  const bool snap = CL && !by_unit && most <= N / clusters / kSnapUnits;
+  const int Gp = by_unit ? a.units : snap ? clusters : even;
   const int c = blockIdx.x;
-  if (c >= Gp) return;
+  if (!snap && c >= Gp) return;
   const Ranges ranges(max(N, 1), Gp);
-  const int start = by_unit ? prefix[c] : ranges.first(c), end = by_unit ? prefix[c + 1] : ranges.first(c + 1);
-  if (start == end) return;
-  // A warp's steps are a contiguous part of its CTA's: units that lie inside it are finished by the
-  // warp alone, and what a boundary cuts is joined once, when all warps are done.
-  const int len = end - start;
-  auto part = [&](int w) { return start + (int)(((int64_t)len * w) >> 3); };
-  static_assert(kNW == 8, "parts are eighths");
+  const int rank = CL ? (int)cluster_rank() : 0;
+  int lo, len;
+  if (snap) {  // lanes 0 and 1: where this cluster's units begin, and the next one's
+    const int k = c / kSnap + (lane & 1), x = min(ranges.first(k), N - 1), v = owner_of(prefix, a.units, x);
+    int at = k >= Gp ? N : x - prefix[v] <= prefix[v + 1] - x ? prefix[v] : prefix[v + 1];
+    if (k == 0) at = 0;
+    lo = __shfl_sync(0xffffffffu, at, 0);
+    len = __shfl_sync(0xffffffffu, at, 1) - lo;
+  } else {
+    lo = by_unit ? prefix[c] : ranges.first(c);
+    len = (by_unit ? prefix[c + 1] : ranges.first(c + 1)) - lo;
+  }
+  if (len == 0) return;  // (all CTAs of the cluster alike)
+  // steps lo .. lo + len - 1 are dealt evenly to 2^parts_log warps, of which this CTA's first is number w_first
+  const int parts_log = snap ? 6 : 3, w_first = snap ? rank * kNW : 0;
+  static_assert(kNW == 8 && kSnap * kNW == 64, "parts are eighths or 64ths");
+  // A warp's steps are a contiguous part: units that lie inside it are finished by the warp alone,
+  // and what a boundary cuts is joined once, when all warps are done.
+  auto part = [&](int w) { return lo + (int)(((int64_t)len * (w_first + w)) >> parts_log); };
+  const int start = part(0), end = part(kNW);
   const int wlo = part(warp), whi = part(warp + 1), n_mine = whi - wlo;
   const FlatMap map{prefix, a.units};
   WarpStream<P, F, FlatMap> ws(a, &tmK, &tmV, sm8, &full[0][0], map, warp, lane, wlo, n_mine);
@@ -900,6 +1046,10 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __gr
   }
   ws.drain();
   release_dependents();
+  if (CL && snap) {
+    join_in_cluster(a, prefix, pieces, lo, len, c, rank, warp, lane);
+    return;
+  }
   __syncthreads();
 
   // What boundaries cut, a (unit, head) a warp.  First the units cut by the CTA's ends (at most two):
@@ -979,31 +1129,6 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_kernel(const __gr
   }
 }
 
-// distributed shared memory of a cluster
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t in_rank(uint32_t smem, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // Few units with short lists: the CTAs of a cluster take equal parts of one unit and join them through
 // distributed shared memory, which costs one cluster barrier where the even split's pieces take a
 // fence, a count and a read through L2; no prefix over the units is needed either.
@@ -1071,8 +1196,9 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_cluster_kernel(co
 }
 
 inline size_t counters8_bytes(int64_t units) { return (size_t)((units * kMaxG * 4 + 255) / 256 * 256); }
-constexpr size_t kSmSmem = 228 * 1024;       // shared memory of an SM
-constexpr size_t kStaticSmem = 1024 + 2048;  // of a CTA besides the dynamic part: the system's and the arrays'
+// shared memory of the largest launch: two such CTAs fit an SM
+constexpr size_t kMostSmem = 1024 + (size_t)kRingBytes8 + kTileBytes + (size_t)(kMaxUnits8 + 1) * 4;
+static_assert(kCtasPerSm * (kMostSmem + 8 * 1024) <= 228 * 1024, "two CTAs an SM");
 constexpr size_t kSlotLse8 = (size_t)kMaxGrid8 * 2 * kMaxG * sizeof(float);
 constexpr size_t kSlotO8 = (size_t)kMaxGrid8 * 2 * kMaxG * kD * sizeof(float);
 constexpr size_t kPieceO8 = (size_t)kMaxGrid8 * kNW * kMaxG * kD * sizeof(float);
@@ -1085,6 +1211,37 @@ bool make_rows_map(CUtensorMap* map, const void* pool, int64_t rows, int box_row
   const cuuint32_t estr[2] = {1, 1};
   return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(pool), dims, strides, box, estr,
                       CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+}
+
+// Clusters of kSnap CTAs that the current device holds at once (0 if it cannot say): a property of the
+// device and the kernel, asked once for each.
+template <int P, int F>
+int snap_clusters() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];  // 0: not asked yet, n + 1: n
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+  const int k = known[dev].load(std::memory_order_relaxed);
+  if (k > 0) return k - 1;
+  auto kern = attn8_kernel<P, F, true>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kSnap);
+  cfg.blockDim = dim3(kThreads8);
+  cfg.dynamicSmemBytes = kMostSmem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kSnap;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess)
+    n = 0;
+  cudaGetLastError();
+  n = min(n, kMaxGrid8 / kSnap);
+  known[dev].store(n + 1, std::memory_order_relaxed);
+  return n;
 }
 
 template <int P, int F>
@@ -1100,33 +1257,44 @@ int launch_attn8(const Attn8Args& a, const scout_launch* launch, cudaStream_t st
   int cs = 1;
   while (cs < kMaxCluster && (int64_t)a.units * cs * 2 <= limit && steps > cs * kNW) cs *= 2;
   const bool cluster = cs > 1 && steps <= (int64_t)cs * kNW * kClusterSteps;
-  size_t smem = 1024 + (size_t)kRingBytes8 + kTileBytes;
-  if (!cluster) smem += (size_t)(a.units + 1) * 4;
-  // two CTAs an SM as long as the prefix over the units leaves room for both
-  const int per_sm = 2 * (smem + kStaticSmem) <= kSmSmem ? kCtasPerSm : 1;
+  const size_t smem = 1024 + (size_t)kRingBytes8 + kTileBytes + (cluster ? 0 : (size_t)(a.units + 1) * 4);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(cluster ? a.units * cs : min(kMaxGrid8, max_ctas > 0 ? max_ctas : sm_count() * per_sm)));
   cfg.blockDim = dim3(kThreads8);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[3];
   cfg.attrs = attr;
   cfg.numAttrs = early_start_attrs(launch, attr, 0);
-  cudaError_t err;
-  if (cluster) {
-    auto kern = attn8_cluster_kernel<P, F>;
+  auto clusters_of = [&](int n) {
     attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    attr[cfg.numAttrs].val.clusterDim.x = (unsigned)cs;
+    attr[cfg.numAttrs].val.clusterDim.x = (unsigned)n;
     attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
     ++cfg.numAttrs;
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err == cudaSuccess) err = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, a, cs);
+  };
+  auto ready = [&](const void* kern) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
+  };
+  bool sent;
+  if (cluster) {
+    auto kern = attn8_cluster_kernel<P, F>;
+    cfg.gridDim = dim3((unsigned)(a.units * cs));
+    clusters_of(cs);
+    sent = ready(reinterpret_cast<const void*>(kern)) && cudaLaunchKernelEx(&cfg, kern, tmK, tmV, a, cs) == cudaSuccess;
   } else {
-    auto kern = attn8_kernel<P, F>;
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err == cudaSuccess) err = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, a);
+    const int resident = snap_clusters<P, F>();
+    const int clusters = max_ctas > 0 ? (max_ctas / kSnap < resident ? max_ctas / kSnap : resident) : resident;
+    if (clusters > 0 && a.units >= kSnapUnits * clusters) {
+      auto kern = attn8_kernel<P, F, true>;
+      cfg.gridDim = dim3((unsigned)(clusters * kSnap));
+      clusters_of(kSnap);
+      sent = ready(reinterpret_cast<const void*>(kern)) && cudaLaunchKernelEx(&cfg, kern, tmK, tmV, a) == cudaSuccess;
+    } else {
+      auto kern = attn8_kernel<P, F, false>;
+      cfg.gridDim = dim3((unsigned)min(kMaxGrid8, limit));
+      sent = ready(reinterpret_cast<const void*>(kern)) && cudaLaunchKernelEx(&cfg, kern, tmK, tmV, a) == cudaSuccess;
+    }
   }
-  if (err != cudaSuccess) {
+  if (!sent) {
     cudaGetLastError();
     return SCOUT_ERR_CUDA;
   }
