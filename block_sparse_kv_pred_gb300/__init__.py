@@ -453,6 +453,8 @@ def build_digest8(kind, K_pool, K_scale, page_table, seq_len, B, Hkv, P, digest,
     fmt, n_slots = _pool8(K_pool, None, P)
     D, cap = K_pool.shape[-1], page_table.shape[-1]
     n_list = 0 if block_list is None else block_list.shape[0]
+    if block_list is not None and n_list == 0:  # an empty list, which has no address, is not "all blocks"
+        return digest
     ddt, per = (_BF16, 2 * D) if kind == MINMAX else (_F32, D)
     _check(lib().scout_build_digest8(
         kind, fmt, _sized(K_pool, K_pool.dtype, n_slots * P * D, "K_pool", d),
@@ -476,10 +478,13 @@ def _attn8(what, merge, q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len
     fmt, n_slots = _pool8(K_pool, V_pool, P)
     D, cap, dtype, rows = K_pool.shape[2], page_table.shape[-1], K_pool.dtype, B * Hq
     odt = _BF16 if merge else _F32
-    if O is None:
-        O = torch.empty((B, Hq, D), dtype=odt, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, Hq), dtype=_F32, device=q.device)
+    if stream is None:
+        O = torch.empty((B, Hq, D), dtype=odt, device=q.device) if O is None else O
+        lse = torch.empty((B, Hq), dtype=_F32, device=q.device) if lse is None else lse
+    else:  # outputs made here come from the stream they are written on
+        with torch.cuda.stream(stream):
+            O = torch.empty((B, Hq, D), dtype=odt, device=q.device) if O is None else O
+            lse = torch.empty((B, Hq), dtype=_F32, device=q.device) if lse is None else lse
     pool, units, wsb = n_slots * P * D, B * Hkv, workspace.numel()
     head = (fmt, _sized(q, _BF16, rows * D, "q", d), _sized(K_pool, dtype, pool, "K_pool", d),
             _sized(V_pool, dtype, pool, "V_pool", d), _sized(K_scale, _F32, n_slots, "K_scale", d),

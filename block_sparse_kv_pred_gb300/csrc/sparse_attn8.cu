@@ -1195,7 +1195,9 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_cluster_kernel(co
   cluster_barrier();  // no CTA leaves while another reads its part
 }
 
-inline size_t counters8_bytes(int64_t units) { return (size_t)((units * kMaxG * 4 + 255) / 256 * 256); }
+// The workspace's layout does not depend on the call's shape: the counters that one call leaves zero
+// are those that the next one, of any shape, finds.
+constexpr size_t kCounters8 = (size_t)kMaxUnits8 * kMaxG * sizeof(int32_t);
 // shared memory of the largest launch: two such CTAs fit an SM
 constexpr size_t kMostSmem = 1024 + (size_t)kRingBytes8 + kTileBytes + (size_t)(kMaxUnits8 + 1) * 4;
 static_assert(kCtasPerSm * (kMostSmem + 8 * 1024) <= 228 * 1024, "two CTAs an SM");
@@ -1271,8 +1273,10 @@ int launch_attn8(const Attn8Args& a, const scout_launch* launch, cudaStream_t st
     attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
     ++cfg.numAttrs;
   };
+  // the limit is the same for every call, so that calls on several host threads do not lower it for
+  // one another
   auto ready = [&](const void* kern) {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem) == cudaSuccess;
   };
   bool sent;
   if (cluster) {
@@ -1328,7 +1332,8 @@ int attn8_entry(int fmt, const void* q, const void* K_pool, const void* V_pool, 
   const int64_t units = (int64_t)B * Hkv;
   const int G = Hq / Hkv;
   if (D != kD || !valid_P(P) || G > kMaxG || units > kMaxUnits8 || !aligned16(K_pool) || !aligned16(V_pool) ||
-      (reinterpret_cast<uintptr_t>(q) & 7u) || n_slots * P > 0x7fffffffLL || units * k > kMaxSteps / 2)
+      (reinterpret_cast<uintptr_t>(q) & 7u) || n_slots > 0x7fffffffLL || n_slots * P > 0x7fffffffLL ||
+      units * k > kMaxSteps / 2)
     return SCOUT_ERR_UNSUPPORTED;
   if (merge ? (reinterpret_cast<uintptr_t>(O_cpu) & 7u) || (reinterpret_cast<uintptr_t>(O_out) & 3u)
             : (reinterpret_cast<uintptr_t>(O_part) & 7u))
@@ -1361,9 +1366,9 @@ int attn8_entry(int fmt, const void* q, const void* K_pool, const void* V_pool, 
   a.lse_out = lse_out;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.counters = reinterpret_cast<int32_t*>(ws);
-  a.slot_lse = reinterpret_cast<float*>(ws + counters8_bytes(units));
-  a.slot_O = reinterpret_cast<float*>(ws + counters8_bytes(units) + kSlotLse8);
-  a.piece_O = reinterpret_cast<float*>(ws + counters8_bytes(units) + kSlotLse8 + kSlotO8);
+  a.slot_lse = reinterpret_cast<float*>(ws + kCounters8);
+  a.slot_O = reinterpret_cast<float*>(ws + kCounters8 + kSlotLse8);
+  a.piece_O = reinterpret_cast<float*>(ws + kCounters8 + kSlotLse8 + kSlotO8);
   a.status = dev_status;
   return fmt == SCOUT_FP8_E4M3 ? attn8_by_P<SCOUT_FP8_E4M3>(P, a, launch, stream)
                                : attn8_by_P<SCOUT_FP8_E5M2>(P, a, launch, stream);
@@ -1377,7 +1382,7 @@ extern "C" size_t scout_sparse_attn8_workspace_bytes(int B, int Hq, int Hkv, int
   (void)D;
   (void)P;
   if (B <= 0 || Hkv <= 0) return 0;
-  return scout::counters8_bytes((int64_t)B * Hkv) + scout::kSlotLse8 + scout::kSlotO8 + scout::kPieceO8;
+  return scout::kCounters8 + scout::kSlotLse8 + scout::kSlotO8 + scout::kPieceO8;
 }
 
 extern "C" int scout_sparse_attn8(int fmt, const void* q, const void* K_pool, const void* V_pool,

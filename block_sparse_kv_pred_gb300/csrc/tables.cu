@@ -7,8 +7,7 @@
 // blocks) in shared memory, and after that no item depends on another: a warp takes a word of 32
 // blocks of a unit (one coalesced row piece, one ballot for the residency word), a touched block
 // of a sequence (its tokens x heads are one contiguous piece of the slot map, stored as pairs of
-// heads where their number is a power of two), or 32 list entries.  One launch, no atomics but
-// the OR of a grown row's residency word.  Bound by instruction issue and the chain lengths ->
+// heads where their number is a power of two), or 32 list entries.  One launch, no atomics.  Bound by instruction issue and the chain lengths ->
 // prefix -> free slot -> store: GB300, device time, 5.5 us for a decode step of 40 sequences, 13.8 us
 // for 40 prompts (3.3 TB/s into L2).
 //
@@ -106,7 +105,7 @@ __global__ void __launch_bounds__(kTabWarps * 32) tables_kernel(const TabArgs a)
   const int64_t n_words = (int64_t)B * a.Hkv * a.words;
   for (int64_t it0 = w0; it0 < n_words; it0 += kBatch * wn) {
     int slot[kBatch];
-    bool fresh[kBatch], mine[kBatch];
+    bool fresh[kBatch], mine[kBatch];  // a new block; a word with one (or any word, made anew)
 #pragma unroll
     for (int y = 0; y < kBatch; ++y) {
       const int64_t it = it0 + y * wn;
@@ -126,12 +125,11 @@ __global__ void __launch_bounds__(kTabWarps * 32) tables_kernel(const TabArgs a)
       const int64_t it = it0 + y * wn;
       const int u = (int)((unsigned)it / (unsigned)a.words), j = ((int)it - u * a.words) * 32 + lane;
       slot[y] = checked(a, fresh[y], slot[y]);
-      const uint32_t m = __ballot_sync(0xffffffffu, slot[y] >= 0);
+      const uint32_t m = __ballot_sync(0xffffffffu, slot[y] >= 0), made = __ballot_sync(0xffffffffu, fresh[y]);
       if (!mine[y]) continue;
       if (j < a.nblk_cap && (fresh[y] || a.prev_len == nullptr)) a.page_table[(int64_t)u * a.nblk_cap + j] = slot[y];
       if (lane == 0) {
-        if (a.prev_len == nullptr) a.bits[it] = m;
-        else if (m != 0u) atomicOr(&a.bits[it], m);
+        a.bits[it] = a.prev_len == nullptr ? m : (a.bits[it] & ~made) | m;  // a word is one warp's alone
       }
     }
   }
@@ -293,8 +291,9 @@ extern "C" int scout_build_tables(const int32_t* prev_len, const int32_t* seq_le
   const int64_t want = (warps + kTabWarps - 1) / kTabWarps;
   const int grid = (int)(want < sm_count() * kTabPerSm ? want : sm_count() * kTabPerSm);
   const size_t smem = (size_t)(5 * B + 3) * sizeof(int);
+  // (the same limit for every call: calls on several host threads do not lower it for one another)
   if (smem > 48 * 1024 && cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem) != cudaSuccess)
+                                               (5 * kMaxBatch + 3) * (int)sizeof(int)) != cudaSuccess)
     return SCOUT_ERR_CUDA;
   tables_kernel<<<grid, kTabWarps * 32, smem, stream>>>(a);
   return launch_status();

@@ -329,13 +329,13 @@ int scout_merge(const float* O_a, const float* lse_a, const float* O_b, const fl
  * its rows are made anew).  Its new blocks are j in [ceil(prev / P), ceil(seq / P)), its
  * touched blocks (those that receive a token) j in [floor(prev / P), ceil(seq / P)) when
  * seq > prev.  The new blocks of the batch, in (b, kvh, j) order, take the entries of
- * free_slots in order: the i-th takes free_slots[i] (NULL: slot i).
+ * free_slots in order: the i-th takes free_slots[i] (NULL: slot i).  They must be distinct.
  *
  * prev_len, seq_len int32 [B]; free_slots int32 [n_free]
  * page_table   int32 [B][Hkv][nblk_cap]: the new blocks' slots.  Without prev_len every
  *              other entry becomes -1; with it every other entry stays.
- * resident_bits uint32 [B][Hkv][ceil(nblk_cap/32)]: the new blocks' bits set; without
- *              prev_len the words are written whole.
+ * resident_bits uint32 [B][Hkv][ceil(nblk_cap/32)]: the new blocks' bits set (cleared where no
+ *              slot was left); without prev_len the words are written whole.
  * cu_tokens    int32 [B + 1]: new tokens before sequence b (rows of the packed new K/V), or NULL
  * slot_map     int64 [max_tokens][Hkv], or NULL: pool row (slot * P + t % P) of every new
  *              token and KV head; -1 where it has no slot, and in the rows past the last
@@ -431,9 +431,10 @@ int scout_build_digest8(int kind, int fmt, const void* K_pool, const float* K_sc
  * probabilities keep about 22 bits and the queries all of theirs, so the fp32 outputs are
  * good to fp32 rounding.  Listed blocks outside the tables, the pool or the sequence are
  * skipped and SCOUT_DEV_BAD_INDEX set.
- * workspace: scout_sparse_attn8_workspace_bytes() bytes, 16-byte aligned; its first 32 * B * Hkv
- * bytes must be zero before the first use and are left zero by every call.  Calls that may
- * overlap (streams, graphs) need a workspace each.
+ * workspace: scout_sparse_attn8_workspace_bytes() bytes (the same for every shape), 16-byte
+ * aligned; its first 131072 bytes must be zero before the first use and are left zero by every
+ * call.  One workspace serves calls of any shape, one after the other; calls that may overlap
+ * (streams, graphs) need one each.
  * Requires G <= 8, B * Hkv <= 4096, B * Hkv * k <= 2^28, n_slots * P < 2^31, pools 16-byte
  * aligned, q, O_part and O_cpu 8-byte and O_out 4-byte aligned. */
 size_t scout_sparse_attn8_workspace_bytes(int B, int Hq, int Hkv, int D, int P);

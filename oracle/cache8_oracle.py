@@ -84,8 +84,7 @@ def build_tables(prev, seq, free, n_slots, Hkv, P, cap, table=None, bits=None, m
                     status |= 1
                 taken += 1
                 table[b, h, j] = s
-                if s >= 0:
-                    bits[b, h, j] = True
+                bits[b, h, j] = s >= 0
             if seq[b] > prev[b]:
                 touched += [(b * Hkv + h, j) for j in range(prev[b] // P, -(-seq[b] // P))]
     cu = np.concatenate([[0], np.cumsum([n - p for n, p in zip(seq, prev)])])

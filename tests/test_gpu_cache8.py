@@ -106,6 +106,26 @@ def test_tables_fresh_then_grown(B, Hkv, P, cap, top):
     run_tables(seq, seq, free[used:], n_slots, Hkv, P, cap, one["table"], one["bits"], max_tokens=2, max_list=3)
 
 
+def test_tables_of_the_largest_batch_and_a_map_at_an_odd_address():
+    rng = np.random.default_rng(9)
+    seq = rng.integers(0, 60, 4096)
+    n_slots = 4096 * 4 * 2
+    run_tables(None, seq, rng.permutation(n_slots), n_slots, 2, 16, 4)
+    exp = C8.build_tables(None, [33, 70], np.arange(20), 20, 4, 32, 3)
+    m = torch.full((1 + 103 * 4,), -7, dtype=torch.int64, device="cuda")[1:].view(103, 4)  # 8 bytes past a 16-byte boundary
+    t, w = (torch.zeros((2, 4, n), dtype=torch.int32, device="cuda") for n in (3, 1))
+    bs.build_tables(i32([33, 70]), None, 20, 2, 4, 32, t, w, slot_map=m)
+    assert np.array_equal(m.cpu().numpy(), exp["slot_map"])
+
+
+def test_tables_stale_bits_of_new_blocks_are_replaced():
+    # a row that an earlier, longer sequence has left bits in; two of the new blocks get no slot
+    table, bits = -np.ones((1, 1, 40), int), np.ones((1, 1, 40), bool)
+    table[0, 0, 0] = 7
+    exp = run_tables([20], [5 * 32], [3, 4], 10, 1, 32, 40, table, bits)
+    assert exp["bits"][0, 0, :6].tolist() == [True, True, True, False, False, True] and exp["status"] == 4
+
+
 def test_tables_identity_slots_and_optional_outputs():
     run_tables(None, [70, 5], np.arange(100), 100, 2, 32, 4, use_free=False)
     seq, t = i32([33]), torch.zeros((1, 1, 2), dtype=torch.int32, device="cuda")
@@ -227,6 +247,40 @@ def test_append8_prompt_then_decode_steps(fmt, B, Hkv, P, top):
             again, _ = run_append8(rng, x, v, prev, s, table, n_slots, codes, scales, fmt, P)  # changes nothing
             assert all(np.array_equal(a[0], c) for a, c in zip(again, codes))
         prev = s
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_append8_after_scales_that_are_no_powers_of_two(fmt):
+    # another writer's scales: kept as they are while they cover, outgrown by a power of two otherwise;
+    # the arithmetic is fp32: x * (1 / scale), and code * (old / new)
+    rng = np.random.default_rng(8)
+    prev, seq, P = [5, 20, 31], [9, 32, 64], 32
+    table, n_slots = make_tables(rng, seq, 2, P, 2)
+    codes = finite_codes(rng, (n_slots, P, D), fmt)
+    # against new values of up to 15: 448 * 0.021 and 57344 * 0.00016 cover 9.4, so some scales grow and some stay
+    old = ((rng.random(n_slots) * 0.02 + 1e-3) * (448.0 / C8.LARGEST[fmt])).astype(np.float32)
+    n = sum(seq) - sum(prev)
+    x = bf16_values(rng, (n, 2, D))
+    x[:4] *= 2.0 ** -9
+    pools, sc = [pool8(codes, fmt) for _ in range(2)], [dev(old) for _ in range(2)]
+    bs.append_kv8(x.cuda(), x.cuda(), i32(table), i32(seq), 3, 2, P, *pools, *sc, prev_len=i32(prev))
+    row, f32 = 0, np.float32
+    exp, es = codes.copy(), old.copy()
+    for b in range(3):
+        for h in range(2):
+            s, had = table[b, h, prev[b] // P], prev[b] % P
+            hi = min(seq[b], (prev[b] // P + 1) * P) - prev[b]
+            new = x[row:row + hi, h].float().numpy()
+            need = f32(C8.block_scale(new.astype(np.float64), fmt))
+            if need > old[s]:
+                es[s] = need
+                exp[s, :had] = C8.encode((C8.decode(codes[s, :had], fmt).astype(f32) * (old[s] / need)).astype(np.float64), fmt)
+            exp[s, had:had + hi] = C8.encode((new * (f32(1) / es[s])).astype(np.float64), fmt)
+        row += seq[b] - prev[b]
+    first = [table[b, h, prev[b] // P] for b in range(3) for h in range(2)]
+    assert (es[first] == old[first]).any() and (es[first] != old[first]).any()
+    for p, s in zip(pools, sc):
+        assert np.array_equal(codes_of(p)[first], exp[first]) and np.array_equal(s.cpu().numpy()[first], es[first])
 
 
 def test_append8_odd_values_and_strides():
@@ -409,7 +463,7 @@ class Attn:
         Om, lm = bs.sparse_attn8_merge(*t, ws, dev(self.O_cpu), dev(self.lse_cpu), status=st, **kw)
         self.check(Om, lm, merged=True)
         assert int(st) == 0
-        assert int(ws[: 32 * self.B * self.Hkv].view(torch.int32).abs().sum()) == 0
+        assert int(ws[:131072].view(torch.int32).abs().sum()) == 0
         return O_, l
 
 
@@ -451,13 +505,65 @@ def test_attn8_more_units_than_ctas():
     Attn(13, B=64, Hkv=8, G=2, P=16, top=90, k=6).run()
 
 
-def test_attn8_is_the_same_every_time():
-    a = Attn(14, B=3, Hkv=4, G=5, P=32, top=4000, k=100)
+def test_attn8_the_most_units():
+    Attn(24, B=512, Hkv=8, G=1, P=16, top=40, k=3).run()
+
+
+def test_attn8_a_long_list_among_many():
+    # units enough for a cluster to take several, one of them longer than a cluster's share
+    a = Attn(25, B=40, Hkv=8, G=5, P=32, lens=[6000] + [100] * 39, k=180)
+    a.run()
+    assert a.counts[0, 0] == 180 and a.counts[1:].max() <= 4
+
+
+# few units, many units, a long one among many, the even split
+SPLITS = [dict(B=3, Hkv=4, G=5, P=32, top=4000, k=100), dict(B=40, Hkv=8, G=5, P=32, top=2000, k=40),
+          dict(B=40, Hkv=8, G=3, P=16, lens=[3000] + [90] * 39, k=180), dict(B=2, Hkv=4, G=4, P=64, top=30000, k=400)]
+
+
+@pytest.mark.parametrize("split", range(4))
+def test_attn8_is_the_same_every_time(split):
+    a = Attn(14, **SPLITS[split])
     t, ws = a.device(), a.workspace()
     O0, l0 = bs.sparse_attn8(*t, ws)
+    a.check(O0, l0)
     for _ in range(20):
         O1, l1 = bs.sparse_attn8(*t, ws)
         assert torch.equal(O0, O1) and torch.equal(l0, l1)
+
+
+def test_attn8_one_workspace_for_calls_of_any_shape():
+    probs = [Attn(26 + i, **c) for i, c in enumerate(SPLITS)]
+    ws = probs[0].workspace()
+    dv = [a.device() for a in probs]
+    assert all(a.workspace().numel() == ws.numel() for a in probs)
+    for i in (0, 3, 1, 2, 3, 0, 2, 1):
+        probs[i].check(*bs.sparse_attn8(*dv[i], ws))
+
+
+@pytest.mark.parametrize("split", range(4))
+def test_attn8_early_start_and_capture_without_a_call_before(split):
+    # as a programmatic dependent of the kernel before it, and captured: each kernel of the four splits
+    a = Attn(30, **SPLITS[split])
+    t, ws = a.device(), a.workspace()
+    O_, l = torch.zeros((a.B, a.Hkv * a.G, D), device="cuda"), torch.zeros((a.B, a.Hkv * a.G), device="cuda")
+    d, s = t[:9], torch.cuda.Stream()
+    torch.cuda.synchronize()
+    call = bs.Prepared("scout_sparse_attn8", 0, *[x.data_ptr() for x in d[:5]], a.n_slots, *[x.data_ptr() for x in d[5:]],
+                       a.B, a.Hkv * a.G, a.Hkv, D, a.P, a.cap, a.k, a.scale, O_.data_ptr(), l.data_ptr(), ws.data_ptr(),
+                       ws.numel(), None, bs._launch(None, pdl=True), s.cuda_stream)
+    for _ in range(5):
+        call()
+    torch.cuda.synchronize()
+    a.check(O_, l)
+    O_.zero_(), l.zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        call()
+        call()
+    g.replay()
+    torch.cuda.synchronize()
+    a.check(O_, l)
 
 
 def test_attn8_garbage_in_masked_places():
@@ -659,3 +765,6 @@ def test_calls_refuse_tensors_elsewhere_and_of_other_sizes():
         bs.sparse_attn8(*t, ws[:100])
     with pytest.raises(bs.ScoutError):
         bs.build_digest8("minmax", t[1], t[3], t[5], t[6], a.B, a.Hkv, a.P, torch.zeros(4, device="cuda"))
+    dg = torch.full((a.B, a.Hkv, a.cap, 2, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    bs.build_digest8("minmax", t[1], t[3], t[5], t[6], a.B, a.Hkv, a.P, dg, block_list=i32(np.zeros((0, 2))))
+    assert (dg == 5.0).all()  # an empty list is no block, not every block
