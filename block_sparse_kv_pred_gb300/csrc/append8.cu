@@ -87,8 +87,7 @@ __global__ void __launch_bounds__(kA8Warps * 32) append8_kernel(const App8Args a
   const int64_t wn = (int64_t)gridDim.x * kA8Warps;
   for (int64_t it = (int64_t)blockIdx.x * kA8Warps + (tid >> 5); it < items; it += wn) {
     const bool is_v = (it & 1) != 0;
-    const int64_t bh = it >> 1;
-    const int blk = (int)(bh / a.Hkv), h = (int)(bh - (int64_t)blk * a.Hkv);
+    const int bh = (int)(it >> 1), blk = (int)((unsigned)bh / (unsigned)a.Hkv), h = bh - blk * a.Hkv;
     const int b = owner_of(tou, B, blk);
     const SeqSpan s = seq_span(a.prev_len, a.seq_len, b, cap_tokens);
     const int j = s.prev / P + blk - tou[b];
@@ -182,7 +181,7 @@ extern "C" int scout_append_kv8(int fmt, const void* K_new, int64_t ld_k, const 
       ld_k < (int64_t)Hkv * D || ld_v < (int64_t)Hkv * D)
     return SCOUT_ERR_INVALID_ARG;
   if (D != kD || !valid_P(P) || B > kMaxBatch || nblk_cap > kMaxNblk || n_slots > 0x7fffffffLL ||
-      (int64_t)B * nblk_cap * P > 0x7fffffffLL || ld_k % 8 != 0 || ld_v % 8 != 0 || !aligned16(K_new) ||
+      (int64_t)B * nblk_cap * P > 0x7fffffffLL || (int64_t)B * Hkv * nblk_cap > 0x7fffffffLL || ld_k % 8 != 0 || ld_v % 8 != 0 || !aligned16(K_new) ||
       !aligned16(V_new) || !aligned16(K_pool) || !aligned16(V_pool))
     return SCOUT_ERR_UNSUPPORTED;
   if (n_tokens == 0) return SCOUT_OK;

@@ -71,8 +71,8 @@ __device__ __forceinline__ Block8 block_of(const Dig8Args& a, int64_t item) {
     u = a.block_list[2 * item];
     j = a.block_list[2 * item + 1];
   } else {
-    u = (int)(item / a.nblk_cap);
-    j = (int)(item - (int64_t)u * a.nblk_cap);
+    u = (int)((unsigned)item / (unsigned)a.nblk_cap);
+    j = (int)item - u * a.nblk_cap;
   }
   if (u == -1 && j == -1) return k;  // padding
   k.slot = -1;
@@ -240,7 +240,7 @@ extern "C" int scout_build_digest8(int kind, int fmt, const void* K_pool, const 
       (kind != SCOUT_DIGEST_MINMAX && kind != SCOUT_DIGEST_MEAN))
     return SCOUT_ERR_INVALID_ARG;
   if (D != kD || !valid_P(P) || !aligned16(K_pool) || !aligned16(digest) || (int64_t)B * Hkv > 0x7fffffffLL ||
-      n_slots > 0x7fffffffLL)
+      (int64_t)B * Hkv * nblk_cap > 0x7fffffffLL || n_slots > 0x7fffffffLL)
     return SCOUT_ERR_UNSUPPORTED;
   const int64_t n_items = block_list != nullptr ? (int64_t)n_list : (int64_t)B * Hkv * nblk_cap;
   if (n_items == 0) return SCOUT_OK;

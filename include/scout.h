@@ -405,7 +405,7 @@ typedef enum scout_fp8 {
  * dev_status (may be NULL): SCOUT_DEV_BAD_INDEX for a touched block whose slot is not in the
  * pool or whose rows are not in K_new (it is skipped), a negative length or prev_len above
  * seq_len (no new tokens); SCOUT_DEV_OVERFLOW for a length above nblk_cap * P (it counts as that).
- * No workspace.  Requires B <= 4096, nblk_cap <= 8192, B * nblk_cap * P < 2^31, n_slots < 2^31,
+ * No workspace.  Requires B <= 4096, nblk_cap <= 8192, B * nblk_cap * max(P, Hkv) < 2^31, n_slots < 2^31,
  * ld >= Hkv * D, ld % 8 == 0, and 16-byte aligned rows and pools. */
 int scout_append_kv8(int fmt, const void* K_new, int64_t ld_k, const void* V_new, int64_t ld_v, int n_tokens,
                      const int32_t* prev_len, const int32_t* seq_len, const int32_t* page_table, int B, int Hkv,
@@ -417,7 +417,7 @@ int scout_append_kv8(int fmt, const void* K_new, int64_t ld_k, const void* V_new
  * down and the maxima up to bf16, so that a digest bounds every score of its block whatever
  * the scale (with power-of-two scales both are exact).  Mean: the codes' fp32 sum (exact for
  * e4m3, at most seven roundings deep for e5m2) times scale / count.  NaN codes are passed over by
- * the minima and maxima.  Requires n_slots < 2^31.
+ * the minima and maxima.  Requires n_slots and B * Hkv * nblk_cap < 2^31.
  * A (-1, -1) entry of block_list is padding and skipped; any other entry outside the tables
  * sets SCOUT_DEV_BAD_INDEX. */
 int scout_build_digest8(int kind, int fmt, const void* K_pool, const float* K_scale, int64_t n_slots,

@@ -70,7 +70,7 @@ def test_append_refusals(L, change, rc):
     (dict(ld_k=128), INVALID), (dict(ld_v=257), UNSUPPORTED), (dict(D=96), UNSUPPORTED), (dict(P=0), UNSUPPORTED),
     (dict(B=4097), UNSUPPORTED), (dict(cap=8193), UNSUPPORTED), (dict(B=4096, cap=8192, P=64), UNSUPPORTED),
     (dict(Kp=ODD), UNSUPPORTED), (dict(V=ctypes.c_void_p(4104)), UNSUPPORTED), (dict(n_slots=1 << 31), UNSUPPORTED),
-    (dict(n=0), OK)])
+    (dict(B=4096, cap=8192, P=16, Hkv=64, ld_k=8192, ld_v=8192), UNSUPPORTED), (dict(n=0), OK)])
 def test_append8_refusals(L, change, rc):
     assert call(L.scout_append_kv8, APPEND8, **change) == rc
 
@@ -79,7 +79,8 @@ def test_append8_refusals(L, change, rc):
     (dict(kind=2), INVALID), (dict(fmt=3), INVALID), (dict(Kp=None), INVALID), (dict(Ks=None), INVALID),
     (dict(table=None), INVALID), (dict(seq=None), INVALID), (dict(digest=None), INVALID), (dict(B=0), INVALID),
     (dict(n_list=-1, list=F), INVALID), (dict(D=64), UNSUPPORTED), (dict(P=128), UNSUPPORTED),
-    (dict(Kp=ODD), UNSUPPORTED), (dict(digest=ctypes.c_void_p(4104)), UNSUPPORTED), (dict(list=F, n_list=0), OK)])
+    (dict(Kp=ODD), UNSUPPORTED), (dict(digest=ctypes.c_void_p(4104)), UNSUPPORTED), (dict(list=F, n_list=0), OK),
+    (dict(B=1 << 20, cap=1 << 12), UNSUPPORTED), (dict(n_slots=1 << 31), UNSUPPORTED)])
 def test_digest8_refusals(L, change, rc):
     assert call(L.scout_build_digest8, DIGEST8, **change) == rc
 
