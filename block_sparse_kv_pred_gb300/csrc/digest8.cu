@@ -7,8 +7,8 @@
 // and scaled once at the end, rounded down and up: a digest still bounds every score of its
 // block.  The mean sums codes in fp32.
 //
-// Bound by DRAM and its start: GB300, 8 x 16K tokens, 8 KV heads, blocks of 32, min/max: 28.5 us
-// for 151 MB (5.3 TB/s, 0.78 of the measured copy bandwidth, launch and first reads included); mean
+// Bound by DRAM and its start: GB300, 8 x 16K tokens, 8 KV heads, blocks of 32, min/max: 27.0 us
+// for 151 MB (5.6 TB/s, 0.82 of the measured copy bandwidth, launch and first reads included); mean
 // digests of 2,800 blocks of 64: 4.5 us.
 #include "fp8.cuh"
 
@@ -16,8 +16,8 @@ namespace scout {
 namespace {
 
 constexpr int kD8Warps = 8;
-// CTAs an SM (four or five are resident, the others follow).  Minima and maxima of 32,768 blocks of 32
-// tokens, GB300: 28.5 us with three, 31.1 with four or five, 28.6 with six or eight.
+// CTAs an SM (three are resident, the others follow).  Minima and maxima of 32,768 blocks of 32 tokens,
+// GB300: 27.2 us with three, 29.8 with four, 27.0 with six, 27.5 with twelve, 29.2 with 24.
 constexpr int kD8PerSm = 6;
 
 __device__ __forceinline__ uint32_t h2min(uint32_t a, uint32_t b) {
