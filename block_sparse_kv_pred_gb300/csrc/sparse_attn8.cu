@@ -70,7 +70,7 @@ constexpr int kSnap = 8;
 constexpr int kSnapUnits = 4;
 constexpr int kMaxUnits8 = 4096;
 constexpr int kMaxGrid8 = 512;
-constexpr int64_t kMaxSteps = (int64_t)1 << 29;
+constexpr int64_t kMaxEntries8 = (int64_t)1 << 28;  // list entries of a launch: at most two steps each, so steps fit an int
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWBoost = 14;            // weights are kept as 2^14 w, so that their low parts stay normal f16
@@ -1333,7 +1333,7 @@ int attn8_entry(int fmt, const void* q, const void* K_pool, const void* V_pool, 
   const int G = Hq / Hkv;
   if (D != kD || !valid_P(P) || G > kMaxG || units > kMaxUnits8 || !aligned16(K_pool) || !aligned16(V_pool) ||
       (reinterpret_cast<uintptr_t>(q) & 7u) || n_slots > 0x7fffffffLL || n_slots * P > 0x7fffffffLL ||
-      units * k > kMaxSteps / 2)
+      units * k > kMaxEntries8)
     return SCOUT_ERR_UNSUPPORTED;
   if (merge ? (reinterpret_cast<uintptr_t>(O_cpu) & 7u) || (reinterpret_cast<uintptr_t>(O_out) & 3u)
             : (reinterpret_cast<uintptr_t>(O_part) & 7u))

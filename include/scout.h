@@ -80,7 +80,8 @@ typedef enum scout_digest_kind {
  * (N / 128) * S <= max_ctas; the grid keeps at least one CTA per 128-row tile of W.
  *
  * Early starts (programmatic dependent launch), for scout_predict_q,
- * scout_score_topk and scout_sparse_attn(_merge).  Each of these kernels may start
+ * scout_score_topk and scout_sparse_attn(_merge), and scout_sparse_attn8(_merge), which does as
+ * scout_sparse_attn does.  Each of these kernels may start
  * before the kernel it depends on has finished, do the part of its work that does
  * not read that kernel's output, and wait for that kernel (its completion and the
  * visibility of its writes) just before the first read that may:

@@ -682,6 +682,36 @@ def test_attn8_on_other_streams_and_in_graphs():
         a.check(O_, l)
 
 
+@pytest.mark.parametrize("split", range(4))
+def test_attn8_started_early_by_an_event(split):
+    # the first call's partial is the second one's CPU partial, on another stream that waits for the event
+    # the first call fires before it completes
+    a, b = Attn(34, **SPLITS[split]), Attn(35, **SPLITS[split])
+    ta, tb, wa, wb = a.device(), b.device(), a.workspace(), b.workspace()
+    s1, s2, ev = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.Event()
+    Hq = a.Hkv * a.G
+    O1, l1 = torch.empty((a.B, Hq, D), device="cuda"), torch.empty((a.B, Hq), device="cuda")
+    O2 = torch.empty((a.B, Hq, D), dtype=torch.bfloat16, device="cuda")
+    l2 = torch.empty((a.B, Hq), device="cuda")
+    ev.record(s1)
+    torch.cuda.synchronize()
+    p = lambda t: [x.data_ptr() for x in t]  # noqa: E731
+    one = bs.Prepared("scout_sparse_attn8", 0, *p(ta[:5]), a.n_slots, *p(ta[5:9]), a.B, Hq, a.Hkv, D, a.P, a.cap, a.k, a.scale,
+                      *p((O1, l1, wa)), wa.numel(), None, bs._launch(None, early_event=ev), s1.cuda_stream)
+    two = bs.Prepared("scout_sparse_attn8_merge", 0, *p(tb[:5]), b.n_slots, *p(tb[5:9]), b.B, Hq, b.Hkv, D, b.P, b.cap, b.k,
+                      b.scale, *p((O1, l1, O2, l2, wb)), wb.numel(), None, None, s2.cuda_stream)
+    for _ in range(3):
+        O1.fill_(3.0), l1.fill_(3.0)
+        torch.cuda.synchronize()
+        one()
+        s2.wait_event(ev)
+        two()
+        torch.cuda.synchronize()
+        a.check(O1, l1)
+        b.O_cpu, b.lse_cpu = O1.cpu().numpy(), l1.cpu().numpy()
+        b.check(O2, l2, merged=True)
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
