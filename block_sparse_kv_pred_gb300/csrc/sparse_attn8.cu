@@ -130,6 +130,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same without an addend: no accumulator has to be cleared.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -216,14 +224,14 @@ template <int F>
 __device__ __forceinline__ void tile_scores(const uint4 (&k)[4], const uint32_t (&qb)[8][2], float (&s)[4]) {
   const uint32_t* lo = reinterpret_cast<const uint32_t*>(&k[0]);  // row g: words 0..7
   const uint32_t* hi = reinterpret_cast<const uint32_t*>(&k[2]);  // row g + 8
-  float s2[4] = {0.f, 0.f, 0.f, 0.f};
-  s[0] = s[1] = s[2] = s[3] = 0.f;
+  float s2[4];
 #pragma unroll
   for (int w = 0; w < 8; ++w) {
     uint32_t a0, a1, a2, a3;
     unpack4<F>(lo[w], a0, a2);
     unpack4<F>(hi[w], a1, a3);
-    mma_f16(w & 1 ? s2 : s, a0, a1, a2, a3, qb[w][0], qb[w][1]);
+    if (w < 2) mma_f16_first(w & 1 ? s2 : s, a0, a1, a2, a3, qb[w][0], qb[w][1]);
+    else mma_f16(w & 1 ? s2 : s, a0, a1, a2, a3, qb[w][0], qb[w][1]);
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) s[e] += s2[e];
@@ -254,8 +262,8 @@ __device__ __forceinline__ void tile_output(const uint4 (&v)[4], const float (&w
     unpack4<F>(__byte_perm(r2[i], r3[i], 0x7362), c[1][0], c[1][1]);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_f16(d, a[x][0], a[x][1], c[x][0], c[x][1], bl0, bl1);
+      float d[4];
+      mma_f16_first(d, a[x][0], a[x][1], c[x][0], c[x][1], bl0, bl1);
       mma_f16(d, a[x][0], a[x][1], c[x][0], c[x][1], bh0, bh1);
 #pragma unroll
       for (int e = 0; e < 4; ++e) st.o[2 * i + x][e] += d[e];
@@ -519,8 +527,9 @@ struct WarpStream {
   LaneOffsets off;
   int i, at;         // the next step, and the ring half of its K
   uint32_t phase;    // of that half's barrier
-  int issued, landed_n;  // halves
-  bool ok;           // false once a bounded wait ran out: nothing more is issued or computed
+  int n_issue;       // n_mine; 0 once a bounded wait ran out: nothing more is issued or computed
+  int lost;          // the half whose wait ran out, -1
+  int trigger;       // the step at which the next batch's resolution goes on
   // a tile on its way through the three dependent reads: list entry, page-table slot, scales
   int ru, rj, rlen, rslot, rrow, rnt;
   float rks, rvs;
@@ -529,8 +538,8 @@ struct WarpStream {
                                         uint64_t* bars, const MAP& mp, int warp, int ln, int lo, int n)
       : a(args), tmK(k), tmV(v), ring(sm + warp * (kHalves * kHalf)),
         tiles(reinterpret_cast<Tile*>(sm + kRingBytes8) + warp * (4 * kBatch)), full(bars + warp * kHalves), map(mp),
-        lane(ln), wlo(lo), n_mine(n), off(lane_offsets(ln)), i(0), at(0), phase(0), issued(0), landed_n(0), ok(true),
-        ru(0), rj(-1), rlen(0), rslot(-1), rrow(0), rnt(0), rks(0.f), rvs(0.f) {}
+        lane(ln), wlo(lo), n_mine(n), off(lane_offsets(ln)), i(0), at(0), phase(0), n_issue(n), lost(-1),
+        trigger(n > kBatch ? 0 : 0x7fffffff), ru(0), rj(-1), rlen(0), rslot(-1), rrow(0), rnt(0), rks(0.f), rvs(0.f) {}
 
   // Tile 2 kBatch b + lane of this warp.
   __device__ __forceinline__ void resolve_entry(int batch) {
@@ -563,16 +572,14 @@ struct WarpStream {
     rvs = fine ? __ldg(a.V_scale + rslot) : 0.f;
   }
   __device__ __forceinline__ Tile* tile_of(int k, int y) {
-    return tiles + ((k / kBatch) & 1) * (2 * kBatch) + 2 * (k % kBatch) + y;
+    return tiles + ((2 * k) & (4 * kBatch - 1)) + y;
   }
 
   // Half h: K (even) or V (odd) of step h / 2, into ring half `to` = h % kHalves.  One lane; every
   // lane has read what was there.  The box starts at a whole row (x = 0).
   __device__ __forceinline__ void issue(int h, int to) {
     const int k = h >> 1;
-    if (k >= n_mine || !ok) return;
-    issued = h + 1;
-    if (lane != 0) return;
+    if (lane != 0 || k >= n_issue) return;
     uint64_t* bar = full + to;
     uint8_t* dst = ring + to * kHalf;
     const CUtensorMap* m = h & 1 ? tmV : tmK;
@@ -596,13 +603,26 @@ struct WarpStream {
     if (w0.y > 0) tma_load_2d(dst, m, 0, w0.x, bar);
     if (w1.y > 0) tma_load_2d(dst + 2048, m, 0, w1.x, bar);
   }
-  __device__ __forceinline__ void landed() {
-    if (ok && !mbar_wait(full + at, phase)) {
-      if (lane == 0) report(a.status, SCOUT_DEV_TIMEOUT);
-      ok = false;
+  // Waits for half h; false (for the whole warp) once a wait has run out.
+  __device__ __forceinline__ bool landed(int h) {
+    if (n_issue == 0) return false;
+    if (__all_sync(0xffffffffu, mbar_wait(full + at, phase))) return true;
+    if (lane == 0) report(a.status, SCOUT_DEV_TIMEOUT);
+    lost = h;
+    n_issue = 0;
+    return false;
+  }
+  // The next batch's resolution, in four parts while this batch runs.
+  __device__ __forceinline__ void go_on() {
+    const int ib = i % kBatch, next = i / kBatch + 1;
+    if (ib == 0) resolve_entry(next);
+    if (ib == 4) resolve_slot();
+    if (ib == 8) resolve_tile();
+    if (ib == 12) {
+      tiles[(next & 1) * (2 * kBatch) + lane] = Tile{rrow, rnt, rks, rvs};
+      __syncwarp();
     }
-    ok = __all_sync(0xffffffffu, ok);
-    landed_n += ok;
+    trigger = ib < 12 ? i + 4 : (next + 1) * kBatch < n_mine ? next * kBatch : 0x7fffffff;
   }
   __device__ __forceinline__ void next_half() {
     if (++at == kHalves) {
@@ -632,22 +652,12 @@ struct WarpStream {
     for (int md = 0; md < 8; ++md) st.o[md][0] = st.o[md][1] = st.o[md][2] = st.o[md][3] = 0.f;
     int was;
     while (true) {
-      const int ib = i % kBatch;  // the next batch is resolved while this one runs
-      if ((i / kBatch + 1) * kBatch < n_mine) {
-        if (ib == 0) resolve_entry(i / kBatch + 1);
-        if (ib == 4) resolve_slot();
-        if (ib == 8) resolve_tile();
-        if (ib == 12) {
-          tiles[(((i / kBatch) + 1) & 1) * (2 * kBatch) + lane] = Tile{rrow, rnt, rks, rvs};
-          __syncwarp();
-        }
-      }
+      if (i == trigger) go_on();
       const Tile t0 = *tile_of(i, 0), t1 = *tile_of(i, 1);
       const float kf[2][2] = {{t0.ks * qf[0], t0.ks * qf[1]}, {t1.ks * qf[0], t1.ks * qf[1]}};
       float s[2][4];
-      const bool any = t0.nt + t1.nt > 0;
-      landed();
-      if (any && ok) {
+      bool any = landed(2 * i) && t0.nt + t1.nt > 0;
+      if (any) {
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           uint4 k[4];
@@ -659,12 +669,12 @@ struct WarpStream {
       __syncwarp();
       issue(2 * i + kHalves, at);
       next_half();
-      if (any && ok) {
+      if (any) {
         if (!(P != 16 && t1.nt == 16 && step_weights_page(s, kf[0], t0.vs, st)))
           step_weights_any(s, kf, t0.nt, t1.nt, t0.vs, t1.vs, g, st);
       }
-      landed();
-      if (any && ok) {
+      any = landed(2 * i + 1) && any;
+      if (any) {
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           uint4 v[4];
@@ -703,7 +713,9 @@ struct WarpStream {
   }
   // Given up: let the copies that were started land (again for a bounded time) before leaving.
   __device__ __forceinline__ void drain() {
-    for (int h = landed_n; !ok && h < issued; ++h) mbar_wait(full + h % kHalves, (uint32_t)(h / kHalves) & 1u);
+    // at most kHalves are on their way: the one that was waited for and what follows it
+    for (int h = lost; lost >= 0 && h < min(lost + kHalves, 2 * n_mine); ++h)
+      mbar_wait(full + h % kHalves, (uint32_t)(h / kHalves) & 1u);
   }
 };
 
