@@ -467,8 +467,9 @@ def build_digest8(kind, K_pool, K_scale, page_table, seq_len, B, Hkv, P, digest,
 
 
 def sparse_attn8_workspace(B, Hq, Hkv, P, D=128, device="cuda") -> torch.Tensor:
-    n = lib().scout_sparse_attn8_workspace_bytes(B, Hq, Hkv, D, P)
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    w = torch.empty(lib().scout_sparse_attn8_workspace_bytes(B, Hq, Hkv, D, P), dtype=torch.uint8, device=device)
+    w[:131072].zero_()  # the counters
+    return w
 
 
 def _attn8(what, merge, q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq, Hkv, P, k,

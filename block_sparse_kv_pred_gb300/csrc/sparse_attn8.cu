@@ -219,22 +219,36 @@ __device__ __forceinline__ void clear_past(uint4 (&v)[4], int nt, int lane) {
     if (2 * (lane & 3) + (i & 1) + 8 * (i >> 1) >= nt) v[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Scores of one tile: s[0], s[1] = token g, heads 2t, 2t+1; s[2], s[3] = token g + 8.
+// Scores of a step's two tiles: s[y][0], s[y][1] = token g of tile y, heads 2t, 2t+1; s[y][2], s[y][3] =
+// token g + 8.  Both tiles advance together, two chains of products each.
 template <int F>
-__device__ __forceinline__ void tile_scores(const uint4 (&k)[4], const uint32_t (&qb)[8][2], float (&s)[4]) {
-  const uint32_t* lo = reinterpret_cast<const uint32_t*>(&k[0]);  // row g: words 0..7
-  const uint32_t* hi = reinterpret_cast<const uint32_t*>(&k[2]);  // row g + 8
-  float s2[4];
+__device__ __forceinline__ void step_scores(const uint8_t* half, const uint32_t (&off)[2], const uint32_t (&qb)[8][2],
+                                            float (&s)[2][4]) {
+  float s2[2][4];
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    uint32_t a0, a1, a2, a3;
-    unpack4<F>(lo[w], a0, a2);
-    unpack4<F>(hi[w], a1, a3);
-    if (w < 2) mma_f16_first(w & 1 ? s2 : s, a0, a1, a2, a3, qb[w][0], qb[w][1]);
-    else mma_f16(w & 1 ? s2 : s, a0, a1, a2, a3, qb[w][0], qb[w][1]);
+  for (int i = 0; i < 2; ++i) {  // pieces 2t + i: k-steps 4 i .. 4 i + 3
+    uint4 lo[2], hi[2];          // rows g and g + 8
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      lo[y] = *reinterpret_cast<const uint4*>(half + y * 2048 + off[i]);
+      hi[y] = *reinterpret_cast<const uint4*>(half + y * 2048 + off[i] + 1024);
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        uint32_t a0, a1, a2, a3;
+        unpack4<F>(w == 0 ? lo[y].x : w == 1 ? lo[y].y : w == 2 ? lo[y].z : lo[y].w, a0, a2);
+        unpack4<F>(w == 0 ? hi[y].x : w == 1 ? hi[y].y : w == 2 ? hi[y].z : hi[y].w, a1, a3);
+        if (i == 0 && w < 2) mma_f16_first(w & 1 ? s2[y] : s[y], a0, a1, a2, a3, qb[4 * i + w][0], qb[4 * i + w][1]);
+        else mma_f16(w & 1 ? s2[y] : s[y], a0, a1, a2, a3, qb[4 * i + w][0], qb[4 * i + w][1]);
+      }
+    }
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) s[e] += s2[e];
+  for (int y = 0; y < 2; ++y)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[y][e] += s2[y][e];
 }
 
 // O^T += V^T W^T of one tile; w[]: the weights in the layout of the scores.  A tile's products start
@@ -657,14 +671,7 @@ struct WarpStream {
       const float kf[2][2] = {{t0.ks * qf[0], t0.ks * qf[1]}, {t1.ks * qf[0], t1.ks * qf[1]}};
       float s[2][4];
       bool any = landed(2 * i) && t0.nt + t1.nt > 0;
-      if (any) {
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          uint4 k[4];
-          read_pieces(ring + at * kHalf + y * 2048, off.k, k);
-          tile_scores<F>(k, qb, s[y]);
-        }
-      }
+      if (any) step_scores<F>(ring + at * kHalf, off.k, qb, s);
       // the reads above have returned: the products that use them have been issued
       __syncwarp();
       issue(2 * i + kHalves, at);
