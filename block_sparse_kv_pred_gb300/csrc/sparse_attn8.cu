@@ -36,11 +36,11 @@
 // tile, and its operands would need q and the weights in 8 bits or K and V widened in shared
 // memory.  The products take 52 ns of an SM's time a step (48 at 1.08 ns), the conversions about
 // as much; a step's 8 KB take 182 ns of the SM's share of DRAM, so a long launch is bound by DRAM:
-// GB300, 4 x 128K tokens dense, 178 us for 1.08 GB (6.0 TB/s, 0.89 of the measured copy bandwidth;
+// GB300, 4 x 128K tokens dense, 175 us for 1.08 GB (6.1 TB/s, 0.90 of the measured copy bandwidth;
 // the SMs' shares of it differ, and the first are done at 0.75 of the time).  40 sequences of 2,048
-// listed tokens, 8 x 5 heads: 38.6 us for 152 MB, of which the first 4 go by before the copies start
+// listed tokens, 8 x 5 heads: 38.0 us for 152 MB, of which the first 4 go by before the copies start
 // (counts, list, page table), 24 stream at 6.3 TB/s, and the rest is the slowest warp and the end
-// phase (barrier, join, barrier).  One 4K sequence: 6.9 us, all latency.
+// phase (barrier, join, barrier).  One 4K sequence: 6.6 us, all latency.
 #include <atomic>
 
 #include "fp8.cuh"
