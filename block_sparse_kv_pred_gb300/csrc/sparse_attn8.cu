@@ -443,7 +443,7 @@ __device__ __forceinline__ void write_head(const Attn8Args& a, int u, int h, int
   }
   const float m = fmaxf(lse, c.lse);
   float wg = 0.f, wc = 0.f, out = -INFINITY;
-  if (m != -INFINITY) {
+  if (lse != -INFINITY || c.lse != -INFINITY) {  // (a NaN on one side is not two empty sides)
     wg = expf(lse - m);
     wc = expf(c.lse - m);
     const float sum = wg + wc;
@@ -452,9 +452,11 @@ __device__ __forceinline__ void write_head(const Attn8Args& a, int u, int h, int
     wc /= sum;
   }
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
-    reinterpret_cast<uint32_t*>(a.O_out + row * kD)[lane + 32 * x] =
-        pack_bf16(wg * o[x].x + wc * c.o[x].x, wg * o[x].y + wc * c.o[x].y);
+  for (int x = 0; x < 2; ++x) {
+    // an empty CPU partial's output is not read: it may never have been written
+    const float2 oc = c.lse == -INFINITY ? make_float2(0.f, 0.f) : make_float2(wc * c.o[x].x, wc * c.o[x].y);
+    reinterpret_cast<uint32_t*>(a.O_out + row * kD)[lane + 32 * x] = pack_bf16(wg * o[x].x + oc.x, wg * o[x].y + oc.y);
+  }
   if (lane == 0 && a.lse_out != nullptr) a.lse_out[row] = out;
 }
 

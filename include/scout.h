@@ -431,7 +431,7 @@ int scout_build_digest8(int kind, int fmt, const void* K_pool, const float* K_sc
  * split and early starts as theirs (it waits before its first global read).  The
  * probabilities keep about 22 bits and the queries all of theirs, so the fp32 outputs are
  * good to fp32 rounding.  Listed blocks outside the tables, the pool or the sequence are
- * skipped and SCOUT_DEV_BAD_INDEX set.
+ * skipped and SCOUT_DEV_BAD_INDEX set.  O_cpu of a head with lse_cpu = -inf is not used.
  * workspace: scout_sparse_attn8_workspace_bytes() bytes (the same for every shape), 16-byte
  * aligned; its first 131072 bytes must be zero before the first use and are left zero by every
  * call.  One workspace serves calls of any shape, one after the other; calls that may overlap

@@ -467,6 +467,11 @@ class Attn:
         return O_, l
 
 
+# few units, many units, a long one among many, the even split
+SPLITS = [dict(B=3, Hkv=4, G=5, P=32, top=4000, k=100), dict(B=40, Hkv=8, G=5, P=32, top=2000, k=40),
+          dict(B=40, Hkv=8, G=3, P=16, lens=[3000] + [90] * 39, k=180), dict(B=2, Hkv=4, G=4, P=64, top=30000, k=400)]
+
+
 @pytest.mark.parametrize("G", range(1, 9))
 def test_attn8_groups(G):
     Attn(G, G=G, fmt="e4m3" if G % 2 else "e5m2", P=(16, 32, 64)[G % 3]).run()
@@ -514,11 +519,6 @@ def test_attn8_a_long_list_among_many():
     a = Attn(25, B=40, Hkv=8, G=5, P=32, lens=[6000] + [100] * 39, k=180)
     a.run()
     assert a.counts[0, 0] == 180 and a.counts[1:].max() <= 4
-
-
-# few units, many units, a long one among many, the even split
-SPLITS = [dict(B=3, Hkv=4, G=5, P=32, top=4000, k=100), dict(B=40, Hkv=8, G=5, P=32, top=2000, k=40),
-          dict(B=40, Hkv=8, G=3, P=16, lens=[3000] + [90] * 39, k=180), dict(B=2, Hkv=4, G=4, P=64, top=30000, k=400)]
 
 
 @pytest.mark.parametrize("split", range(4))
@@ -586,6 +586,20 @@ def test_attn8_nan_in_a_live_place_is_seen():
     O_, l = bs.sparse_attn8(*a.device(), a.workspace())
     assert torch.isnan(l[0, :2]).all() and torch.isnan(O_[0, :2]).all()
     assert torch.isfinite(l[0, 2:]).all() and torch.isfinite(O_[0, 2:]).all()
+    # and through the merge, beside an empty CPU partial too
+    lc = dev(np.array([[-np.inf, 1.0, -np.inf, 1.0]], np.float32))
+    O_, l = bs.sparse_attn8_merge(*a.device(), a.workspace(), torch.ones((1, 4, D), device="cuda"), lc)
+    assert torch.isnan(l[0, :2]).all() and torch.isnan(O_[0, :2]).all()
+    assert torch.isfinite(l[0, 2:]).all() and torch.isfinite(O_[0, 2:]).all()
+
+
+@pytest.mark.parametrize("split", range(4))
+def test_attn8_an_empty_cpu_partial_is_not_read(split):
+    a = Attn(40, **SPLITS[split])
+    a.counts[0, 0] = 0  # with and without blocks on the GPU
+    oc = dev(np.where(np.isinf(a.lse_cpu)[..., None], np.nan, a.O_cpu).astype(np.float32))
+    a.O_cpu[np.isinf(a.lse_cpu)] = 0
+    a.check(*bs.sparse_attn8_merge(*a.device(), a.workspace(), oc, dev(a.lse_cpu)), merged=True)
 
 
 def test_attn8_zero_and_tiny_values():
