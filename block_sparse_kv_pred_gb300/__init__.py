@@ -4,6 +4,8 @@ Argument marshalling only: every entry point forwards device pointers of torch
 tensors, sizes and the current CUDA stream to the C ABI declared in
 ``include/scout.h``; all arithmetic runs in the library's CUDA kernels.  There is
 no fallback: if ``libscout.so`` is missing or fails to load, every call raises.
+The calls around the tables and the 8-bit cache do the same in native code
+(``csrc/binding.cpp``), the others through ``ctypes``.
 """
 from __future__ import annotations
 
@@ -317,58 +319,23 @@ def merge(O_a, lse_a, O_b, lse_b, O_out=None, lse_out=None, stream=None):
 # ---------------------------------------------------------------------------
 # tables, cache writes and 8-bit caches
 # ---------------------------------------------------------------------------
-_FP8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
-_I32, _I64, _F32, _BF16, _U8 = torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.uint8
+_NATIVE = None
 
 
-def _sized(t, dtype, numel, name: str, device: int) -> int:
-    """Device pointer of a contiguous tensor of this type and size on the call's device."""
-    try:
-        if t.dtype is dtype and t.numel() == numel and t.get_device() == device and t.is_contiguous():
-            return t.data_ptr()
-        have = f"{t.dtype} of {tuple(t.shape)} on {t.device}"
-    except AttributeError:
-        have = type(t).__name__
-    where = f"cuda:{device}" if device >= 0 else "the call's device"
-    raise ScoutError(f"{name} must be a contiguous {dtype} tensor of {numel} elements on {where}, got {have}")
-
-
-def _here(t, name: str) -> int:
-    """The device of a call: that of ``t``, which must be the current one."""
-    d = t.get_device() if isinstance(t, torch.Tensor) else -1
-    if d < 0 or d != torch.cuda.current_device():
-        raise ScoutError(f"{name} must be a CUDA tensor on the current device")
-    return d
-
-
-def _stream_on(stream, device: int) -> int:
-    """The handle of ``stream``, or of the device's current one."""
-    if stream is None:
-        return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
-    return stream.cuda_stream
-
-
-def _pool8(K_pool, V_pool, P):
-    """(format, slots) of an 8-bit pool or pair of pools [n_slots][P][D]."""
-    fmt = _FP8.get(K_pool.dtype)
-    if fmt is None:
-        raise ScoutError(f"an 8-bit pool must be float8_e4m3fn or float8_e5m2, got {K_pool.dtype}")
-    shape = K_pool.shape
-    if len(shape) != 3 or shape[1] != P or (V_pool is not None and V_pool.shape != shape):
-        raise ScoutError(f"the pools must be [n_slots][{P}][D] alike, got {tuple(shape)}")
-    return fmt, shape[0]
-
-
-def _rows(t, Hkv, D, name, device):
-    """(pointer, token stride) of new rows [n_tokens][Hkv][D], each token's heads contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.dim() != 3 or t.shape[1:] != (Hkv, D):
-        raise ScoutError(f"{name} must be a bf16 tensor [n_tokens][{Hkv}][{D}]")
-    if t.get_device() != device:
-        raise ScoutError(f"{name} must be on the call's CUDA device, got {t.device}")
-    n, (s0, s1, s2) = t.shape[0], t.stride()
-    if n and (s2 != 1 or (Hkv > 1 and s1 != D)):
-        raise ScoutError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
-    return t.data_ptr(), (s0 if n > 1 else Hkv * D)
+def _native():
+    """The native binding of these calls (csrc/binding.cpp): one call checks the tensors, their
+    device and their sizes and enters the C ABI."""
+    global _NATIVE
+    if _NATIVE is None:
+        lib()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ScoutError(f"_binding.so is missing or does not load ({e}): "
+                             "run `python -m block_sparse_kv_pred_gb300.build`") from e
+        _binding.set_error(ScoutError)
+        _NATIVE = _binding
+    return _NATIVE
 
 
 def build_tables(seq_len, free_slots, n_slots, B, Hkv, P, page_table, resident_bits, prev_len=None, cu_tokens=None,
@@ -383,39 +350,15 @@ def build_tables(seq_len, free_slots, n_slots, B, Hkv, P, page_table, resident_b
     ``block_list`` int32 [max_list][2] (the touched blocks, -1 past the last), ``counts`` int32 [3]
     (new tokens, touched blocks, new blocks).  ``status`` receives SCOUT_DEV_OVERFLOW (4) when
     something did not fit and SCOUT_DEV_BAD_INDEX (1) for a bad slot or length."""
-    d = _here(page_table, "page_table")
-    cap = page_table.shape[-1]
-    n_free = n_slots if free_slots is None else free_slots.numel()
-    max_tokens = 0 if slot_map is None else slot_map.shape[0]
-    max_list = 0 if block_list is None else block_list.shape[0]
-    _check(lib().scout_build_tables(
-        None if prev_len is None else _sized(prev_len, _I32, B, "prev_len", d), _sized(seq_len, _I32, B, "seq_len", d),
-        None if free_slots is None else _sized(free_slots, _I32, n_free, "free_slots", d), n_free, n_slots, B, Hkv, P, cap,
-        _sized(page_table, _I32, B * Hkv * cap, "page_table", d),
-        _sized(resident_bits, _I32, B * Hkv * (-(-cap // 32)), "resident_bits", d),
-        None if cu_tokens is None else _sized(cu_tokens, _I32, B + 1, "cu_tokens", d),
-        None if slot_map is None else _sized(slot_map, _I64, max_tokens * Hkv, "slot_map", d), max_tokens,
-        None if block_list is None else _sized(block_list, _I32, max_list * 2, "block_list", d), max_list,
-        None if counts is None else _sized(counts, _I32, 3, "counts", d),
-        None if status is None else _sized(status, _I32, 1, "status", d), _stream_on(stream, d)), "scout_build_tables")
+    _native().build_tables(page_table, seq_len, free_slots, n_slots, B, Hkv, P, resident_bits, prev_len, cu_tokens,
+                           slot_map, block_list, counts, status, stream)
     return page_table, resident_bits
 
 
 def append_kv(K_new, V_new, slot_map, Hkv, P, K_pool, V_pool, status=None, stream=None):
     """New bf16 K/V rows [n_tokens][Hkv][D] (token strides free) into bf16 pools [n_slots][P][D] at
     the pool rows of ``slot_map`` int64 [n_tokens][Hkv] (negative: skipped)."""
-    d = _here(K_pool, "K_pool")
-    D, n, n_slots = K_pool.shape[-1], K_new.shape[0], K_pool.shape[0]
-    kp, ld_k = _rows(K_new, Hkv, D, "K_new", d)
-    vp, ld_v = _rows(V_new, Hkv, D, "V_new", d)
-    if V_new.shape[0] != n:
-        raise ScoutError("K_new and V_new must hold the same tokens")
-    if n == 0:
-        return K_pool, V_pool
-    _check(lib().scout_append_kv(
-        kp, ld_k, vp, ld_v, _sized(slot_map, _I64, n * Hkv, "slot_map", d), n, Hkv, D, P,
-        _sized(K_pool, _BF16, n_slots * P * D, "K_pool", d), _sized(V_pool, _BF16, n_slots * P * D, "V_pool", d), n_slots,
-        None if status is None else _sized(status, _I32, 1, "status", d), _stream_on(stream, d)), "scout_append_kv")
+    _native().append_kv(K_pool, V_pool, Hkv, P, K_new, V_new, slot_map, status, stream)
     return K_pool, V_pool
 
 
@@ -425,22 +368,8 @@ def append_kv8(K_new, V_new, page_table, seq_len, B, Hkv, P, K_pool, V_pool, K_s
     [n_slots][P][D] (float8_e4m3fn or float8_e5m2) with a power-of-two scale per slot, fp32
     [n_slots].  Sequence b grows from ``prev_len[b]`` (None: 0) to ``seq_len[b]`` tokens.  The scale of
     a block that holds tokens already never shrinks; when it grows, their codes are rounded to it."""
-    d = _here(K_pool, "K_pool")
-    fmt, n_slots = _pool8(K_pool, V_pool, P)
-    D, n, cap = K_pool.shape[-1], K_new.shape[0], page_table.shape[-1]
-    kp, ld_k = _rows(K_new, Hkv, D, "K_new", d)
-    vp, ld_v = _rows(V_new, Hkv, D, "V_new", d)
-    if V_new.shape[0] != n:
-        raise ScoutError("K_new and V_new must hold the same tokens")
-    if n == 0:
-        return K_pool, V_pool
-    pool, dtype = n_slots * P * D, K_pool.dtype
-    _check(lib().scout_append_kv8(
-        fmt, kp, ld_k, vp, ld_v, n, None if prev_len is None else _sized(prev_len, _I32, B, "prev_len", d),
-        _sized(seq_len, _I32, B, "seq_len", d), _sized(page_table, _I32, B * Hkv * cap, "page_table", d), B, Hkv, D, P, cap,
-        _sized(K_pool, dtype, pool, "K_pool", d), _sized(V_pool, dtype, pool, "V_pool", d),
-        _sized(K_scale, _F32, n_slots, "K_scale", d), _sized(V_scale, _F32, n_slots, "V_scale", d), n_slots,
-        None if status is None else _sized(status, _I32, 1, "status", d), _stream_on(stream, d)), "scout_append_kv8")
+    _native().append_kv8(K_pool, V_pool, B, Hkv, P, K_new, V_new, page_table, seq_len, K_scale, V_scale, prev_len, status,
+                         stream)
     return K_pool, V_pool
 
 
@@ -448,21 +377,8 @@ def build_digest8(kind, K_pool, K_scale, page_table, seq_len, B, Hkv, P, digest,
                   stream=None):
     """Block digests of an 8-bit pool: as build_digest, over code * scale (minima rounded down, maxima
     up).  (-1, -1) entries of ``block_list`` are skipped."""
-    kind = _KIND[kind]
-    d = _here(K_pool, "K_pool")
-    fmt, n_slots = _pool8(K_pool, None, P)
-    D, cap = K_pool.shape[-1], page_table.shape[-1]
-    n_list = 0 if block_list is None else block_list.shape[0]
-    if block_list is not None and n_list == 0:  # an empty list, which has no address, is not "all blocks"
-        return digest
-    ddt, per = (_BF16, 2 * D) if kind == MINMAX else (_F32, D)
-    _check(lib().scout_build_digest8(
-        kind, fmt, _sized(K_pool, K_pool.dtype, n_slots * P * D, "K_pool", d),
-        _sized(K_scale, _F32, n_slots, "K_scale", d), n_slots, _sized(page_table, _I32, B * Hkv * cap, "page_table", d),
-        _sized(seq_len, _I32, B, "seq_len", d), B, Hkv, D, P, cap,
-        None if block_list is None else _sized(block_list, _I32, n_list * 2, "block_list", d), n_list,
-        _sized(digest, ddt, B * Hkv * cap * per, "digest", d),
-        None if status is None else _sized(status, _I32, 1, "status", d), _stream_on(stream, d)), "scout_build_digest8")
+    _native().build_digest8(_KIND[kind], K_pool, B, Hkv, P, K_scale, page_table, seq_len, digest, block_list, status,
+                            stream)
     return digest
 
 
@@ -472,54 +388,22 @@ def sparse_attn8_workspace(B, Hq, Hkv, P, D=128, device="cuda") -> torch.Tensor:
     return w
 
 
-def _attn8(what, merge, q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq, Hkv, P, k,
-           scale, workspace, cpu, O, lse, status, max_ctas, stream):
-    """Both 8-bit attention calls: ``cpu`` is the (O, lse) partial to merge, or None."""
-    d = _here(q, "q")
-    fmt, n_slots = _pool8(K_pool, V_pool, P)
-    D, cap, dtype, rows = K_pool.shape[2], page_table.shape[-1], K_pool.dtype, B * Hq
-    odt = _BF16 if merge else _F32
-    if stream is None:
-        O = torch.empty((B, Hq, D), dtype=odt, device=q.device) if O is None else O
-        lse = torch.empty((B, Hq), dtype=_F32, device=q.device) if lse is None else lse
-    else:  # outputs made here come from the stream they are written on
-        with torch.cuda.stream(stream):
-            O = torch.empty((B, Hq, D), dtype=odt, device=q.device) if O is None else O
-            lse = torch.empty((B, Hq), dtype=_F32, device=q.device) if lse is None else lse
-    pool, units, wsb = n_slots * P * D, B * Hkv, workspace.numel()
-    head = (fmt, _sized(q, _BF16, rows * D, "q", d), _sized(K_pool, dtype, pool, "K_pool", d),
-            _sized(V_pool, dtype, pool, "V_pool", d), _sized(K_scale, _F32, n_slots, "K_scale", d),
-            _sized(V_scale, _F32, n_slots, "V_scale", d), n_slots, _sized(page_table, _I32, units * cap, "page_table", d),
-            _sized(seq_len, _I32, B, "seq_len", d), _sized(res_list, _I32, units * k, "res_list", d),
-            _sized(res_count, _I32, units, "res_count", d), B, Hq, Hkv, D, P, cap, k, scale)
-    tail = (_sized(O, odt, rows * D, "O", d), _sized(lse, _F32, rows, "lse", d), _sized(workspace, _U8, wsb, "workspace", d),
-            wsb, None if status is None else _sized(status, _I32, 1, "status", d),
-            None if max_ctas is None else _launch(max_ctas), _stream_on(stream, d))
-    if merge:
-        rc = lib().scout_sparse_attn8_merge(*head, _sized(cpu[0], _F32, rows * D, "O_cpu", d),
-                                            _sized(cpu[1], _F32, rows, "lse_cpu", d), *tail)
-    else:
-        rc = lib().scout_sparse_attn8(*head, *tail)
-    if rc != 0:
-        _check(rc, what)
-    return O, lse
-
-
 def sparse_attn8(q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq, Hkv, P, k, scale,
                  workspace, O=None, lse=None, status=None, max_ctas=None, stream=None):
     """Partial attention over the listed blocks of an 8-bit cache (float8 pools [n_slots][P][D], fp32
     scales [n_slots]) -> (O fp32 [B][Hq][D], lse fp32 [B][Hq])."""
-    return _attn8("scout_sparse_attn8", False, q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list,
-                  res_count, B, Hq, Hkv, P, k, scale, workspace, None, O, lse, status, max_ctas, stream)
+    return _native().sparse_attn8(q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq,
+                                  Hkv, P, k, scale, workspace, None, None, O, lse, status, max_ctas, stream)
 
 
 def sparse_attn8_merge(q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq, Hkv, P, k,
                        scale, workspace, O_cpu, lse_cpu, O_out=None, lse_out=None, status=None, max_ctas=None,
                        stream=None):
     """The same merged with the CPU partial -> (O bf16 [B][Hq][D], lse fp32 [B][Hq])."""
-    return _attn8("scout_sparse_attn8_merge", True, q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list,
-                  res_count, B, Hq, Hkv, P, k, scale, workspace, (O_cpu, lse_cpu), O_out, lse_out, status, max_ctas,
-                  stream)
+    if O_cpu is None or lse_cpu is None:
+        raise ScoutError("O_cpu and lse_cpu must be CUDA tensors")
+    return _native().sparse_attn8(q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq,
+                                  Hkv, P, k, scale, workspace, O_cpu, lse_cpu, O_out, lse_out, status, max_ctas, stream)
 
 
 def recall_async(ops, host_K, host_V, K_pool, V_pool, B, Hkv, P, nblk_cap, side_stream, wait_event=None,

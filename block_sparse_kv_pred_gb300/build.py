@@ -1,4 +1,4 @@
-"""Build libscout.so and libscoutgen.so in-tree with nvcc for sm_103a.
+"""Build libscout.so, libscoutgen.so and the native binding in-tree with nvcc for sm_103a.
 
     python -m block_sparse_kv_pred_gb300.build
 
@@ -12,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -27,6 +28,19 @@ LIBS = {
                      "cpu_attend.cpp")],
     "libscoutgen.so": [os.path.join(PKG, "workload", "gen.cu")],
 }
+# the native part of the Python binding: plain C++ against PyTorch's and Python's headers
+BINDING = os.path.join(PKG, "csrc", "binding.cpp")
+
+
+def _binding_flags() -> tuple[list[str], list[str]]:
+    import torch
+
+    t = os.path.dirname(os.path.abspath(torch.__file__))
+    inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_path("include"), os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    libs = ["-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-L" + PKG, "-lscout", "-Xlinker", "-rpath=$ORIGIN"]
+    return [f for d in inc for f in ("-I", d)], libs
 
 
 def nvcc() -> str:
@@ -54,12 +68,15 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> dict[str, st
     extra = list(extra or [])
     out = {}
     srcs = [s for v in LIBS.values() for s in v]
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        objs = dict(zip(srcs, ex.map(lambda s: _compile(s, extra), srcs)))
-    for name, lib_srcs in LIBS.items():
+    srcs.append(BINDING)
+    b_inc, b_libs = _binding_flags()
+    with cf.ThreadPoolExecutor(max_workers=min(16, len(srcs))) as ex:
+        objs = dict(zip(srcs, ex.map(lambda s: _compile(s, b_inc if s == BINDING else extra), srcs)))
+    for name, lib_srcs in [*LIBS.items(), ("_binding.so", [BINDING])]:
         target = lib_path(name)
         tmp = target + ".tmp"
-        cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *[objs[s] for s in lib_srcs], "-lcudart", "-Xcompiler", "-pthread"]
+        libs = b_libs if name == "_binding.so" else []
+        cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *[objs[s] for s in lib_srcs], *libs, "-lcudart", "-Xcompiler", "-pthread"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed for {name}:\n{r.stdout}\n{r.stderr}")

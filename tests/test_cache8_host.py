@@ -122,16 +122,83 @@ def test_binding_refuses_host_and_mismatched_tensors(L):
     x = torch.zeros((2, 32, 128), dtype=torch.float8_e4m3fn)
     with pytest.raises(bs.ScoutError, match="CUDA tensor"):
         bs.build_digest8("minmax", x, t, t, t, 1, 1, 32, t)
+    f = torch.zeros(2)  # scales
+    n = torch.ones(1, dtype=torch.int32)
+
+    def write(rows=torch.zeros((1, 2, 128), dtype=torch.bfloat16), K=x, V=x, table=torch.zeros((1, 2, 1), dtype=torch.int32),
+              scale=f, **kw):
+        bs.append_kv8(rows, rows, table, n, 1, 2, 32, K, V, scale, scale, **kw)
+
     with pytest.raises(bs.ScoutError, match="float8"):
-        bs._pool8(x.view(torch.uint8), None, 32)
+        write(K=x.view(torch.uint8))
     with pytest.raises(bs.ScoutError, match="alike"):
-        bs._pool8(x, x[:1], 32)
+        write(V=x[:1])
+    with pytest.raises(bs.ScoutError, match="alike"):
+        write(V=x.view(torch.float8_e5m2))
     with pytest.raises(bs.ScoutError, match="elements"):
-        bs._sized(t, torch.int32, 5, "x", -1)
+        write(scale=f[:1])
+    with pytest.raises(bs.ScoutError, match="elements, got 2 Double"):
+        write(scale=f.double())
+    with pytest.raises(bs.ScoutError, match="strided"):
+        write(scale=torch.zeros(4)[::2])
+    with pytest.raises(bs.ScoutError, match="CUDA tensor, got list"):
+        write(scale=[1.0, 1.0])
     with pytest.raises(bs.ScoutError, match="heads of a token"):
-        bs._rows(torch.zeros((3, 128, 2), dtype=torch.bfloat16).transpose(1, 2), 2, 128, "K_new", -1)
+        write(torch.zeros((3, 128, 2), dtype=torch.bfloat16).transpose(1, 2))
+    with pytest.raises(bs.ScoutError, match=r"\[n_tokens\]\[2\]\[128\]"):
+        write(torch.zeros((3, 3, 128), dtype=torch.bfloat16))
+    with pytest.raises(bs.ScoutError, match="K_pool must be a CUDA tensor on"):  # everything else fits
+        write()
     rows = torch.zeros((5, 3 * 128), dtype=torch.bfloat16)[:, 128:].view(5, 2, 128)  # heads contiguous, tokens strided
-    assert bs._rows(rows, 2, 128, "K_new", -1)[1] == 384
+    with pytest.raises(bs.ScoutError, match="K_pool must be a CUDA tensor on"):
+        write(rows)
+
+
+def test_binding_refuses_sizes_that_wrap(L):
+    """Products of sizes that pass 64 bits, and sizes that pass a C int, fit no tensor."""
+    t = torch.zeros(0, dtype=torch.int32)
+    with pytest.raises(bs.ScoutError, match="elements"):
+        bs.build_tables(t, None, 4, 1 << 30, 1 << 30, 32, t.view(0, 16), t)  # 2^64 elements, not 0
+    with pytest.raises(bs.ScoutError, match="32-bit"):
+        bs.build_tables(t, None, 4, 1 << 32, 1, 32, t, t)
+    with pytest.raises(TypeError):
+        bs.build_tables(t, None, 4, 1.5, 1, 32, t, t)
+
+
+def test_binding_attention_arguments(L):
+    """Host tensors that fit in everything but their place: each argument's own refusal comes first."""
+    B, Hq, Hkv, P, k, D, slots, cap = 2, 4, 2, 32, 3, 128, 5, 4
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    pool = torch.zeros((slots, P, D), dtype=torch.float8_e5m2)
+    good = [torch.zeros((B, Hq, D), dtype=torch.bfloat16), pool, pool.clone(), torch.zeros(slots), torch.zeros(slots),
+            i(B, Hkv, cap), i(B), i(B, Hkv, k), i(B, Hkv)]
+    names = ["q", "", "", "K_scale", "V_scale", "page_table", "seq_len", "res_list", "res_count"]
+    ws = torch.zeros(1 << 18, dtype=torch.uint8)
+    part = torch.zeros((B, Hq, D)), torch.zeros((B, Hq))
+
+    def run(t=good, ws=ws, part=None, **kw):
+        a = (*t, B, Hq, Hkv, P, k, D ** -0.5, ws)
+        return bs.sparse_attn8(*a, **kw) if part is None else bs.sparse_attn8_merge(*a, *part, **kw)
+
+    for p in (None, part):
+        with pytest.raises(bs.ScoutError, match="q must be a CUDA tensor on"):
+            run(part=p)
+        for at, name in enumerate(names):
+            with pytest.raises(bs.ScoutError, match=f"^{name}.*(elements|alike)"):
+                run([*good[:at], good[at][:1], *good[at + 1:]], part=p)
+        with pytest.raises(bs.ScoutError, match="workspace"):
+            run(ws=ws.int(), part=p)
+        with pytest.raises(bs.ScoutError, match="^O must be"):
+            run(part=p, **{"O" if p is None else "O_out": part[0][:1]})
+        with pytest.raises(bs.ScoutError, match="^lse must be"):
+            run(part=p, **{"lse" if p is None else "lse_out": part[1][:1]})
+        with pytest.raises(bs.ScoutError, match="status must be"):
+            run(part=p, status=i(2))
+    for at, name in enumerate(("O_cpu", "lse_cpu")):
+        with pytest.raises(bs.ScoutError, match=name):
+            run(part=[part[j][:1] if j == at else part[j] for j in (0, 1)])
+        with pytest.raises(bs.ScoutError, match=name):
+            run(part=[None if j == at else part[j] for j in (0, 1)])
 
 
 # ---------------------------------------------------------------------------

@@ -10,6 +10,9 @@ products, each off by at most 2^-23 A, and two fp32 products, so it is off by at
 es = 17 * 2^-23 A + 2^-22 A; the weights are off by 2 es (numerator and sum), 2^-20 (exp2, the split
 and the scales) and n 2^-24 (the running sums), all relative, against sum_t p_t |v_t|.  The bf16 result
 adds half a step of bf16, 2^-9 .. 2^-8 of the value."""
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -812,3 +815,62 @@ def test_calls_refuse_tensors_elsewhere_and_of_other_sizes():
     dg = torch.full((a.B, a.Hkv, a.cap, 2, D), 5.0, dtype=torch.bfloat16, device="cuda")
     bs.build_digest8("minmax", t[1], t[3], t[5], t[6], a.B, a.Hkv, a.P, dg, block_list=i32(np.zeros((0, 2))))
     assert (dg == 5.0).all()  # an empty list is no block, not every block
+
+
+def test_outputs_of_the_binding():
+    """Given outputs come back as the same objects, new ones belong to the call's stream and are freed with the
+    last reference; a refused call keeps nothing."""
+    a = Attn(24, B=2, Hkv=2, G=4, P=32, top=900, k=20)
+    t, ws = a.device(), a.workspace()
+    O_, l = torch.zeros((a.B, a.Hkv * a.G, D), device="cuda"), torch.zeros((a.B, a.Hkv * a.G), device="cuda")
+    r = bs.sparse_attn8(*t, ws, O=O_, lse=l)
+    assert r[0] is O_ and r[1] is l
+    a.check(O_, l)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for given in (s, None):
+        with torch.cuda.stream(s):  # named, and current
+            r = bs.sparse_attn8(*t, ws, stream=given)
+        torch.cuda.synchronize()
+        assert r[0].shape == O_.shape and r[0].dtype == torch.float32 and torch.equal(r[0], O_) and torch.equal(r[1], l)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = bs.sparse_attn8(*t, ws)  # outputs from the graph's pool
+    r[0].zero_(), r[1].zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(r[0], O_) and torch.equal(r[1], l)
+    refs, held = [sys.getrefcount(x) for x in (*t[:9], ws, O_, l)], torch.cuda.memory_allocated()
+    for _ in range(200):
+        bs.sparse_attn8(*t, ws)
+        bs.sparse_attn8(*t, ws, O=O_)
+        with pytest.raises(bs.ScoutError):
+            bs.sparse_attn8(*t, ws, O=O_[:1], lse=l)
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() == held and refs == [sys.getrefcount(x) for x in (*t[:9], ws, O_, l)]
+
+
+def test_calls_from_several_threads():
+    """Each thread with its own problem, workspace and stream, all calling at once."""
+    probs = [Attn(30 + i, B=1 + i, Hkv=2, G=4, P=32, top=900, k=20) for i in range(4)]
+    out, failed = [None] * 4, []
+    dev = [(a.device(), a.workspace(), torch.cuda.Stream()) for a in probs]
+    torch.cuda.synchronize()
+
+    def run(i):
+        try:
+            t, ws, s = dev[i]
+            for _ in range(100):
+                out[i] = bs.sparse_attn8(*t, ws, stream=s)
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for a, (O_, l) in zip(probs, out):
+        a.check(O_, l)
