@@ -170,6 +170,8 @@ int format_of(Args& a, const at::Tensor* t, const at::Tensor* v, int P) {
   }
   if (t->dim() != 3 || t->size(1) != P || (v != nullptr && (v->scalar_type() != s || v->sizes() != t->sizes())))
     a.fail("the pools must be [n_slots][%d][D] alike", P);
+  else if (t->size(2) != (int)t->size(2))
+    a.fail("a row of %lld elements does not fit a 32-bit size", (long long)t->size(2));
   return s == at::kFloat8_e4m3fn ? SCOUT_FP8_E4M3 : SCOUT_FP8_E5M2;
 }
 
@@ -247,7 +249,8 @@ PyObject* append_kv(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Args a(args, n, 9);
     const at::Tensor *kp = a.tensor("K_pool"), *vp = a.tensor("V_pool");
     const int Hkv = a.i32(), P = a.i32();
-    if (a.ok() && kp->dim() != 3) a.fail("K_pool must be a CUDA tensor [n_slots][%d][D]", P);
+    if (a.ok() && (kp->dim() != 3 || kp->size(2) != (int)kp->size(2)))
+      a.fail("K_pool must be a CUDA tensor [n_slots][%d][D]", P);
     if (!a.ok()) return nullptr;
     const int64_t slots = kp->size(0), D = kp->size(2), pool = count(slots, P, D);
     void *kpp = a.sized(kp, "K_pool", at::kBFloat16, pool), *vpp = a.sized(vp, "V_pool", at::kBFloat16, pool);

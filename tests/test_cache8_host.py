@@ -161,6 +161,11 @@ def test_binding_refuses_sizes_that_wrap(L):
         bs.build_tables(t, None, 4, 1 << 30, 1 << 30, 32, t.view(0, 16), t)  # 2^64 elements, not 0
     with pytest.raises(bs.ScoutError, match="32-bit"):
         bs.build_tables(t, None, 4, 1 << 32, 1, 32, t, t)
+    wide = torch.zeros((0, 32, (1 << 32) + 128), dtype=torch.uint8)  # 128 in 32 bits
+    with pytest.raises(bs.ScoutError, match="32-bit"):
+        bs.build_digest8("mean", wide.view(torch.float8_e5m2), t, t, t, 0, 1, 32, t)
+    with pytest.raises(bs.ScoutError, match=r"\[n_slots\]"):
+        bs.append_kv(t, t, t, 1, 32, wide, wide)
     with pytest.raises(TypeError):
         bs.build_tables(t, None, 4, 1.5, 1, 32, t, t)
 
