@@ -579,7 +579,8 @@ struct WarpStream {
     rslot = rj >= 0 ? a.page_table[(int64_t)ru * a.nblk_cap + rj] : -1;
   }
   __device__ __forceinline__ void resolve_tile() {
-    const int nv = rj >= 0 ? min(P, rlen - rj * P) : 0;
+    // in 64 bits: the table's columns may number more tokens than 32 bits do
+    const int nv = rj >= 0 ? (int)max((int64_t)0, min((int64_t)P, rlen - (int64_t)rj * P)) : 0;
     const bool fine = nv > 0 && rslot >= 0 && rslot < a.n_slots;
     if (!fine && rj != -1) report(a.status, SCOUT_DEV_BAD_INDEX);
     rnt = fine ? min(max(nv - rrow, 0), 16) : 0;

@@ -1,0 +1,43 @@
+"""The tables, cache writes and 8-bit cache at the ends of what they take: batches around a limit of the
+launch, calls without rows, tables wider than 32-bit token numbers, values that are not finite, counts
+outside their lists, failures of a wait and of an allocation, recalled blocks."""
+
+import pytest
+import torch
+
+import block_sparse_kv_pred_gb300 as bs
+from _parity import ensure_built
+from test_gpu_cache8 import Attn, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ensure_built()
+
+
+def word():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+# ---------------------------------------------------------------------------
+# tables wider than 2^31 tokens
+# ---------------------------------------------------------------------------
+def far_block(P):
+    """(columns, block): the block starts at token 2^31 + 2 P."""
+    j = (1 << 31) // P + 2
+    return j + 1, j
+
+
+@pytest.mark.parametrize("P", [32, 64])
+def test_attn8_blocks_past_32_bit_token_numbers_are_past_the_end(P):
+    a = Attn(50, B=1, Hkv=1, G=4, P=P, lens=[P], k=2)
+    a.lists[0, 0], a.counts[0, 0] = [0, -1], 1
+    cap, j = far_block(P)
+    t, st = list(a.device()), word()
+    t[5] = torch.full((1, 1, cap), int(a.table[0, 0, 0]), dtype=torch.int32, device="cuda")  # every entry names a slot
+    t[7], t[8] = i32([[[0, j]]]), i32([[2]])
+    O_, l = bs.sparse_attn8(*t, a.workspace(), status=st)
+    a.check(O_, l)
+    assert int(st) == 1
