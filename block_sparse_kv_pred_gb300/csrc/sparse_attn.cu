@@ -718,7 +718,9 @@ __global__ void __launch_bounds__(threads_of<NC>(), 1) sparse_attn_kernel(const 
     nt = 0;
     if (ru < 0) return;
     const int h = (warp + kConsumerWarps * kk) % C::kSub;
-    const int nv = rj >= 0 && rj < a.nblk_cap ? min(P, rlen - rj * P) : 0;
+    // in 64 bits: the table's columns may number more tokens than 32 bits do
+    const int nv =
+        rj >= 0 && rj < a.nblk_cap ? (int)max((int64_t)0, min((int64_t)P, rlen - (int64_t)rj * P)) : 0;
     if (nv <= 0 || sl < 0 || sl >= a.n_slots) {
       if (h == 0) report(a.status, SCOUT_DEV_BAD_INDEX);
       return;

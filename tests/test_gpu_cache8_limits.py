@@ -2,12 +2,13 @@
 launch, calls without rows, tables wider than 32-bit token numbers, values that are not finite, counts
 outside their lists, failures of a wait and of an allocation, recalled blocks."""
 
+import numpy as np
 import pytest
 import torch
 
 import block_sparse_kv_pred_gb300 as bs
 from _parity import ensure_built
-from test_gpu_cache8 import Attn, i32
+from test_gpu_cache8 import D, Attn, bf16_values, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +42,18 @@ def test_attn8_blocks_past_32_bit_token_numbers_are_past_the_end(P):
     O_, l = bs.sparse_attn8(*t, a.workspace(), status=st)
     a.check(O_, l)
     assert int(st) == 1
+
+
+@pytest.mark.parametrize("P", [32, 64])
+def test_attention_blocks_past_32_bit_token_numbers_are_past_the_end(P):
+    rng = np.random.default_rng(51)
+    q, K, V = (bf16_values(rng, s, outliers=False) for s in ((1, 4, D), (1, P, D), (1, P, D)))
+    cap, j = far_block(P)
+    table = torch.zeros((1, 1, cap), dtype=torch.int32, device="cuda")  # every entry names the only slot
+    ws, st = bs.sparse_attn_workspace(1, 4, 1, P), word()
+    O_, l = bs.sparse_attn(q.cuda(), K.cuda(), V.cuda(), table, i32([P]), i32([[[0, j]]]), i32([[2]]), 1, 4, 1, P, 2,
+                           D ** -0.5, ws, status=st)
+    s = q[0].double() @ K[0].double().T * D ** -0.5  # the block taken twice would raise the lse by log 2
+    assert int(st) == 1
+    assert ((l[0].cpu().double() - torch.logsumexp(s, 1)).abs() <= 2e-3).all()
+    assert ((O_[0].cpu().double() - torch.softmax(s, 1) @ V[0].double()).abs() <= 2e-3).all()
