@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kWarps * 32) digest_kernel(const __nv_bfloat16
   }
   const int b = (int)(u / Hkv);
   const int len = seq_len[b];
-  const int valid = min(P, len - (int)(j * P));
+  const int valid = (int)max((int64_t)0, min((int64_t)P, len - j * P));
   if (valid <= 0) return;  // block holds no tokens: left untouched
   const int32_t slot = page_table[u * nblk_cap + j];
   if (slot < 0 || slot >= n_slots) {

@@ -8,7 +8,7 @@ import torch
 
 import block_sparse_kv_pred_gb300 as bs
 from _parity import ensure_built
-from test_gpu_cache8 import D, Attn, bf16_values, i32
+from test_gpu_cache8 import D, Attn, bf16_values, i32, pool8
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +57,20 @@ def test_attention_blocks_past_32_bit_token_numbers_are_past_the_end(P):
     assert int(st) == 1
     assert ((l[0].cpu().double() - torch.logsumexp(s, 1)).abs() <= 2e-3).all()
     assert ((O_[0].cpu().double() - torch.softmax(s, 1) @ V[0].double()).abs() <= 2e-3).all()
+
+
+@pytest.mark.parametrize("kind", ["minmax", "mean"])
+def test_digests_of_blocks_past_32_bit_token_numbers_stay(kind):
+    P = 64
+    cap, j = far_block(P)
+    table = torch.zeros((1, 1, cap), dtype=torch.int32, device="cuda")
+    K, seq, lst = torch.ones((1, P, D), dtype=torch.bfloat16, device="cuda"), i32([P]), i32([[0, j], [0, 0]])
+    dg = (torch.empty((1, 1, cap, 2, D), dtype=torch.bfloat16, device="cuda") if kind == "minmax" else
+          torch.empty((1, 1, cap, D), device="cuda"))
+    for build in (lambda: bs.build_digest(kind, K, table, seq, 1, 1, P, dg, block_list=lst),
+                  lambda: bs.build_digest8(kind, pool8(np.full((1, P, D), 0x38, np.uint8), "e4m3"), torch.ones(1, device="cuda"),
+                                           table, seq, 1, 1, P, dg, block_list=lst)):
+        dg[0, 0, j] = 5.0
+        dg[0, 0, 0] = 5.0
+        build()
+        assert bool((dg[0, 0, j] == 5.0).all()) and bool((dg[0, 0, 0] == 1.0).all())
