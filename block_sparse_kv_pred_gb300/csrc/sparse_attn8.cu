@@ -285,11 +285,13 @@ __device__ __forceinline__ void tile_output(const uint4 (&v)[4], const float (&w
   }
 }
 
-// vs = f 2^e: e (at least -126, so that zero has f = 0), f through the result.
+// vs = f 2^e: e (at least -126, so that zero has f = 0), f through the result.  Infinities and NaN are
+// their own f, so that they are passed on.
 __device__ __forceinline__ float split_scale(float vs, float& e) {
   const int be = max((int)((__float_as_uint(vs) >> 23) & 0xffu), 1);
   e = (float)(be - 127);
-  return be <= 1 ? vs * 0x1p126f : __uint_as_float((__float_as_uint(vs) & 0x807fffffu) | 0x3f800000u);
+  const float f = __uint_as_float((__float_as_uint(vs) & 0x807fffffu) | 0x3f800000u);
+  return be <= 1 ? vs * 0x1p126f : be == 255 ? vs : f;
 }
 
 // 2^x, results below the normal range as zero (weights and probabilities are relative to 1)

@@ -381,7 +381,8 @@ int scout_append_kv(const void* K_new, int64_t ld_k, const void* V_new, int64_t 
  * A pool holds one byte per value, [n_slots][P][D], with one fp32 scale per slot (a block of
  * one KV head) in K_scale / V_scale [n_slots]: code c of slot s stands for c * scale[s].
  * Scales are finite and not negative; the writer below makes powers of two, the readers take
- * any.  The codes are one of two floating-point formats:
+ * any, and pass one that is not finite on to what they compute with it.  The codes are one of
+ * two floating-point formats:
  * ------------------------------------------------------------------------ */
 typedef enum scout_fp8 {
   SCOUT_FP8_E4M3 = 0, /* 4 exponent bits, 3 of significand, largest 448, no infinities */

@@ -8,7 +8,7 @@ import torch
 
 import block_sparse_kv_pred_gb300 as bs
 from _parity import ensure_built
-from test_gpu_cache8 import D, Attn, bf16_values, i32, pool8
+from test_gpu_cache8 import D, Attn, bf16_values, dev, i32, pool8
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +74,25 @@ def test_digests_of_blocks_past_32_bit_token_numbers_stay(kind):
         dg[0, 0, 0] = 5.0
         build()
         assert bool((dg[0, 0, j] == 5.0).all()) and bool((dg[0, 0, 0] == 1.0).all())
+
+
+# ---------------------------------------------------------------------------
+# values that are not finite, counts outside the lists
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("P", [16, 32])
+@pytest.mark.parametrize("split", [0, 1])
+def test_attn8_a_v_scale_that_is_not_finite_is_seen(bad, P, split):
+    # it spoils the output of its unit's heads and nothing else, their lse included
+    a = Attn(52, B=(2, 40)[split], Hkv=(2, 8)[split], G=3, P=P, lens=None if split == 0 else [200] * 40, top=600, k=12)
+    eO, el = a.expect()[:2]
+    assert a.counts[0, 0] > 0
+    a.vs[a.table[0, 0, a.lists[0, 0, 0]]] = bad
+    t, ws = a.device(), a.workspace()
+    O_, l = bs.sparse_attn8(*t, ws)
+    Om, lm = bs.sparse_attn8_merge(*t, ws, dev(np.zeros_like(a.O_cpu)), dev(np.full_like(a.lse_cpu, -np.inf)))
+    for o, s in ((O_, l), (Om, lm)):
+        assert not torch.isfinite(o[0, :3]).any()
+        assert np.isfinite(s[0, :3].cpu().numpy()).all() and np.abs(s[0, :3].cpu().numpy() - el[0, :3]).max() < 1e-4
+        rest = o.float().cpu().numpy().reshape(-1, D)[3:]
+        assert np.isfinite(rest).all() and np.abs(rest - eO.reshape(-1, D)[3:]).max() < 0.1
