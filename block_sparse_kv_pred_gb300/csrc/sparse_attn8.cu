@@ -114,6 +114,7 @@ struct Attn8Args {
   float* slot_O;      // [kMaxGrid8][2][kMaxG][kD] a CTA's pieces of units it shares with others
   float* piece_O;     // [kMaxGrid8][kNW][kMaxG][kD] a warp's first piece, while it goes on
   int32_t* status;
+  int inject;         // SCOUT_INJECT_* (tests)
 };
 
 // Steps (32 tokens) of a unit with n listed blocks.
@@ -557,7 +558,7 @@ struct WarpStream {
       : a(args), tmK(k), tmV(v), ring(sm + warp * (kHalves * kHalf)),
         tiles(reinterpret_cast<Tile*>(sm + kRingBytes8) + warp * (4 * kBatch)), full(bars + warp * kHalves), map(mp),
         lane(ln), wlo(lo), n_mine(n), off(lane_offsets(ln)), i(0), at(0), phase(0), n_issue(n), lost(-1),
-        trigger(n > kBatch ? 0 : 0x7fffffff), ru(0), rj(-1), rlen(0), rslot(-1), rrow(0), rnt(0), rks(0.f), rvs(0.f) {}
+        trigger(args.inject == SCOUT_INJECT_ABANDON ? min(1, n - 1) : n > kBatch ? 0 : 0x7fffffff), ru(0), rj(-1), rlen(0), rslot(-1), rrow(0), rnt(0), rks(0.f), rvs(0.f) {}
 
   // Tile 2 kBatch b + lane of this warp.
   __device__ __forceinline__ void resolve_entry(int batch) {
@@ -626,13 +627,23 @@ struct WarpStream {
   __device__ __forceinline__ bool landed(int h) {
     if (n_issue == 0) return false;
     if (__all_sync(0xffffffffu, mbar_wait(full + at, phase))) return true;
+    give_up(h);
+    return false;
+  }
+  // The wait for half h has run out: nothing more is issued or computed.
+  __device__ __forceinline__ void give_up(int h) {
     if (lane == 0) report(a.status, SCOUT_DEV_TIMEOUT);
     lost = h;
     n_issue = 0;
-    return false;
   }
-  // The next batch's resolution, in four parts while this batch runs.
+  // The next batch's resolution, in four parts while this batch runs.  (Under SCOUT_INJECT_ABANDON: what
+  // happens when the wait for this step's K runs out.)
   __device__ __forceinline__ void go_on() {
+    if (a.inject == SCOUT_INJECT_ABANDON) {
+      trigger = 0x7fffffff;
+      give_up(2 * i);
+      return;
+    }
     const int ib = i % kBatch, next = i / kBatch + 1;
     if (ib == 0) resolve_entry(next);
     if (ib == 4) resolve_slot();
@@ -707,6 +718,8 @@ struct WarpStream {
       st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], o);
       st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], o);
     }
+    // steps are missing from this state: as NaN it spoils its heads' results rather than pass for a sum
+    if (n_issue == 0) st.l[0] = st.l[1] = __uint_as_float(0x7fffffffu);
     float2* own = reinterpret_cast<float2*>(ring + was * kHalf);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -1352,7 +1365,9 @@ int attn8_entry(int fmt, const void* q, const void* K_pool, const void* V_pool, 
   if (!valid_fp8(fmt) || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || n_slots <= 0 || nblk_cap <= 0 || k <= 0 ||
       !(scale > 0.f))
     return SCOUT_ERR_INVALID_ARG;
-  if (launch != nullptr && launch->max_ctas < 0) return SCOUT_ERR_INVALID_ARG;
+  if (launch != nullptr && (launch->max_ctas < 0 || (launch->inject != SCOUT_INJECT_NONE &&
+                                                     launch->inject != SCOUT_INJECT_ABANDON)))
+    return SCOUT_ERR_INVALID_ARG;
   const int64_t units = (int64_t)B * Hkv;
   const int G = Hq / Hkv;
   if (D != kD || !valid_P(P) || G > kMaxG || units > kMaxUnits8 || !aligned16(K_pool) || !aligned16(V_pool) ||
@@ -1394,6 +1409,7 @@ int attn8_entry(int fmt, const void* q, const void* K_pool, const void* V_pool, 
   a.slot_O = reinterpret_cast<float*>(ws + kCounters8 + kSlotLse8);
   a.piece_O = reinterpret_cast<float*>(ws + kCounters8 + kSlotLse8 + kSlotO8);
   a.status = dev_status;
+  a.inject = launch != nullptr ? launch->inject : SCOUT_INJECT_NONE;
   return fmt == SCOUT_FP8_E4M3 ? attn8_by_P<SCOUT_FP8_E4M3>(P, a, launch, stream)
                                : attn8_by_P<SCOUT_FP8_E5M2>(P, a, launch, stream);
 }

@@ -111,12 +111,15 @@ typedef struct scout_launch {
 
 /* Values of scout_launch.inject.  They make a failure happen without faulting or hanging
  * the GPU, so that tests can check how it is reported and that it does no lasting harm.
- *   SCOUT_INJECT_ABANDON  scout_score_topk only: every CTA behaves as if a bounded wait of
+ *   SCOUT_INJECT_ABANDON  scout_score_topk: every CTA behaves as if a bounded wait of
  *     its copy-issuing warp had expired after its first unit: it reports SCOUT_DEV_TIMEOUT,
  *     hands out no further work, lets every copy it started land, and leaves the scoring
  *     warps to wait for a stage that never comes, under a short poll limit (a real bounded
  *     wait that expires).  The units it skipped keep stale lists.  The call still leaves
  *     its workspace counter at zero, so the next call on the same workspace is correct.
+ *     scout_sparse_attn8(_merge): every warp behaves as if its bounded wait for the K of its
+ *     second step (its only one's, if it has one) had expired: it reports SCOUT_DEV_TIMEOUT,
+ *     computes nothing more and lets every copy it started land.
  *   SCOUT_INJECT_COPY_FAIL  scout_recall_async and scout_recall_gather_async only: the
  *     call returns SCOUT_ERR_CUDA as if the CUDA runtime had refused a copy or the launch
  *     (scout_recall_async: its second run of copies, after the first was enqueued;
@@ -432,7 +435,8 @@ int scout_build_digest8(int kind, int fmt, const void* K_pool, const float* K_sc
  * split and early starts as theirs (it waits before its first global read).  The
  * probabilities keep about 22 bits and the queries all of theirs, so the fp32 outputs are
  * good to fp32 rounding.  Listed blocks outside the tables, the pool or the sequence are
- * skipped and SCOUT_DEV_BAD_INDEX set.  O_cpu of a head with lse_cpu = -inf is not used.
+ * skipped and SCOUT_DEV_BAD_INDEX set.  When a bounded wait expires, SCOUT_DEV_TIMEOUT is set and
+ * the heads of every unit with a block that was left out become NaN, O and lse.  O_cpu of a head with lse_cpu = -inf is not used.
  * workspace: scout_sparse_attn8_workspace_bytes() bytes (the same for every shape), 16-byte
  * aligned; its first 131072 bytes must be zero before the first use and are left zero by every
  * call.  One workspace serves calls of any shape, one after the other; calls that may overlap

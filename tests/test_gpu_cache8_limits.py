@@ -8,7 +8,7 @@ import torch
 
 import block_sparse_kv_pred_gb300 as bs
 from _parity import ensure_built
-from test_gpu_cache8 import D, Attn, bf16_values, dev, i32, pool8
+from test_gpu_cache8 import D, SPLITS, Attn, bf16_values, dev, i32, pool8
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +96,43 @@ def test_attn8_a_v_scale_that_is_not_finite_is_seen(bad, P, split):
         assert np.isfinite(s[0, :3].cpu().numpy()).all() and np.abs(s[0, :3].cpu().numpy() - el[0, :3]).max() < 1e-4
         rest = o.float().cpu().numpy().reshape(-1, D)[3:]
         assert np.isfinite(rest).all() and np.abs(rest - eO.reshape(-1, D)[3:]).max() < 0.1
+
+
+# ---------------------------------------------------------------------------
+# failures
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("merge", [False, True])
+@pytest.mark.parametrize("split", range(4))
+def test_attn8_an_expired_wait_is_reported_and_spoils_its_units_alone(split, merge):
+    # every warp gives up at its second step: what it left out shows as NaN, what was done before is right, and the
+    # next call on the same workspace is right
+    a = Attn(56, **SPLITS[split])
+    t, ws, st = a.device(), a.workspace(), word()
+    Hq = a.Hkv * a.G
+    cpu = (dev(a.O_cpu), dev(a.lse_cpu)) if merge else ()
+    O_ = torch.zeros((a.B, Hq, D), dtype=torch.bfloat16 if merge else torch.float32, device="cuda")
+    l = torch.zeros((a.B, Hq), device="cuda")
+
+    def call(inject):
+        p = [x.data_ptr() for x in t[:9]]
+        bs.Prepared("scout_sparse_attn8_merge" if merge else "scout_sparse_attn8", 0, *p[:5], a.n_slots, *p[5:], a.B, Hq, a.Hkv,
+                    D, a.P, a.cap, a.k, a.scale, *[x.data_ptr() for x in cpu], O_.data_ptr(), l.data_ptr(), ws.data_ptr(),
+                    ws.numel(), st.data_ptr(), bs._launch(None, inject=inject), torch.cuda.current_stream().cuda_stream)()
+        torch.cuda.synchronize()
+        return O_.clone(), l.clone()
+
+    good = call(bs.INJECT_NONE)
+    a.check(*good, merged=merge)
+    assert int(st) == 0
+    bad = call(bs.INJECT_ABANDON)
+    assert int(st) == 2 and not ws[:131072].any()
+    lost = torch.isnan(bad[1])
+    assert lost.any() and torch.equal(torch.isnan(bad[0]), lost[..., None].expand(-1, -1, D))
+    units = lost.view(-1, a.G)
+    assert torch.equal(units.all(1), units.any(1))  # all heads of a unit alike
+    assert not units[torch.from_numpy(a.counts.flatten() == 0)].any()
+    assert torch.equal(bad[0][~lost], good[0][~lost]) and torch.equal(bad[1][~lost], good[1][~lost])
+    again = call(bs.INJECT_NONE)
+    assert torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
+    with pytest.raises(bs.ScoutError, match="INVALID_ARG"):
+        call(bs.INJECT_COPY_FAIL)
