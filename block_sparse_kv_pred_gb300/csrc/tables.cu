@@ -19,6 +19,7 @@ namespace scout {
 namespace {
 
 constexpr int kTabWarps = 8;
+constexpr int kTabPartials = 3 * 32;  // ints of static shared memory, for the prefixes
 
 struct TabArgs {
   const int32_t* prev_len;
@@ -61,7 +62,7 @@ __device__ __forceinline__ int checked(const TabArgs& a, bool has, int s) {
 
 __global__ void __launch_bounds__(kTabWarps * 32) tables_kernel(const TabArgs a) {
   extern __shared__ int sm[];
-  __shared__ int partial[3 * 32];
+  __shared__ int partial[kTabPartials];
   const int B = a.B, P = a.P;
   int* tok = sm;              // [B + 1] new tokens before sequence b
   int* tou = sm + (B + 1);    // [B + 1] touched blocks (of one KV head)
@@ -291,9 +292,11 @@ extern "C" int scout_build_tables(const int32_t* prev_len, const int32_t* seq_le
   const int64_t want = (warps + kTabWarps - 1) / kTabWarps;
   const int grid = (int)(want < sm_count() * kTabPerSm ? want : sm_count() * kTabPerSm);
   const size_t smem = (size_t)(5 * B + 3) * sizeof(int);
-  // (the same limit for every call: calls on several host threads do not lower it for one another)
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (5 * kMaxBatch + 3) * (int)sizeof(int)) != cudaSuccess)
+  // More than 48 KB, the static part included, has to be asked for.  (The same limit for every call: calls
+  // on several host threads do not lower it for one another.)
+  if (smem + kTabPartials * sizeof(int) > 48 * 1024 &&
+      cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (5 * kMaxBatch + 3) * (int)sizeof(int)) != cudaSuccess)
     return SCOUT_ERR_CUDA;
   tables_kernel<<<grid, kTabWarps * 32, smem, stream>>>(a);
   return launch_status();

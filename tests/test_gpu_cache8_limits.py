@@ -1,6 +1,9 @@
 """The tables, cache writes and 8-bit cache at the ends of what they take: batches around a limit of the
 launch, calls without rows, tables wider than 32-bit token numbers, values that are not finite, counts
 outside their lists, failures of a wait and of an allocation, recalled blocks."""
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -11,6 +14,7 @@ from _parity import ensure_built
 from test_gpu_cache8 import D, SPLITS, Attn, bf16_values, dev, i32, pool8
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -20,6 +24,27 @@ def _built():
 
 def word():
     return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+# ---------------------------------------------------------------------------
+# build_tables
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("B", [2437, 2438, 2457, 2458])
+def test_tables_of_batches_around_48_kb_of_shared_memory(B):
+    # (5 B + 3) * 4 bytes and the kernel's own 384 pass 48 KB from 2,438 sequences on; in a process of its own,
+    # as a call with a larger batch would raise the kernel's limit for those after it
+    text = f"""
+import torch, block_sparse_kv_pred_gb300 as bs
+n = torch.arange({B}, dtype=torch.int32, device="cuda") % 3
+t = torch.full(({B}, 1, 1), -7, dtype=torch.int32, device="cuda")
+w, cu = torch.full_like(t, -7), torch.zeros({B} + 1, dtype=torch.int32, device="cuda")
+bs.build_tables(n, None, {B}, {B}, 1, 16, t, w, cu_tokens=cu)
+has = n > 0
+assert torch.equal(t.flatten()[has].long(), torch.arange(int(has.sum()), device="cuda")) and bool((t.flatten()[~has] == -1).all())
+assert torch.equal(w.flatten(), has.int()) and torch.equal(cu[1:].long(), n.long().cumsum(0)) and cu[0] == 0
+"""
+    r = subprocess.run([sys.executable, "-c", text], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 # ---------------------------------------------------------------------------
