@@ -113,6 +113,13 @@ class Args {
     const at::Tensor* t = optional(name);
     return t == nullptr ? nullptr : sized(t, name, type, numel);
   }
+  // An output with room for `rows` rows, or None.  One without room has no address of its own but is still
+  // asked for: it gets one that nothing is written to, so that what does not fit is reported.
+  void* room(const at::Tensor* t, const char* name, at::ScalarType type, int rows, int64_t width) {
+    if (t == nullptr) return nullptr;
+    void* p = sized(t, name, type, count(rows, width));
+    return rows == 0 ? reinterpret_cast<void*>(kNowhere) : p;
+  }
   // rows [n_tokens][Hkv][D], each token's heads contiguous; ld: elements from a token to the next
   void* rows(const char* name, int Hkv, int64_t D, int64_t* n, int64_t* ld) {
     const at::Tensor* t = tensor(name);
@@ -153,6 +160,7 @@ class Args {
 
  private:
   static constexpr int kNone = -2;
+  static constexpr uintptr_t kNowhere = 256;
   PyObject* const* at_;
   PyObject* const* end_;
   int device_ = kNone;                // of the first tensor
@@ -225,10 +233,10 @@ PyObject* build_tables(PyObject*, PyObject* const* args, Py_ssize_t n) {
     auto cu = static_cast<int32_t*>(a.optional("cu_tokens", at::kInt, (int64_t)B + 1));
     const at::Tensor* map = a.optional("slot_map");
     const int max_tokens = first_size(a, map, "slot_map");
-    auto map_p = static_cast<int64_t*>(map != nullptr ? a.sized(map, "slot_map", at::kLong, count(max_tokens, Hkv)) : nullptr);
+    auto map_p = static_cast<int64_t*>(a.room(map, "slot_map", at::kLong, max_tokens, Hkv));
     const at::Tensor* list = a.optional("block_list");
     const int max_list = first_size(a, list, "block_list");
-    auto list_p = static_cast<int32_t*>(list != nullptr ? a.sized(list, "block_list", at::kInt, count(max_list, 2)) : nullptr);
+    auto list_p = static_cast<int32_t*>(a.room(list, "block_list", at::kInt, max_list, 2));
     auto counts = static_cast<int32_t*>(a.optional("counts", at::kInt, 3));
     auto status = static_cast<int32_t*>(a.optional("status", at::kInt, 1));
     const cudaStream_t st = a.stream();

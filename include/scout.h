@@ -341,10 +341,10 @@ int scout_merge(const float* O_a, const float* lse_a, const float* O_b, const fl
  * resident_bits uint32 [B][Hkv][ceil(nblk_cap/32)]: the new blocks' bits set (cleared where no
  *              slot was left); without prev_len the words are written whole.
  * cu_tokens    int32 [B + 1]: new tokens before sequence b (rows of the packed new K/V), or NULL
- * slot_map     int64 [max_tokens][Hkv], or NULL: pool row (slot * P + t % P) of every new
+ * slot_map     int64 [max_tokens][Hkv], or NULL (not wanted): pool row (slot * P + t % P) of every new
  *              token and KV head; -1 where it has no slot, and in the rows past the last
  *              new token (a padded batch's rows).
- * block_list   int32 [max_list][2], or NULL: the touched blocks as (unit, block) pairs in
+ * block_list   int32 [max_list][2], or NULL (not wanted): the touched blocks as (unit, block) pairs in
  *              (b, kvh, j) order, as the digest builders take them; then (-1, -1).
  * counts       int32 [3], or NULL: new tokens, touched blocks (of all KV heads), new blocks.
  * dev_status   may be NULL.  SCOUT_DEV_OVERFLOW: more new blocks than n_free (their entries

@@ -47,6 +47,18 @@ assert torch.equal(w.flatten(), has.int()) and torch.equal(cu[1:].long(), n.long
     assert r.returncode == 0, r.stderr[-2000:]
 
 
+@pytest.mark.parametrize("which", ["slot_map", "block_list"])
+def test_tables_with_an_empty_map_or_list(which):
+    # asked for, with no room: what does not fit is reported, as with too little room
+    kw = {"slot_map": torch.empty((0, 2), dtype=torch.int64, device="cuda"),
+          "block_list": torch.empty((0, 2), dtype=torch.int32, device="cuda")}
+    for n, want in ((5, 4), (0, 0)):
+        st, t = word(), torch.full((1, 2, 2), -7, dtype=torch.int32, device="cuda")
+        bs.build_tables(i32([n]), None, 4, 1, 2, 16, t, torch.zeros((1, 2, 1), dtype=torch.int32, device="cuda"),
+                        status=st, **{which: kw[which]})
+        assert int(st) == want and t.flatten().tolist() == ([0, -1, 1, -1] if n else [-1] * 4)
+
+
 # ---------------------------------------------------------------------------
 # tables wider than 2^31 tokens
 # ---------------------------------------------------------------------------
