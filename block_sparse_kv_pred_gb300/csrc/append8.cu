@@ -103,8 +103,9 @@ __global__ void __launch_bounds__(kA8Warps * 32) append8_kernel(const App8Args a
       const int r = 2 * i + half;
       v[i] = r >= r0 && r < r1 && rows_ok ? ldg_stream(src + (int64_t)r * ld) : make_uint4(0u, 0u, 0u, 0u);
     }
-    if (slot < 0 || slot >= a.n_slots || !rows_ok) {
+    if (!rows_ok || slot < 0 || slot >= a.n_slots) {
       if (lane == 0) report(a.status, SCOUT_DEV_BAD_INDEX);
+      if (!rows_ok) break;  // the rows are packed: those of the items that follow end no earlier
       continue;
     }
     uint8_t* page = (is_v ? a.V_pool : a.K_pool) + (int64_t)slot * (P * kD) + chunk * 8;
@@ -174,7 +175,7 @@ extern "C" int scout_append_kv8(int fmt, const void* K_new, int64_t ld_k, const 
                                 void* V_pool, float* K_scale, float* V_scale, int64_t n_slots, int32_t* dev_status,
                                 cudaStream_t stream) {
   using namespace scout;
-  if (K_new == nullptr || V_new == nullptr || seq_len == nullptr || page_table == nullptr || K_pool == nullptr ||
+  if ((n_tokens > 0 && (K_new == nullptr || V_new == nullptr)) || seq_len == nullptr || page_table == nullptr || K_pool == nullptr ||
       V_pool == nullptr || K_scale == nullptr || V_scale == nullptr)
     return SCOUT_ERR_INVALID_ARG;
   if (!valid_fp8(fmt) || n_tokens < 0 || B <= 0 || Hkv <= 0 || nblk_cap <= 0 || n_slots <= 0 ||
@@ -184,7 +185,7 @@ extern "C" int scout_append_kv8(int fmt, const void* K_new, int64_t ld_k, const 
       (int64_t)B * nblk_cap * P > 0x7fffffffLL || (int64_t)B * Hkv * nblk_cap > 0x7fffffffLL || ld_k % 8 != 0 || ld_v % 8 != 0 || !aligned16(K_new) ||
       !aligned16(V_new) || !aligned16(K_pool) || !aligned16(V_pool))
     return SCOUT_ERR_UNSUPPORTED;
-  if (n_tokens == 0) return SCOUT_OK;
+  if (n_tokens == 0 && dev_status == nullptr) return SCOUT_OK;  // no rows, and nowhere to say that some were due
   App8Args a;
   a.K = static_cast<const __nv_bfloat16*>(K_new);
   a.V = static_cast<const __nv_bfloat16*>(V_new);
@@ -205,7 +206,7 @@ extern "C" int scout_append_kv8(int fmt, const void* K_new, int64_t ld_k, const 
   a.status = dev_status;
   // at most n_tokens / P + 2 B blocks of a head are touched (each span's two ends partly)
   const int64_t warps = ((int64_t)n_tokens / P + 2 * (int64_t)(B < n_tokens ? B : n_tokens)) * Hkv * 2;
-  const int64_t want = (warps + kA8Warps - 1) / kA8Warps;
+  const int64_t want = (warps + kA8Warps - 1) / kA8Warps + (n_tokens == 0);  // (without rows: the report alone)
   const int grid = (int)(want < sm_count() * 8 ? want : sm_count() * 8);
   const size_t smem = (size_t)(2 * B + 2) * sizeof(int);
   return fmt == SCOUT_FP8_E4M3 ? dispatch_append8<SCOUT_FP8_E4M3>(P, a, grid, smem, stream)

@@ -265,11 +265,11 @@ PyObject* append_kv(PyObject*, PyObject* const* args, Py_ssize_t n) {
     int64_t nk = 0, nv = 0, ld_k = 0, ld_v = 0;
     void *k = a.rows("K_new", Hkv, D, &nk, &ld_k), *v = a.rows("V_new", Hkv, D, &nv, &ld_v);
     if (nk != nv) a.fail("K_new and V_new must hold the same tokens");
-    if (a.ok() && nk == 0) return a.settle() ? Py_NewRef(Py_None) : nullptr;
     auto map = static_cast<const int64_t*>(a.sized("slot_map", at::kLong, count(nk, Hkv)));
     auto status = static_cast<int32_t*>(a.optional("status", at::kInt, 1));
     const cudaStream_t st = a.stream();
     if (!a.ok()) return nullptr;
+    if (nk == 0) Py_RETURN_NONE;
     int rc;
     Py_BEGIN_ALLOW_THREADS;
     rc = scout_append_kv(k, ld_k, v, ld_v, map, (int)nk, Hkv, (int)D, P, kpp, vpp, slots, status, st);
@@ -293,7 +293,6 @@ PyObject* append_kv8(PyObject*, PyObject* const* args, Py_ssize_t n) {
     int64_t nk = 0, nv = 0, ld_k = 0, ld_v = 0;
     void *k = a.rows("K_new", Hkv, D, &nk, &ld_k), *v = a.rows("V_new", Hkv, D, &nv, &ld_v);
     if (nk != nv) a.fail("K_new and V_new must hold the same tokens");
-    if (a.ok() && nk == 0) return a.settle() ? Py_NewRef(Py_None) : nullptr;
     const at::Tensor* pt = a.tensor("page_table");
     const int cap = last_size(a, pt, "page_table");
     auto pt_p = static_cast<const int32_t*>(a.sized(pt, "page_table", at::kInt, count(B, Hkv, cap)));

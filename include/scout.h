@@ -410,6 +410,7 @@ typedef enum scout_fp8 {
  * dev_status (may be NULL): SCOUT_DEV_BAD_INDEX for a touched block whose slot is not in the
  * pool or whose rows are not in K_new (it is skipped), a negative length or prev_len above
  * seq_len (no new tokens); SCOUT_DEV_OVERFLOW for a length above nblk_cap * P (it counts as that).
+ * With n_tokens 0, K_new and V_new may be NULL and all a call does is report.
  * No workspace.  Requires B <= 4096, nblk_cap <= 8192, B * nblk_cap * max(P, Hkv) < 2^31, n_slots < 2^31,
  * ld >= Hkv * D, ld % 8 == 0, and 16-byte aligned rows and pools. */
 int scout_append_kv8(int fmt, const void* K_new, int64_t ld_k, const void* V_new, int64_t ld_v, int n_tokens,

@@ -1,0 +1,36 @@
+"""What the native binding of the tables, writes and 8-bit calls refuses and reports, without a GPU."""
+import pytest
+import torch
+
+import block_sparse_kv_pred_gb300 as bs
+from _parity import ensure_built
+
+D = 128
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ensure_built()
+
+
+def test_writes_without_rows_check_everything_else():
+    rows = torch.zeros((0, 2, D), dtype=torch.bfloat16)
+    pool, plain = torch.zeros((3, 32, D), dtype=torch.float8_e5m2), torch.zeros((3, 32, D), dtype=torch.bfloat16)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    good = {"page_table": i(1, 2, 4), "seq_len": i(1), "K_scale": torch.zeros(3), "V_scale": torch.zeros(3),
+            "prev_len": i(1), "status": i(1)}
+
+    def write8(**kw):
+        v = {**good, **kw}
+        bs.append_kv8(rows, rows, v["page_table"], v["seq_len"], 1, 2, 32, pool, pool, v["K_scale"], v["V_scale"],
+                      prev_len=v["prev_len"], status=v["status"])
+
+    for name in good:
+        with pytest.raises(bs.ScoutError, match=f"^{name} must be a contiguous"):
+            write8(**{name: good[name].double()})
+    with pytest.raises(bs.ScoutError, match="K_pool must be a CUDA tensor on"):  # everything else fits
+        write8()
+    for name, kw in (("slot_map", {"slot_map": i(0, 2)}), ("status", {"status": i(2)}), ("K_pool", {})):
+        with pytest.raises(bs.ScoutError, match=f"^{name} must be a"):
+            bs.append_kv(rows, rows, **{"slot_map": torch.zeros((0, 2), dtype=torch.int64), "Hkv": 2, "P": 32,
+                                        "K_pool": plain, "V_pool": plain, **kw})

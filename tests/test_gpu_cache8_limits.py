@@ -10,8 +10,9 @@ import pytest
 import torch
 
 import block_sparse_kv_pred_gb300 as bs
+from oracle import cache8_oracle as C8
 from _parity import ensure_built
-from test_gpu_cache8 import D, SPLITS, Attn, bf16_values, dev, i32, pool8
+from test_gpu_cache8 import D, SPLITS, Attn, bf16_values, codes_of, dev, finite_codes, i32, make_tables, pool8
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -57,6 +58,66 @@ def test_tables_with_an_empty_map_or_list(which):
         bs.build_tables(i32([n]), None, 4, 1, 2, 16, t, torch.zeros((1, 2, 1), dtype=torch.int32, device="cuda"),
                         status=st, **{which: kw[which]})
         assert int(st) == want and t.flatten().tolist() == ([0, -1, 1, -1] if n else [-1] * 4)
+
+
+# ---------------------------------------------------------------------------
+# append_kv8
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("prev,seq,want", [(None, [40, 0], 1), ([8, 3], [8, 3], 0), ([8, 3], [8, 4], 1), (None, [0, 97], 5),
+                                           (None, [0, -1], 1), ([8, 4], [8, 3], 1), (None, [0, 0], 0)])
+def test_append8_without_rows_reports_what_the_lengths_say(prev, seq, want):
+    Hkv, P, n_slots = 2, 32, 20
+    pools = [pool8(np.full((n_slots, P, D), 0x31, np.uint8), "e4m3") for _ in range(2)]
+    sc = [torch.full((n_slots,), 0.5, device="cuda") for _ in range(2)]
+    table, st = i32(np.arange(2 * Hkv * 3).reshape(2, Hkv, 3)), word()
+    none = torch.empty((0, Hkv, D), dtype=torch.bfloat16, device="cuda")
+    bs.append_kv8(none, none, table, i32(seq), 2, Hkv, P, *pools, *sc, prev_len=None if prev is None else i32(prev),
+                  status=st)
+    assert int(st) == want
+    assert all((codes_of(p) == 0x31).all() for p in pools) and all(bool((s == 0.5).all()) for s in sc)
+
+
+@pytest.mark.parametrize("n", [1, 70, 1000])
+def test_append8_stops_where_the_rows_end(n):
+    # lengths that say far more than there are rows: the blocks whose rows are all there, and no others
+    rng = np.random.default_rng(n)
+    B, Hkv, P, cap, n_slots = 30, 2, 16, 200, 30 * 2 * 200
+    seq = rng.integers(20, 60, B)
+    seq[20:] = cap * P
+    table = rng.permutation(n_slots).reshape(B, Hkv, cap)
+    x = bf16_values(rng, (n, Hkv, D))
+    codes = np.full((n_slots, P, D), 0x31, np.uint8)
+    pools, sc, st = [pool8(codes, "e4m3") for _ in range(2)], [torch.ones(n_slots, device="cuda") for _ in range(2)], word()
+    bs.append_kv8(x.cuda(), x.cuda(), i32(table), i32(seq), B, Hkv, P, *pools, *sc, status=st)
+    # the oracle with the lengths cut to whole blocks that lie within the rows
+    cut, at = np.zeros(B, int), 0
+    for b in range(B):
+        left = n - at
+        cut[b] = seq[b] if left >= seq[b] else max(left, 0) // P * P
+        at += int(seq[b])
+    have = x.double().numpy()[: int(cut.sum())]
+    ec, es = C8.append8(have, None, cut, table, codes, np.ones(n_slots), "e4m3", P)
+    assert int(st) == 1
+    for p, s in zip(pools, sc):
+        assert np.array_equal(codes_of(p), ec) and np.array_equal(s.cpu().numpy(), es)
+
+
+def test_append8_of_the_largest_batch_with_padding_rows():
+    rng = np.random.default_rng(2)
+    B, P, cap = 4096, 16, 3
+    prev = rng.integers(0, 30, B)
+    seq = prev + rng.integers(0, 4, B)
+    table, n_slots = make_tables(rng, seq, 1, P, cap)
+    n = int((seq - prev).sum())
+    x = bf16_values(rng, (n + 100, 1, D))
+    x[n:] = float("nan")  # rows of a padded batch, past the last new token
+    codes, scales = finite_codes(rng, (n_slots, P, D), "e5m2"), 2.0 ** rng.integers(-20, -10, n_slots)
+    pools, sc, st = [pool8(codes, "e5m2") for _ in range(2)], [dev(scales.astype(np.float32)) for _ in range(2)], word()
+    bs.append_kv8(x.cuda(), x.cuda(), i32(table), i32(seq), B, 1, P, *pools, *sc, prev_len=i32(prev), status=st)
+    ec, es = C8.append8(x.double().numpy()[:n], prev, seq, table, codes, scales, "e5m2", P)
+    assert int(st) == 0
+    for p, s in zip(pools, sc):
+        assert np.array_equal(codes_of(p), ec) and np.array_equal(s.cpu().numpy(), es.astype(np.float32))
 
 
 # ---------------------------------------------------------------------------
