@@ -333,7 +333,7 @@ def _native():
         except ImportError as e:
             raise ScoutError(f"_binding.so is missing or does not load ({e}): "
                              "run `python -m block_sparse_kv_pred_gb300.build`") from e
-        _binding.set_error(ScoutError)
+        _binding.set_errors(ScoutError, torch.OutOfMemoryError)
         _NATIVE = _binding
     return _NATIVE
 

@@ -10,6 +10,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/util/Exception.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -18,7 +19,8 @@
 
 namespace {
 
-PyObject* g_error = nullptr;  // ScoutError
+PyObject* g_error = nullptr;   // ScoutError
+PyObject* g_memory = nullptr;  // torch.OutOfMemoryError
 
 // The product of sizes; -1, which no tensor has, when it passes 64 bits.
 template <class... A>
@@ -204,11 +206,14 @@ PyObject* done(int rc, const char* what) {
   return nullptr;
 }
 
-// Runs f, with C++ exceptions (an allocation that fails) as Python errors.
+// Runs f, with C++ exceptions as Python errors: an allocation that fails as PyTorch's own calls raise it.
 template <class F>
 PyObject* guarded(F f) {
   try {
     return f();
+  } catch (const c10::OutOfMemoryError& e) {
+    PyErr_SetString(g_memory, e.what_without_backtrace());
+    return nullptr;
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
     return nullptr;
@@ -423,9 +428,14 @@ PyObject* sparse_attn8(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-PyObject* set_error(PyObject*, PyObject* cls) {
-  Py_INCREF(cls);
-  Py_XSETREF(g_error, cls);
+// (ScoutError, torch.OutOfMemoryError)
+PyObject* set_errors(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 2) {
+    PyErr_SetString(PyExc_TypeError, "2 arguments expected");
+    return nullptr;
+  }
+  Py_XSETREF(g_error, Py_NewRef(args[0]));
+  Py_XSETREF(g_memory, Py_NewRef(args[1]));
   Py_RETURN_NONE;
 }
 
@@ -438,7 +448,7 @@ PyMethodDef g_methods[] = {{"build_tables", fast(build_tables), METH_FASTCALL, n
                            {"append_kv8", fast(append_kv8), METH_FASTCALL, nullptr},
                            {"build_digest8", fast(build_digest8), METH_FASTCALL, nullptr},
                            {"sparse_attn8", fast(sparse_attn8), METH_FASTCALL, nullptr},
-                           {"set_error", set_error, METH_O, nullptr},
+                           {"set_errors", fast(set_errors), METH_FASTCALL, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

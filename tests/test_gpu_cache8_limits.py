@@ -234,3 +234,23 @@ def test_attn8_an_expired_wait_is_reported_and_spoils_its_units_alone(split, mer
     assert torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
     with pytest.raises(bs.ScoutError, match="INVALID_ARG"):
         call(bs.INJECT_COPY_FAIL)
+
+
+def test_outputs_that_do_not_fit_raise_torch_out_of_memory():
+    # no memory is filled: the process's share is set below what it holds, so that the allocator refuses
+    a = Attn(54, B=256, Hkv=8, G=2, P=16, lens=[20] * 256, k=2)
+    t, ws = a.device(), a.workspace()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = []
+    try:
+        torch.cuda.set_per_process_memory_fraction(1e-6)
+        with pytest.raises(torch.OutOfMemoryError):
+            while True:  # ends when the cached blocks are used up: what is left is smaller than the 2 MB output
+                held.append(torch.empty((1 << 20) + 1, dtype=torch.uint8, device="cuda"))
+        with pytest.raises(torch.OutOfMemoryError):
+            bs.sparse_attn8(*t, ws)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+        del held
+    a.check(*bs.sparse_attn8(*t, ws))
