@@ -24,8 +24,8 @@ SCORE_REL = 1e-4
 
 
 def ensure_built():
-    if not (os.path.exists(bs.lib_path()) and os.path.exists(os.path.join(os.path.dirname(bs.lib_path()),
-                                                                          "libscoutgen.so"))):
+    at = os.path.dirname(bs.lib_path())
+    if not all(os.path.exists(os.path.join(at, n)) for n in ("libscout.so", "libscoutgen.so", "_binding.so")):
         B.build()
 
 

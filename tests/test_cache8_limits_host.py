@@ -1,8 +1,11 @@
 """What the native binding of the tables, writes and 8-bit calls refuses and reports, without a GPU."""
+import os
+
 import pytest
 import torch
 
 import block_sparse_kv_pred_gb300 as bs
+from block_sparse_kv_pred_gb300 import build as B
 from _parity import ensure_built
 
 D = 128
@@ -34,3 +37,15 @@ def test_writes_without_rows_check_everything_else():
         with pytest.raises(bs.ScoutError, match=f"^{name} must be a"):
             bs.append_kv(rows, rows, **{"slot_map": torch.zeros((0, 2), dtype=torch.int64), "Hkv": 2, "P": 32,
                                         "K_pool": plain, "V_pool": plain, **kw})
+
+
+@pytest.mark.parametrize("missing", ["libscout.so", "libscoutgen.so", "_binding.so", None])
+def test_a_tree_without_one_of_the_built_files_is_built(missing, monkeypatch, tmp_path):
+    for n in ("libscout.so", "libscoutgen.so", "_binding.so"):
+        if n != missing:
+            (tmp_path / n).touch()
+    built = []
+    monkeypatch.setattr(bs, "lib_path", lambda: os.path.join(tmp_path, "libscout.so"))
+    monkeypatch.setattr(B, "build", lambda: built.append(True))
+    ensure_built()
+    assert bool(built) == (missing is not None)
