@@ -63,26 +63,38 @@ def lib_path(name: str) -> str:
     return os.path.join(PKG, name)
 
 
+def _link(name: str, objs: list[str], libs: list[str]) -> str:
+    target = lib_path(name)
+    tmp = target + ".tmp"
+    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, *libs, "-lcudart", "-Xcompiler", "-pthread"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed for {name}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, target)
+    return target
+
+
+def _binding_object() -> tuple[str, list[str]]:
+    flags, libs = _binding_flags()
+    return _compile(BINDING, flags), libs
+
+
 def build(verbose: bool = False, extra: list[str] | None = None) -> dict[str, str]:
+    """The libraries, then the native binding: where PyTorch's headers are missing, or do not fit, it raises
+    with the libraries in place."""
     os.makedirs(BUILD, exist_ok=True)
     extra = list(extra or [])
     out = {}
     srcs = [s for v in LIBS.values() for s in v]
-    srcs.append(BINDING)
-    b_inc, b_libs = _binding_flags()
-    with cf.ThreadPoolExecutor(max_workers=min(16, len(srcs))) as ex:
-        objs = dict(zip(srcs, ex.map(lambda s: _compile(s, b_inc if s == BINDING else extra), srcs)))
-    for name, lib_srcs in [*LIBS.items(), ("_binding.so", [BINDING])]:
-        target = lib_path(name)
-        tmp = target + ".tmp"
-        libs = b_libs if name == "_binding.so" else []
-        cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *[objs[s] for s in lib_srcs], *libs, "-lcudart", "-Xcompiler", "-pthread"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed for {name}:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, target)
-        out[name] = target
-        if verbose:
+    with cf.ThreadPoolExecutor(max_workers=min(16, len(srcs) + 1)) as ex:
+        binding = ex.submit(_binding_object)
+        objs = {s: ex.submit(_compile, s, extra) for s in srcs}
+        for name, lib_srcs in LIBS.items():
+            out[name] = _link(name, [objs[s].result() for s in lib_srcs], [])
+        obj, libs = binding.result()
+    out["_binding.so"] = _link("_binding.so", [obj], libs)
+    if verbose:
+        for target in out.values():
             print("built", target)
     return out
 

@@ -1,5 +1,6 @@
 """What the native binding of the tables, writes and 8-bit calls refuses and reports, without a GPU."""
 import os
+import subprocess
 
 import pytest
 import torch
@@ -49,3 +50,20 @@ def test_a_tree_without_one_of_the_built_files_is_built(missing, monkeypatch, tm
     monkeypatch.setattr(B, "build", lambda: built.append(True))
     ensure_built()
     assert bool(built) == (missing is not None)
+
+
+def test_the_libraries_are_built_where_the_binding_cannot_be(monkeypatch, tmp_path):
+    # a compiler and a linker that only touch their output, and PyTorch headers that are not there
+    def run(cmd, **kw):
+        src = cmd[cmd.index("-c") + 1] if "-c" in cmd else ""
+        if src == B.BINDING:
+            return subprocess.CompletedProcess(cmd, 1, "", "torch/extension.h: No such file or directory")
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(B, "PKG", str(tmp_path))
+    monkeypatch.setattr(B, "BUILD", str(tmp_path / "o"))
+    monkeypatch.setattr(B.subprocess, "run", run)
+    with pytest.raises(RuntimeError, match="binding.cpp"):
+        B.build()
+    assert {n for n in os.listdir(tmp_path) if n.endswith(".so")} == {"libscout.so", "libscoutgen.so"}
