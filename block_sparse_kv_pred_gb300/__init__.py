@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import re
 
 import torch
 
@@ -333,6 +334,10 @@ def _native():
         except ImportError as e:
             raise ScoutError(f"_binding.so is missing or does not load ({e}): "
                              "run `python -m block_sparse_kv_pred_gb300.build`") from e
+        have = re.match(r"\d+\.\d+\.\d+", torch.__version__)
+        if have is not None and have.group() != _binding.torch_version:
+            raise ScoutError(f"_binding.so was built with PyTorch {_binding.torch_version}, this is "
+                             f"{torch.__version__}: run `python -m block_sparse_kv_pred_gb300.build`")
         _binding.set_errors(ScoutError, torch.OutOfMemoryError)
         _NATIVE = _binding
     return _NATIVE

@@ -12,6 +12,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <c10/util/Exception.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <exception>
 
@@ -454,4 +455,15 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&g_module); }
+#define SCOUT_TEXT_(x) #x
+#define SCOUT_TEXT(x) SCOUT_TEXT_(x)
+
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&g_module);
+  // the PyTorch whose headers this was built with: its objects are read by their layout there
+  if (m != nullptr &&
+      PyModule_AddStringConstant(m, "torch_version", SCOUT_TEXT(TORCH_VERSION_MAJOR) "." SCOUT_TEXT(
+                                     TORCH_VERSION_MINOR) "." SCOUT_TEXT(TORCH_VERSION_PATCH)) != 0)
+    Py_CLEAR(m);
+  return m;
+}

@@ -67,3 +67,11 @@ def test_the_libraries_are_built_where_the_binding_cannot_be(monkeypatch, tmp_pa
     with pytest.raises(RuntimeError, match="binding.cpp"):
         B.build()
     assert {n for n in os.listdir(tmp_path) if n.endswith(".so")} == {"libscout.so", "libscoutgen.so"}
+
+
+def test_a_binding_built_with_another_pytorch_is_refused(monkeypatch):
+    assert torch.__version__.startswith(bs._native().torch_version)
+    monkeypatch.setattr(bs, "_NATIVE", None)
+    monkeypatch.setattr(torch, "__version__", "1.2.3+cpu")
+    with pytest.raises(bs.ScoutError, match=r"built with PyTorch \d+\.\d+\.\d+, this is 1\.2\.3"):
+        bs.build_tables(None, None, 1, 1, 1, 16, None, None)
