@@ -148,11 +148,11 @@ __global__ void __launch_bounds__(kA8Warps * 32) append8_kernel(const App8Args a
   }
 }
 
+// the prefixes' static part and the two rows of the largest batch: within what needs no request
+static_assert((2 * 32 + 2 * kMaxBatch + 2) * sizeof(int) <= 48 * 1024, "48 KB of shared memory");
+
 template <int P, int F>
 int launch_append8(const App8Args& a, int grid, size_t smem, cudaStream_t st) {
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(append8_kernel<P, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem) != cudaSuccess)
-    return SCOUT_ERR_CUDA;
   append8_kernel<P, F><<<grid, kA8Warps * 32, smem, st>>>(a);
   return launch_status();
 }
