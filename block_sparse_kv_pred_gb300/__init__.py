@@ -389,7 +389,7 @@ def build_digest8(kind, K_pool, K_scale, page_table, seq_len, B, Hkv, P, digest,
 
 def sparse_attn8_workspace(B, Hq, Hkv, P, D=128, device="cuda") -> torch.Tensor:
     w = torch.empty(lib().scout_sparse_attn8_workspace_bytes(B, Hq, Hkv, D, P), dtype=torch.uint8, device=device)
-    w[:131072].zero_()  # the counters
+    w[:_native().attn8_zero_bytes].zero_()  # the counters
     return w
 
 

@@ -462,8 +462,9 @@ PyMODINIT_FUNC PyInit__binding() {
   PyObject* m = PyModule_Create(&g_module);
   // the PyTorch whose headers this was built with: its objects are read by their layout there
   if (m != nullptr &&
-      PyModule_AddStringConstant(m, "torch_version", SCOUT_TEXT(TORCH_VERSION_MAJOR) "." SCOUT_TEXT(
-                                     TORCH_VERSION_MINOR) "." SCOUT_TEXT(TORCH_VERSION_PATCH)) != 0)
+      (PyModule_AddStringConstant(m, "torch_version", SCOUT_TEXT(TORCH_VERSION_MAJOR) "." SCOUT_TEXT(
+                                      TORCH_VERSION_MINOR) "." SCOUT_TEXT(TORCH_VERSION_PATCH)) != 0 ||
+       PyModule_AddIntConstant(m, "attn8_zero_bytes", SCOUT_SPARSE_ATTN8_ZERO_BYTES) != 0))
     Py_CLEAR(m);
   return m;
 }

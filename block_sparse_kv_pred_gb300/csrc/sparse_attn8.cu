@@ -1235,6 +1235,7 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm) attn8_cluster_kernel(co
 // The workspace's layout does not depend on the call's shape: the counters that one call leaves zero
 // are those that the next one, of any shape, finds.
 constexpr size_t kCounters8 = (size_t)kMaxUnits8 * kMaxG * sizeof(int32_t);
+static_assert(kCounters8 == SCOUT_SPARSE_ATTN8_ZERO_BYTES, "as the header says");
 // shared memory of the largest launch: two such CTAs fit an SM
 constexpr size_t kMostSmem = 1024 + (size_t)kRingBytes8 + kTileBytes + (size_t)(kMaxUnits8 + 1) * 4;
 static_assert(kCtasPerSm * (kMostSmem + 8 * 1024) <= 228 * 1024, "two CTAs an SM");

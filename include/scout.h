@@ -439,11 +439,12 @@ int scout_build_digest8(int kind, int fmt, const void* K_pool, const float* K_sc
  * skipped and SCOUT_DEV_BAD_INDEX set.  When a bounded wait expires, SCOUT_DEV_TIMEOUT is set and
  * the heads of every unit with a block that was left out become NaN, O and lse.  O_cpu of a head with lse_cpu = -inf is not used.
  * workspace: scout_sparse_attn8_workspace_bytes() bytes (the same for every shape), 16-byte
- * aligned; its first 131072 bytes must be zero before the first use and are left zero by every
- * call.  One workspace serves calls of any shape, one after the other; calls that may overlap
+ * aligned; its first SCOUT_SPARSE_ATTN8_ZERO_BYTES must be zero before the first use and are left
+ * zero by every call.  One workspace serves calls of any shape, one after the other; calls that may overlap
  * (streams, graphs) need one each.
  * Requires G <= 8, B * Hkv <= 4096, B * Hkv * k <= 2^28, n_slots * P < 2^31, pools 16-byte
  * aligned, q, O_part and O_cpu 8-byte and O_out 4-byte aligned. */
+#define SCOUT_SPARSE_ATTN8_ZERO_BYTES 131072
 size_t scout_sparse_attn8_workspace_bytes(int B, int Hq, int Hkv, int D, int P);
 int scout_sparse_attn8(int fmt, const void* q, const void* K_pool, const void* V_pool, const float* K_scale,
                        const float* V_scale, int64_t n_slots, const int32_t* page_table, const int32_t* seq_len,

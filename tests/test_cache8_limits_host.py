@@ -75,3 +75,11 @@ def test_a_binding_built_with_another_pytorch_is_refused(monkeypatch):
     monkeypatch.setattr(torch, "__version__", "1.2.3+cpu")
     with pytest.raises(bs.ScoutError, match=r"built with PyTorch \d+\.\d+\.\d+, this is 1\.2\.3"):
         bs.build_tables(None, None, 1, 1, 1, 16, None, None)
+
+
+def test_the_bytes_of_a_workspace_that_start_as_zero():
+    n = bs._native().attn8_zero_bytes
+    assert n == 4096 * 8 * 4  # a counter for each head of the most units
+    assert bs.lib().scout_sparse_attn8_workspace_bytes(1, 8, 1, 128, 32) > n
+    w = bs.sparse_attn8_workspace(1, 8, 1, 32, device="cpu")
+    assert w.numel() == bs.lib().scout_sparse_attn8_workspace_bytes(1, 8, 1, 128, 32) and not w[:n].any()

@@ -223,7 +223,7 @@ def test_attn8_an_expired_wait_is_reported_and_spoils_its_units_alone(split, mer
     a.check(*good, merged=merge)
     assert int(st) == 0
     bad = call(bs.INJECT_ABANDON)
-    assert int(st) == 2 and not ws[:131072].any()
+    assert int(st) == 2 and not ws[:bs._native().attn8_zero_bytes].any()
     lost = torch.isnan(bad[1])
     assert lost.any() and torch.equal(torch.isnan(bad[0]), lost[..., None].expand(-1, -1, D))
     units = lost.view(-1, a.G)
