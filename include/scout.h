@@ -402,8 +402,8 @@ typedef enum scout_fp8 {
  *           x of the block
  *   scale = need for a block without cached tokens, else max(its scale, need)
  *   code  = x * (1 / scale) rounded to nearest even (infinities to +-F, NaN to NaN);
- *           the cached tokens' codes become code * (old scale / scale), rounded, when the
- *           scale grew, and stay as they are otherwise.
+ *           the cached tokens' codes become code * (old scale / scale), rounded in the
+ *           same way, when the scale grew, and stay as they are otherwise.
  * Everything else in the pools and scales is left as it was: rows at and past seq_len too.
  * Running it again on the same rows changes nothing.  The scales of blocks with cached tokens must be
  * positive.  Every touched block needs a slot of its own.
@@ -423,9 +423,9 @@ int scout_append_kv8(int fmt, const void* K_new, int64_t ld_k, const void* V_new
  * down and the maxima up to bf16, so that a digest bounds every score of its block whatever
  * the scale (with power-of-two scales both are exact).  Mean: the codes' fp32 sum (exact for
  * e4m3, at most seven roundings deep for e5m2) times scale / count.  NaN codes are passed over by
- * the minima and maxima.  Requires n_slots and B * Hkv * nblk_cap < 2^31.
+ * the minima and maxima; a channel that holds nothing else gets +inf and -inf.
  * A (-1, -1) entry of block_list is padding and skipped; any other entry outside the tables
- * sets SCOUT_DEV_BAD_INDEX. */
+ * sets SCOUT_DEV_BAD_INDEX.  Requires n_slots and B * Hkv * nblk_cap < 2^31. */
 int scout_build_digest8(int kind, int fmt, const void* K_pool, const float* K_scale, int64_t n_slots,
                         const int32_t* page_table, const int32_t* seq_len, int B, int Hkv, int D, int P, int nblk_cap,
                         const int32_t* block_list, int n_list, void* digest, int32_t* dev_status,

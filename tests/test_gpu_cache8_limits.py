@@ -196,6 +196,45 @@ def test_attn8_a_v_scale_that_is_not_finite_is_seen(bad, P, split):
         assert np.isfinite(rest).all() and np.abs(rest - eO.reshape(-1, D)[3:]).max() < 0.1
 
 
+def nan_codes(fmt):
+    v = C8.code_values(fmt)
+    return np.flatnonzero(np.isnan(v))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("P,n", [(16, 16), (32, 32), (32, 7), (64, 50)])
+def test_digest8_passes_over_nan_codes(fmt, P, n):
+    rng = np.random.default_rng(P + n)
+    codes = finite_codes(rng, (1, P, D), fmt)
+    bad = nan_codes(fmt)
+    for c in range(0, D, 3):  # in some rows
+        rows = rng.permutation(n)[: rng.integers(1, n)]
+        codes[0, rows, c] = rng.choice(bad, len(rows))
+    none = [5, 64, 127]       # in every row of a channel
+    codes[0, :, none] = rng.choice(bad, (3, P))
+    inf = np.array([], int)
+    if fmt == "e5m2":
+        inf = np.array([1, 70])
+        codes[0, 0, inf] = 0x7C, 0xFC
+    scale = np.float32(2.0 ** -3)
+    x = C8.decode(codes[0, :n], fmt) * float(scale)
+    x[:, none] = 0.0  # (silences numpy; replaced below)
+    lo, hi = np.nanmin(x, 0), np.nanmax(x, 0)
+    lo[none], hi[none] = np.inf, -np.inf
+    dg = torch.zeros((1, 1, 1, 2, D), dtype=torch.bfloat16, device="cuda")
+    args = pool8(codes, fmt), torch.tensor([scale], device="cuda"), i32([[[0]]]), i32([n]), 1, 1, P
+    bs.build_digest8("minmax", *args, dg)
+    got = dg.double().cpu().numpy()[0, 0, 0]
+    assert np.array_equal(got, [lo, hi])
+    if fmt == "e5m2":
+        assert hi[1] == np.inf and lo[70] == -np.inf
+    mean = torch.zeros((1, 1, 1, D), device="cuda")
+    bs.build_digest8("mean", *args, mean)
+    want = C8.decode(codes[0, :n], fmt).sum(0)
+    m = mean.cpu().numpy()[0, 0, 0]
+    assert np.array_equal(np.isnan(m), np.isnan(want)) and (m[inf] == want[inf]).all()
+
+
 # ---------------------------------------------------------------------------
 # failures
 # ---------------------------------------------------------------------------
