@@ -12,7 +12,7 @@ import torch
 import block_sparse_kv_pred_gb300 as bs
 from oracle import cache8_oracle as C8
 from _parity import ensure_built
-from test_gpu_cache8 import D, SPLITS, Attn, bf16_values, codes_of, dev, finite_codes, i32, make_tables, pool8
+from test_gpu_cache8 import D, DT, SPLITS, Attn, bf16_values, codes_of, dev, finite_codes, i32, make_tables, pool8
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -58,6 +58,46 @@ def test_tables_with_an_empty_map_or_list(which):
         bs.build_tables(i32([n]), None, 4, 1, 2, 16, t, torch.zeros((1, 2, 1), dtype=torch.int32, device="cuda"),
                         status=st, **{which: kw[which]})
         assert int(st) == want and t.flatten().tolist() == ([0, -1, 1, -1] if n else [-1] * 4)
+
+
+def test_tables_of_a_pool_with_the_most_slots():
+    # slots whose rows' numbers pass 32 bits
+    n, slots = (1 << 31) - 1, [(1 << 31) - 2, 5, (1 << 26) + 3]
+    m, st = torch.full((130, 1), -7, dtype=torch.int64, device="cuda"), word()
+    t, w = torch.zeros((1, 1, 3), dtype=torch.int32, device="cuda"), torch.zeros((1, 1, 1), dtype=torch.int32, device="cuda")
+    bs.build_tables(i32([130]), i32(slots), n, 1, 1, 64, t, w, slot_map=m, status=st)
+    assert int(st) == 0 and t.flatten().tolist() == slots
+    assert m.flatten().tolist() == [slots[i // 64] * 64 + i % 64 for i in range(130)]
+
+
+# ---------------------------------------------------------------------------
+# append_kv
+# ---------------------------------------------------------------------------
+def test_append_rows_and_pools_past_32_bit_offsets():
+    # rows 2^25 elements apart, into the last slots of pools of more than 2^31 elements
+    rng = np.random.default_rng(58)
+    n, Hkv, P, ld = 70, 2, 32, 1 << 25
+    n_slots = (1 << 31) // (P * D) + 10
+    at = n_slots * P - 1 - rng.permutation(n * Hkv).reshape(n, Hkv)
+    x = bf16_values(rng, (n, Hkv, D)).cuda()
+    wide = torch.empty((n, ld), dtype=torch.bfloat16, device="cuda")
+    wide[:, 8:8 + Hkv * D] = x.view(n, -1)
+    far, st = wide[:, 8:8 + Hkv * D].view(n, Hkv, D), word()
+    pools = [torch.empty((n_slots, P, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for p in pools:
+        p[-8:] = 9.0
+    bs.append_kv(far, x, dev(at), Hkv, P, *pools, status=st)
+    want = torch.full((8 * P, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    want[dev(at - (n_slots - 8) * P).flatten()] = x.view(-1, D)
+    assert int(st) == 0 and all(torch.equal(p[-8:].view(-1, D), want) for p in pools)
+    del pools
+    # and the quantising write from the same rows
+    codes, table = np.zeros((6, P, D), np.uint8), np.arange(6).reshape(1, Hkv, 3)
+    pools, sc = [pool8(codes, "e4m3") for _ in range(2)], [torch.zeros(6, device="cuda") for _ in range(2)]
+    bs.append_kv8(far, x, i32(table), i32([n]), 1, Hkv, P, *pools, *sc, status=st)
+    ec, es = C8.append8(x.double().cpu().numpy(), None, [n], table, codes, np.zeros(6), "e4m3", P)
+    assert int(st) == 0 and all(np.array_equal(codes_of(p), ec) for p in pools)
+    assert all(np.array_equal(s.cpu().numpy(), es.astype(np.float32)) for s in sc)
 
 
 # ---------------------------------------------------------------------------
@@ -196,6 +236,26 @@ def test_attn8_a_v_scale_that_is_not_finite_is_seen(bad, P, split):
         assert np.isfinite(rest).all() and np.abs(rest - eO.reshape(-1, D)[3:]).max() < 0.1
 
 
+@pytest.mark.parametrize("shape", [dict(SPLITS[0], lens=[4000, 100, 3500]), dict(SPLITS[1], lens=[2000] * 3 + [500] * 37),
+                                   SPLITS[2], dict(SPLITS[3], lens=[30000, 500])])
+def test_attn8_counts_outside_the_lists_are_cut_to_them(shape):
+    a = Attn(53, **shape)
+    full = a.counts == a.k
+    assert full.any()
+    a.counts[full] = a.k + 3
+    a.counts.flat[np.flatnonzero(~full)[0]] = -1
+    a.run()
+
+
+@pytest.mark.parametrize("shape", [dict(B=2, Hkv=2, G=4, P=16, lens=[300, 40], k=9), dict(SPLITS[3], lens=[30000, 500])])
+def test_attn8_a_block_listed_more_than_once_counts_each_time(shape):
+    a = Attn(59, **shape)
+    c = int(a.counts[0, 0])
+    a.lists[0, 0, :c] = np.sort(a.rng.choice(a.lists[0, 0, : (c + 1) // 2], c))
+    a.lists[1, 1, :2], a.counts[1, 1] = 0, 2
+    a.run()
+
+
 def nan_codes(fmt):
     v = C8.code_values(fmt)
     return np.flatnonzero(np.isnan(v))
@@ -293,3 +353,75 @@ def test_outputs_that_do_not_fit_raise_torch_out_of_memory():
         torch.cuda.set_per_process_memory_fraction(1.0)
         del held
     a.check(*bs.sparse_attn8(*t, ws))
+
+
+# ---------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------
+class State:
+    """Pools, tables and buffers of a batch that decodes; step() is one token for the sequences that grow."""
+
+    def __init__(self, B, Hkv, G, P, cap, k, rows):
+        self.B, self.Hkv, self.G, self.P, self.cap, self.k = B, Hkv, G, P, cap, k
+        n_slots = B * Hkv * cap
+        z = lambda *s, dtype=torch.int32: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731
+        self.prev, self.seq, self.counts, self.status = z(B), z(B), z(3), z(1)
+        self.table, self.bits, self.free = z(B, Hkv, cap), z(B, Hkv, -(-cap // 32)), z(n_slots)
+        self.map, self.list = z(rows, Hkv, dtype=torch.int64), z(rows * Hkv, 2)
+        self.pools = [z(n_slots, P, D, dtype=torch.uint8).view(DT["e4m3"]) for _ in range(2)]
+        self.plain = [z(n_slots, P, D, dtype=torch.bfloat16) for _ in range(2)]
+        self.scales = [z(n_slots, dtype=torch.float32) for _ in range(2)]
+        self.digest, self.K, self.V = (z(*s, dtype=torch.bfloat16) for s in ((B, Hkv, cap, 2, D), (rows, Hkv, D), (rows, Hkv, D)))
+        self.q, self.O = z(B, Hkv * G, D, dtype=torch.bfloat16), z(B, Hkv * G, D, dtype=torch.bfloat16)
+        self.lse, self.O_cpu = z(B, Hkv * G, dtype=torch.float32), z(B, Hkv * G, D, dtype=torch.float32)
+        self.lse_cpu = torch.full_like(self.lse, -np.inf)
+        self.sel = {n: z(B, Hkv, k) for n in ("topk", "res", "cpu", "delta")}
+        self.sel.update({n + "_count": z(B, Hkv) for n in tuple(self.sel)})
+        self.ws_t, self.ws_a = bs.score_topk_workspace(B, Hkv, cap), bs.sparse_attn8_workspace(B, Hkv * G, Hkv, P)
+
+    def step(self, n, fresh=False):
+        B, Hkv, P, st, p = self.B, self.Hkv, self.P, self.status, None if fresh else self.prev
+        bs.build_tables(self.seq, self.free, self.free.numel(), B, Hkv, P, self.table, self.bits, prev_len=p, slot_map=self.map,
+                        block_list=self.list, counts=self.counts, status=st)
+        bs.append_kv(self.K[:n], self.V[:n], self.map[:n], Hkv, P, *self.plain, status=st)
+        bs.append_kv8(self.K[:n], self.V[:n], self.table, self.seq, B, Hkv, P, *self.pools, *self.scales, prev_len=p, status=st)
+        bs.build_digest8("minmax", self.pools[0], self.scales[0], self.table, self.seq, B, Hkv, P, self.digest,
+                         block_list=self.list, status=st)
+        bs.score_topk("minmax", self.q, self.digest, self.seq, self.bits, B, Hkv * self.G, Hkv, P, self.cap, self.k, self.ws_t,
+                      out=self.sel, status=st)
+        bs.sparse_attn8_merge(self.q, *self.pools, *self.scales, self.table, self.seq, self.sel["res"], self.sel["res_count"], B,
+                              Hkv * self.G, Hkv, P, self.k, D ** -0.5, self.ws_a, self.O_cpu, self.lse_cpu, self.O, self.lse, st)
+        self.prev.copy_(self.seq)
+
+
+def test_decode_steps_captured_once_and_replayed():
+    """A graph of a padded decode step (a row for every sequence, whether it grows or not), replayed as the lengths move
+    on, against calls with the rows there are: tables, pools, scales, digests and outputs alike."""
+    rng = np.random.default_rng(57)
+    B, Hkv, G, P, cap, k = 5, 2, 4, 16, 12, 5
+    seq = np.array([100, 15, 31, 1, 64])
+    a, b = (State(B, Hkv, G, P, cap, k, int(seq.sum())) for _ in range(2))
+    g = torch.cuda.CUDAGraph()
+    free = rng.permutation(a.free.numel())
+    for i in range(24):
+        grow = seq if i == 0 else rng.integers(0, 2, B)
+        n = int(grow.sum())
+        x = [bf16_values(rng, s) for s in ((n, Hkv, D), (n, Hkv, D), (B, Hkv * G, D))]
+        for s in (a, b):
+            s.K[:n], s.V[:n], s.q[:] = (y.cuda() for y in x)
+            s.K[n:], s.V[n:] = float("nan"), float("nan")
+            s.seq += i32(grow)
+            s.free[: len(free)] = i32(free)
+        torch.cuda.synchronize()
+        if i == 1:
+            with torch.cuda.graph(g):
+                a.step(B)
+        g.replay() if i else a.step(n, fresh=True)
+        b.step(n, fresh=i == 0)
+        torch.cuda.synchronize()
+        assert int(a.status) == 0 and int(b.status) == 0
+        for x, y in ((getattr(a, m), getattr(b, m)) for m in ("prev", "table", "bits", "counts", "digest", "O", "lse")):
+            assert torch.equal(x, y)
+        assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a.pools + a.plain + a.scales, b.pools + b.plain + b.scales))
+        assert torch.isfinite(a.O).all() and torch.isfinite(a.lse).all()
+        free = free[int(a.counts[2]):]
