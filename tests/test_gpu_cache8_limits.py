@@ -356,6 +356,40 @@ def test_outputs_that_do_not_fit_raise_torch_out_of_memory():
 
 
 # ---------------------------------------------------------------------------
+# recalled blocks
+# ---------------------------------------------------------------------------
+def test_a_recalled_block_is_written_as_a_sequence_of_its_own():
+    """Blocks whose host copy is bf16 come back through append_kv8, each as a fresh sequence of one KV head, and their
+    digests are rebuilt: the codes need not be those that were evicted, as a block that was filled piece by piece may
+    have been rounded twice."""
+    rng = np.random.default_rng(55)
+    Hkv, P, n_slots = 2, 16, 12
+    seq, grown = [20], [32]  # block 1 filled in two parts, the second with larger values
+    x = bf16_values(rng, (32, Hkv, D))
+    x[20:] *= 64.0
+    pools = [pool8(np.zeros((n_slots, P, D), np.uint8), "e4m3") for _ in range(2)]
+    sc = [torch.zeros(n_slots, device="cuda") for _ in range(2)]
+    table = i32([[[0, 1], [2, 3]]])
+    bs.append_kv8(x[:20].cuda(), x[:20].cuda(), table, i32(seq), 1, Hkv, P, *pools, *sc)
+    bs.append_kv8(x[20:].cuda(), x[20:].cuda(), table, i32(grown), 1, Hkv, P, *pools, *sc, prev_len=i32(seq))
+    dg = torch.zeros((1, Hkv, 2, 2, D), dtype=torch.bfloat16, device="cuda")
+    bs.build_digest8("minmax", pools[0], sc[0], table, i32(grown), 1, Hkv, P, dg)
+    # both heads' block 1 leave slots 1 and 3 and come back into slots 9 and 5
+    rows = torch.cat([x[16:32, h] for h in range(Hkv)]).view(2 * P, 1, D).cuda()
+    bs.append_kv8(rows, rows, i32([[[9]], [[5]]]), i32([P, P]), 2, 1, P, *pools, *sc)
+    table[0, 0, 1], table[0, 1, 1] = 9, 5
+    bs.build_digest8("minmax", pools[0], sc[0], table, i32(grown), 1, Hkv, P, dg, block_list=i32([[0, 1], [1, 1]]))
+    got, scale = codes_of(pools[0]), sc[0].cpu().numpy()
+    for h, (was, now) in enumerate(((1, 9), (3, 5))):
+        new = x[16:32, h].double().numpy()
+        s = C8.block_scale(new, "e4m3")
+        assert scale[now] == s and np.array_equal(got[now], C8.encode(new / s, "e4m3")) and scale[was] == s
+        v = C8.decode(got[now], "e4m3") * s
+        lo, hi = dg[0, h, 1].double().cpu().numpy()
+        assert np.array_equal(lo, v.min(0)) and np.array_equal(hi, v.max(0))
+
+
+# ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
 class State:
