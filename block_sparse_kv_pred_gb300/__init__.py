@@ -93,10 +93,10 @@ _SIGS = {
 
 
 class Launch(ctypes.Structure):
-    """scout_launch: launch options of the persistent kernels.  max_ctas 0 = one CTA per SM;
-    pdl 1 = start early after the previous kernel on the stream; early_event = a
-    cudaEvent_t (timing disabled) this launch records programmatically, so that one of the
-    three persistent kernels on a stream waiting for it may start early; inject = a
+    """scout_launch: launch options of the persistent kernels.  max_ctas 0 = one CTA per SM (two
+    of the 8-bit attention); pdl 1 = start early after the previous kernel on the stream;
+    early_event = a cudaEvent_t (timing disabled) this launch records programmatically, so that
+    one of the persistent kernels on a stream waiting for it may start early; inject = a
     SCOUT_INJECT_* fault for tests (0 in normal use)."""
     _fields_ = [("max_ctas", ctypes.c_int), ("pdl", ctypes.c_int), ("early_event", ctypes.c_void_p),
                 ("inject", ctypes.c_int)]

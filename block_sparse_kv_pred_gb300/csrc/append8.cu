@@ -12,8 +12,8 @@
 // codes are then rounded to the new scale (a power of two coarser: exact but for codes that fall
 // below the normal range).
 //
-// Bound by DRAM for prompts: GB300, 8 of up to 16K tokens, 8 KV heads, 69.9 us for 428 MB (6.1 TB/s,
-// 0.90 of the measured copy bandwidth); a decode step of 40 sequences takes 3.8 us, a chain of
+// Bound by DRAM for prompts: GB300, 8 of up to 16K tokens, 8 KV heads, 70.4 us for 428 MB (6.1 TB/s,
+// 0.90 of the measured copy bandwidth); a decode step of 40 sequences takes 3.9 us, a chain of
 // dependent reads (lengths, slot and rows, scale).
 #include "fp8.cuh"
 

@@ -1,7 +1,7 @@
 // The Python side of the tables, the cache writes and the 8-bit cache: arguments checked and handed to
 // the C ABI in one native call each.  A decode step's calls are short (3 to 7 us on the device), so
 // what their checks cost counts: with ctypes and a Python check per tensor they took 8 to 11 us of
-// host time and the attention 21, here 2.6 to 3.2 and 8 (two allocations and a launch of 2 us among
+// host time and the attention 21, here 2.6 to 3.2 and 7 to 8 (two allocations and a launch of 2 us among
 // them; GB300's Grace cores).  Nothing but marshalling happens here: the tensors' types, sizes, order
 // and device are checked, as the C ABI, which checks everything else, sees addresses only.
 #include <Python.h>

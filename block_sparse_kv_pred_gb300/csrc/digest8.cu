@@ -7,9 +7,9 @@
 // and scaled once at the end, rounded down and up: a digest still bounds every score of its
 // block.  The mean sums codes in fp32.
 //
-// Bound by DRAM and its start: GB300, 8 x 16K tokens, 8 KV heads, blocks of 32, min/max: 27.0 us
-// for 151 MB (5.6 TB/s, 0.82 of the measured copy bandwidth, launch and first reads included); mean
-// digests of 2,800 blocks of 64: 4.5 us.
+// Bound by DRAM and its start: GB300, 8 x 16K tokens, 8 KV heads, blocks of 32, min/max: 27.3 us
+// for 151 MB (5.5 TB/s, 0.82 of the measured copy bandwidth, launch and first reads included); mean
+// digests of 2,800 blocks of 64: 5.3 us.
 #include "fp8.cuh"
 
 namespace scout {

@@ -36,11 +36,11 @@
 // tile, and its operands would need q and the weights in 8 bits or K and V widened in shared
 // memory.  The products take 52 ns of an SM's time a step (48 at 1.08 ns), the conversions about
 // as much; a step's 8 KB take 182 ns of the SM's share of DRAM, so a long launch is bound by DRAM:
-// GB300, 4 x 128K tokens dense, 175 us for 1.08 GB (6.1 TB/s, 0.90 of the measured copy bandwidth;
-// the SMs' shares of it differ, and the first are done at 0.75 of the time).  40 sequences of 2,048
-// listed tokens, 8 x 5 heads: 38.0 us for 152 MB, of which the first 4 go by before the copies start
+// GB300, 4 x 128K tokens dense, 172 us for 1.08 GB (6.2 TB/s, 0.92 of the measured copy bandwidth;
+// the SMs' shares of it differ, and the first are done at 0.75 of the time).  40 sequences of 58
+// blocks of 32 tokens, 8 x 5 heads: 38.4 us for 152 MB, of which the first 4 go by before the copies start
 // (counts, list, page table), 24 stream at 6.3 TB/s, and the rest is the slowest warp and the end
-// phase (barrier, join, barrier).  One 4K sequence: 6.6 us, all latency.
+// phase (barrier, join, barrier).  One 4K sequence: 6.7 us, all latency.
 #include <atomic>
 
 #include "fp8.cuh"
@@ -57,8 +57,8 @@ constexpr int kCtasPerSm = 2;
 // more) 29.3 | 31.6 us.
 constexpr int kWholeSteps = 2;
 constexpr int kPieces = 8;             // of a cut unit, merged at a time
-// Clusters.  With few units and lists that give each warp at most kClusterSteps steps, the CTAs of a
-// cluster share one unit.  Measured on GB300, even split | cluster, lists of 58 blocks of 32 tokens, 8
+// Clusters.  With few units and lists that give each warp at most kClusterSteps steps (as long as they may
+// be: the host does not know the counts), the CTAs of a cluster share one unit.  Measured on GB300, even split | cluster, lists of 58 blocks of 32 tokens, 8
 // KV heads x 4: 1 sequence 11.9 | 7.2 us, 8 17.2 | 11.4, 16 23.3 | 18.4; 4 of 512 blocks (8 steps a
 // warp) 32.3 | 27.8, 1 of 1,024 (16 steps) 27.1 | 33.4.
 constexpr int kMaxCluster = 8;
@@ -76,8 +76,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWBoost = 14;            // weights are kept as 2^14 w, so that their low parts stay normal f16
 constexpr int kHalf = 4096;            // K or V of a step: 32 tokens x 128 bytes
 // Halves of a warp's ring.  Two, so that an SM has at most 128 KB in flight: with three it had 192
-// KB, which bought no bandwidth but longer queues for every other access (40 sequences of 2,048
-// listed tokens, 8 KV heads: 42.8 us with two, 46.5 with three; 4 x 128K tokens: 176 and 189 us).
+// KB, which bought no bandwidth but longer queues for every other access (40 sequences of 58
+// blocks of 32 tokens, 8 KV heads: 42.8 us with two, 46.5 with three; 4 x 128K tokens: 176 and 189 us).
 constexpr int kHalves = 2;
 constexpr int kBatch = 16;             // steps whose tiles are resolved together (32 tiles, one a lane)
 constexpr int kRingBytes8 = kNW * kHalves * kHalf;

@@ -7,12 +7,13 @@
 // blocks) in shared memory, and after that no item depends on another: a warp takes a word of 32
 // blocks of a unit (one coalesced row piece, one ballot for the residency word), a touched block
 // of a sequence (its tokens x heads are one contiguous piece of the slot map, stored as pairs of
-// heads where their number is a power of two), or 32 list entries.  One launch, no atomics.  Bound by instruction issue and the chain lengths ->
-// prefix -> free slot -> store: GB300, device time, 5.5 us for a decode step of 40 sequences, 13.8 us
-// for 40 prompts (3.3 TB/s into L2).
+// heads where their number is a power of two), or 32 list entries.  One launch, no atomics.  GB300, device
+// time: 13.7 us for 40 prompts (3.3 TB/s into L2), bound by the issue of this index arithmetic, some 120
+// instructions for each 512 bytes of map; 5.5 us for a decode step of 40 sequences, the launch and
+// three sections in turn of two dependent reads each (a length, then a free slot or a table entry).
 //
-// Append: bound by DRAM.  8 prompts of up to 16K tokens, 8 KV heads: 88.8 us for 575 MB (6.5 TB/s, 0.95
-// of the measured copy bandwidth); 2.7 us for a decode step of 8 sequences.
+// Append: bound by DRAM.  8 prompts of up to 16K tokens, 8 KV heads: 89.1 us for 575 MB (6.5 TB/s, 0.95
+// of the measured copy bandwidth); 2.6 us for a decode step of 8 sequences.
 #include "fp8.cuh"
 
 namespace scout {

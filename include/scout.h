@@ -72,7 +72,9 @@ typedef enum scout_digest_kind {
  * persistent kernel launches (at most one per SM each): kernels of independent
  * work, e.g. the next layer's selection and this layer's attention (Algorithm 1),
  * can then share the SMs from separate streams.  0 means one CTA per SM; a
- * negative value is SCOUT_ERR_INVALID_ARG.  scout_score_topk deals whole units to
+ * negative value is SCOUT_ERR_INVALID_ARG.  scout_sparse_attn8(_merge) runs two CTAs
+ * an SM: 0 means that many, and under a bound two of its CTAs may share an SM.
+ * scout_score_topk deals whole units to
  * its CTAs as they start, so it also takes the SMs other kernels free up while it
  * runs; its default (0) is the fewest CTAs that take ceil(units / SMs) units each
  * (a last round of units then keeps as many SMs streaming as the others).  For
@@ -96,8 +98,8 @@ typedef enum scout_digest_kind {
  *                    programmatically and fires before the primary completes, once
  *                    every CTA of it has passed its trigger: scout_predict_q at its
  *                    start, scout_score_topk once its last unit has been handed out,
- *                    scout_sparse_attn once its attention warps are done.  One of the
- *                    three kernels launched on a stream that waits for the event then
+ *                    scout_sparse_attn once its attention warps are done.  One of
+ *                    these kernels launched on a stream that waits for the event then
  *                    starts early as above.  Anything else that waits for the event
  *                    (a copy, a host wait, another library's kernel) is NOT ordered
  *                    after the primary's writes: record a plain event after the call
@@ -432,8 +434,8 @@ int scout_build_digest8(int kind, int fmt, const void* K_pool, const float* K_sc
                         cudaStream_t stream);
 
 /* Attention over the listed blocks of an 8-bit cache: scout_sparse_attn and
- * scout_sparse_attn_merge with K and V read as code * scale; outputs, conventions, work
- * split and early starts as theirs (it waits before its first global read).  The
+ * scout_sparse_attn_merge with K and V read as code * scale; outputs, conventions and early
+ * starts as theirs (it waits before its first global read), with a work split of its own.  The
  * probabilities keep about 22 bits and the queries all of theirs, so the fp32 outputs are
  * good to fp32 rounding.  Listed blocks outside the tables, the pool or the sequence are
  * skipped and SCOUT_DEV_BAD_INDEX set.  When a bounded wait expires, SCOUT_DEV_TIMEOUT is set and
