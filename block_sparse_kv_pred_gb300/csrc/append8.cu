@@ -175,15 +175,15 @@ extern "C" int scout_append_kv8(int fmt, const void* K_new, int64_t ld_k, const 
                                 void* V_pool, float* K_scale, float* V_scale, int64_t n_slots, int32_t* dev_status,
                                 cudaStream_t stream) {
   using namespace scout;
-  if ((n_tokens > 0 && (K_new == nullptr || V_new == nullptr)) || seq_len == nullptr || page_table == nullptr || K_pool == nullptr ||
-      V_pool == nullptr || K_scale == nullptr || V_scale == nullptr)
+  if ((n_tokens > 0 && (K_new == nullptr || V_new == nullptr)) || seq_len == nullptr || page_table == nullptr ||
+      K_pool == nullptr || V_pool == nullptr || K_scale == nullptr || V_scale == nullptr)
     return SCOUT_ERR_INVALID_ARG;
   if (!valid_fp8(fmt) || n_tokens < 0 || B <= 0 || Hkv <= 0 || nblk_cap <= 0 || n_slots <= 0 ||
       ld_k < (int64_t)Hkv * D || ld_v < (int64_t)Hkv * D)
     return SCOUT_ERR_INVALID_ARG;
   if (D != kD || !valid_P(P) || B > kMaxBatch || nblk_cap > kMaxNblk || n_slots > 0x7fffffffLL ||
-      (int64_t)B * nblk_cap * P > 0x7fffffffLL || (int64_t)B * Hkv * nblk_cap > 0x7fffffffLL || ld_k % 8 != 0 || ld_v % 8 != 0 || !aligned16(K_new) ||
-      !aligned16(V_new) || !aligned16(K_pool) || !aligned16(V_pool))
+      (int64_t)B * nblk_cap * P > 0x7fffffffLL || (int64_t)B * Hkv * nblk_cap > 0x7fffffffLL || ld_k % 8 != 0 ||
+      ld_v % 8 != 0 || !aligned16(K_new) || !aligned16(V_new) || !aligned16(K_pool) || !aligned16(V_pool))
     return SCOUT_ERR_UNSUPPORTED;
   if (n_tokens == 0 && dev_status == nullptr) return SCOUT_OK;  // no rows, and nowhere to say that some were due
   App8Args a;

@@ -58,9 +58,10 @@ constexpr int kCtasPerSm = 2;
 constexpr int kWholeSteps = 2;
 constexpr int kPieces = 8;             // of a cut unit, merged at a time
 // Clusters.  With few units and lists that give each warp at most kClusterSteps steps (as long as they may
-// be: the host does not know the counts), the CTAs of a cluster share one unit.  Measured on GB300, even split | cluster, lists of 58 blocks of 32 tokens, 8
-// KV heads x 4: 1 sequence 11.9 | 7.2 us, 8 17.2 | 11.4, 16 23.3 | 18.4; 4 of 512 blocks (8 steps a
-// warp) 32.3 | 27.8, 1 of 1,024 (16 steps) 27.1 | 33.4.
+// be: the host does not know the counts), the CTAs of a cluster share one unit.  Measured on GB300,
+// even split | cluster, lists of 58 blocks of 32 tokens, 8 KV heads x 4: 1 sequence 11.9 | 7.2 us, 8
+// 17.2 | 11.4, 16 23.3 | 18.4; 4 of 512 blocks (8 steps a warp) 32.3 | 27.8, 1 of 1,024 (16 steps)
+// 27.1 | 33.4.
 constexpr int kMaxCluster = 8;
 constexpr int kClusterSteps = 8;
 // With at least kSnapUnits units for each cluster of kSnap CTAs that the device holds, a cluster takes
