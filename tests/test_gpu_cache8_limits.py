@@ -256,6 +256,35 @@ def test_attn8_a_block_listed_more_than_once_counts_each_time(shape):
     a.run()
 
 
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("shape", [dict(B=2, Hkv=2, G=3, P=16, lens=[300, 40], k=9), dict(SPLITS[1], lens=[300] * 40, k=8)])
+def test_attn8_a_query_that_is_not_finite_spoils_its_head_alone(bad, shape):
+    a = Attn(60, **shape)
+    assert a.counts[0, 0] > 0
+    a.q[0, 1, 5] = bad
+    O_, l = bs.sparse_attn8(*a.device(), a.workspace())
+    assert not torch.isfinite(O_[0, 1]).any() and not torch.isfinite(l[0, 1])
+    a.q[0, 1] = 0  # the other heads, to the tolerance of any call
+    zero = bs.sparse_attn8(*a.device(), a.workspace())
+    O_[0, 1], l[0, 1] = zero[0][0, 1], zero[1][0, 1]
+    a.check(O_, l)
+
+
+@pytest.mark.parametrize("shape", [*SPLITS, dict(B=64, Hkv=8, G=2, P=16, top=90, k=6), dict(B=1, Hkv=1, G=8, P=32, top=900, k=20)])
+def test_attn8_with_every_list_empty(shape):
+    a = Attn(61, **shape)
+    a.counts[:], a.lists[:] = 0, -1
+    O_, l = a.run()
+    assert not O_.any() and torch.isinf(l).all()
+
+
+@pytest.mark.parametrize("B,Hkv,P", [(1, 2, 32), (5, 8, 16), (64, 8, 32), (7, 4, 64)])
+def test_attn8_short_lists_in_long_buffers(B, Hkv, P):
+    a = Attn(62, B=B, Hkv=Hkv, G=4, P=P, top=6 * P, k=3000)
+    assert a.counts.max() <= 6
+    a.run()
+
+
 def nan_codes(fmt):
     v = C8.code_values(fmt)
     return np.flatnonzero(np.isnan(v))
