@@ -4,7 +4,7 @@ Argument marshalling only: every entry point forwards device pointers of torch
 tensors, sizes and the current CUDA stream to the C ABI declared in
 ``include/scout.h``; all arithmetic runs in the library's CUDA kernels.  There is
 no fallback: if ``libscout.so`` is missing or fails to load, every call raises.
-The calls around the tables and the 8-bit cache do the same in native code
+The calls around the tables, the 8-bit cache and a layer's rows do the same in native code
 (``csrc/binding.cpp``), the others through ``ctypes``.
 """
 from __future__ import annotations
@@ -21,7 +21,8 @@ __all__ = [
     "plan_recall", "plan_recall_pages", "recall_intervals", "cpu_attend", "RecallOp", "Launch", "Prepared",
     "INJECT_NONE", "INJECT_ABANDON", "INJECT_COPY_FAIL", "recall_gather_async", "CpuPool", "resident_list",
     "POOL_SUM", "build_tables", "append_kv", "append_kv8", "build_digest8", "sparse_attn8", "sparse_attn8_merge",
-    "sparse_attn8_workspace",
+    "sparse_attn8_workspace", "Rope", "rope", "rotate", "append_rotated_kv", "append_rotated_kv8", "predict_q_rotated",
+    "read_kv", "read_kv8", "add_norm",
 ]
 
 MINMAX = 0
@@ -88,6 +89,18 @@ _SIGS = {
                             _sz, _p, _p, _p], _i),
     "scout_sparse_attn8_merge": ([_i, _p, _p, _p, _p, _p, _i64, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _f, _p,
                                   _p, _p, _p, _p, _sz, _p, _p, _p], _i),
+    "scout_add_norm": ([_i, _p, _i64, _p, _p, _p, _i64, _f, _i, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _i, _i, _f,
+                        _p], _i),
+    "scout_rope_turns": ([ctypes.c_double, _i, _p, _p, _p], _i),
+    "scout_rotate": ([_p, _i64, _p, _i64, _p, _i, _i, _i, _p, _p, _f, _p], _i),
+    "scout_append_rotated_kv": ([_p, _i64, _p, _i64, _p, _p, _p, _f, _p, _i, _i, _i, _i, _p, _p, _i64, _p, _i64, _i, _p,
+                                 _p, _i64, _p, _p], _i),
+    "scout_append_rotated_kv8": ([_i, _p, _i64, _p, _i64, _i, _p, _p, _p, _f, _p, _p, _p, _i, _i, _i, _i, _i, _p, _p, _p,
+                                  _p, _i64, _p, _i64, _i, _p, _p, _i64, _p, _p], _i),
+    "scout_predict_q_rotated": ([_p, _p, _p, _i, _i, _i, _p, _p, _p, _f, _p, _p, _p], _i),
+    "scout_read_kv": ([_p, _p, _i64, _p, _p, _i, _i, _i, _i, _i, _p, _i, _p, _p, _i64, _i64, _i64, _i64, _i, _p, _p], _i),
+    "scout_read_kv8": ([_i, _p, _p, _p, _p, _i64, _p, _p, _i, _i, _i, _i, _i, _p, _i, _p, _p, _i64, _i64, _i64, _i64, _i,
+                        _p, _p], _i),
     "scout_plan_recall_pages": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _p, _i, _p], _i),
 }
 
@@ -409,6 +422,145 @@ def sparse_attn8_merge(q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len,
         raise ScoutError("O_cpu and lse_cpu must be CUDA tensors")
     return _native().sparse_attn8(q, K_pool, V_pool, K_scale, V_scale, page_table, seq_len, res_list, res_count, B, Hq,
                                   Hkv, P, k, scale, workspace, O_cpu, lse_cpu, O_out, lse_out, status, max_ctas, stream)
+
+
+# ---------------------------------------------------------------------------
+# a layer's rows: rotary positions, residual stream and norms, the cache read back
+# ---------------------------------------------------------------------------
+class RopeScaling(ctypes.Structure):
+    """scout_rope_scaling."""
+    _fields_ = [("kind", _i), ("factor", ctypes.c_double), ("original", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("amplitude", ctypes.c_double), ("divisors", _p)]
+
+
+class RopeArgs(ctypes.Structure):
+    """scout_rope."""
+    _fields_ = [("turns", _p), ("rot_dim", _i), ("layout", _i), ("amplitude", _f)]
+
+
+_LAYOUT = {"half": 0, "interleaved": 1}
+_SCALING = {"linear": 1, "ntk": 2, "rotations": 3, "index": 4, "divisors": 5}
+
+
+class Rope:
+    """Rotary positions of a model's heads: ``turns`` int64 [rot_dim / 2] on the device (each pair's angle a
+    position step, as a fraction of 2^64 of a turn), the number of channels turned, their layout and the
+    amplitude.  Made once by ``rope``, passed to every call that turns heads."""
+    __slots__ = ("turns", "rot_dim", "layout", "amplitude", "_args")
+
+    def __init__(self, turns, rot_dim, layout, amplitude):
+        if layout not in _LAYOUT:
+            raise ScoutError(f"layout must be 'half' or 'interleaved', got {layout!r}")
+        self.turns, self.rot_dim, self.layout, self.amplitude = turns, int(rot_dim), layout, float(amplitude)
+        self._args = (turns, self.rot_dim, _LAYOUT[layout], self.amplitude)
+
+
+def rope(base=10000.0, rot_dim=128, layout="half", scaling=None, device="cuda") -> Rope:
+    """Rotary positions with frequencies base^(-2i / rot_dim).
+
+    ``layout``: pairs (i, i + rot_dim / 2) ("half") or (2i, 2i + 1) ("interleaved"); rot_dim a multiple of
+    16, channels past it are not turned.  ``scaling`` (contexts longer than those trained on): None, or
+    a dict with "kind" and what it takes: "linear" and "ntk" (factor), "rotations" and "index" (factor,
+    original: the original length, low and high: the turns over it between which the slowing sets in;
+    1 and 4, or 1 and 32, unless given), "divisors" (divisors: one for each pair); and "amplitude" (by
+    default 1, of "index" 0.1 ln(factor) + 1).  The formulas are beside scout_rope_turns."""
+    import numpy as np
+
+    s = None
+    if scaling is not None:
+        more = dict(scaling)
+        kind = more.pop("kind", None)
+        if kind not in _SCALING:
+            raise ScoutError(f"scaling kind must be one of {', '.join(_SCALING)}, got {kind!r}")
+        s = RopeScaling(kind=_SCALING[kind], amplitude=float(more.pop("amplitude", None) or 0.0))
+        takes = {"rotations": ("factor", "original", "low", "high"), "divisors": ("divisors",)}
+        takes["index"] = takes["rotations"]
+        if kind in ("rotations", "index"):
+            more.setdefault("low", 1.0)
+            more.setdefault("high", 4.0 if kind == "rotations" else 32.0)
+        if set(more) != set(takes.get(kind, ("factor",))):
+            raise ScoutError(f"scaling {kind!r} takes {', '.join(takes.get(kind, ('factor',)))}, got {', '.join(more)}")
+        if kind == "divisors":
+            div = np.ascontiguousarray(more["divisors"], dtype=np.float64)
+            if div.shape != (rot_dim // 2,):
+                raise ScoutError(f"divisors must hold {rot_dim // 2} numbers, got {div.shape}")
+            s.divisors = div.ctypes.data
+        else:
+            for k, v in more.items():
+                setattr(s, k, float(v))
+    if layout not in _LAYOUT:
+        raise ScoutError(f"layout must be 'half' or 'interleaved', got {layout!r}")
+    turns = np.zeros(max(1, int(rot_dim) // 2), dtype=np.uint64)
+    amp = ctypes.c_float(0)
+    _check(lib().scout_rope_turns(float(base), int(rot_dim), None if s is None else ctypes.byref(s), turns.ctypes.data,
+                                  ctypes.byref(amp)), "scout_rope_turns")
+    return Rope(torch.from_numpy(turns.view(np.int64)).to(device), rot_dim, layout, amp.value)
+
+
+def rotate(x, positions, rope, norm=None, eps=1e-6, out=None, stream=None):
+    """Heads of bf16 rows x [n_tokens][heads][D] (token strides free), normalised by ``norm`` (bf16 [D], None: not)
+    and turned by ``positions`` int32 [n_tokens] -> out, bf16, alike (x itself for in place).  Rows with a
+    negative position are left alone."""
+    return _native().rotate(x, positions, *rope._args, norm, eps, out, stream)
+
+
+def append_rotated_kv(K_new, V_new, positions, rope, slot_map, Hkv, P, K_pool, V_pool, k_norm=None, q=None, q_norm=None,
+                      q_out=None, eps=1e-6, status=None, stream=None):
+    """append_kv with the keys normalised (``k_norm``) and turned by ``positions`` int32 [n_tokens] on their way, and
+    the same tokens' queries ``q`` [n_tokens][Hq][D] beside them (``q_norm``) into ``q_out`` (q itself for in
+    place, None: a new tensor) -> q_out, or None without q.  Rows with a negative position are left alone."""
+    return _native().append_rotated_kv(K_pool, V_pool, Hkv, P, K_new, V_new, positions, *rope._args, k_norm, eps, slot_map,
+                                       q, q_norm, q_out, status, stream)
+
+
+def append_rotated_kv8(K_new, V_new, rope, page_table, seq_len, B, Hkv, P, K_pool, V_pool, K_scale, V_scale, prev_len=None,
+                       positions=None, k_norm=None, q=None, q_norm=None, q_out=None, eps=1e-6, status=None, stream=None):
+    """append_kv8 with the keys normalised, turned and rounded to bf16 first, and the same tokens' queries beside
+    them, as append_rotated_kv -> q_out, or None without q.  ``positions``: by default each token's index in its
+    sequence.  Rows past the last new token are left alone, in q_out too."""
+    return _native().append_rotated_kv8(K_pool, V_pool, B, Hkv, P, K_new, V_new, *rope._args, k_norm, eps, page_table,
+                                        seq_len, K_scale, V_scale, prev_len, positions, q, q_norm, q_out, status, stream)
+
+
+def predict_q_rotated(X, W, positions, rope, norm=None, eps=1e-6, Q=None, status=None, max_ctas=None, stream=None):
+    """predict_q with the heads of X W^T normalised (``norm`` bf16 [128], None: not) and turned by ``positions`` int32
+    [M] before they are rounded -> Q bf16 [M][N].  Rows with a negative position are not written."""
+    return _native().predict_q_rotated(X, W, positions, *rope._args, norm, eps, Q, status, max_ctas, stream)
+
+
+def read_kv(K_pool, V_pool, page_table, seq_len, B, Hkv, P, K_out, V_out, block_list=None, status=None, stream=None):
+    """Blocks of a bf16 cache as rows in token order: K_out, V_out bf16 [B][Hkv][T][D] of any strides with contiguous
+    rows, on the device or in pinned host memory (what cpu_attend and the recalls read).  ``block_list``
+    int32 [n][2] of (unit, block), None: every valid block on the GPU.  Rows at and past a sequence's end stay."""
+    _native().read_kv(K_pool, V_pool, B, Hkv, P, None, None, page_table, seq_len, K_out, V_out, block_list, status, stream)
+    return K_out, V_out
+
+
+def read_kv8(K_pool, V_pool, K_scale, V_scale, page_table, seq_len, B, Hkv, P, K_out, V_out, block_list=None, status=None,
+             stream=None):
+    """read_kv of an 8-bit cache: code * scale, rounded to bf16."""
+    if K_scale is None or V_scale is None:
+        raise ScoutError("K_scale and V_scale must be CUDA tensors")
+    _native().read_kv(K_pool, V_pool, B, Hkv, P, K_scale, V_scale, page_table, seq_len, K_out, V_out, block_list, status,
+                      stream)
+    return K_out, V_out
+
+
+_NORM = {"rms": 0, "layer": 1}
+
+
+def add_norm(kind, Y, H, w, eps=1e-6, b=None, w_post=None, b_post=None, gate=None, alpha=1.0, H_out=None, X=None,
+             w_ahead=None, b_ahead=None, X_ahead=None, stream=None):
+    """H' = H + alpha * gate * p, with p = Y or norm(Y) * w_post + b_post, and X = norm(H') * w + b, in one pass
+    -> (H', X), or with ``w_ahead`` (H', X, X_ahead), X_ahead the same stream under the next layer's norm,
+    the input of its query prediction.
+
+    ``kind``: "rms" or "layer".  Y bf16 [M][N] (None: the norms alone), H and H' bf16 or fp32, X bf16; rows may be
+    strided, X is contiguous.  gate bf16 [N] or [M][N].  ``H_out`` may be H."""
+    if kind not in _NORM:
+        raise ScoutError(f"kind must be 'rms' or 'layer', got {kind!r}")
+    return _native().add_norm(_NORM[kind], Y, H, w, eps, b, w_post, b_post, gate, alpha, H_out, X, w_ahead, b_ahead, X_ahead,
+                              stream)
 
 
 def recall_async(ops, host_K, host_V, K_pool, V_pool, B, Hkv, P, nblk_cap, side_stream, wait_event=None,

@@ -25,7 +25,7 @@ LIBS = {
     "libscout.so": [os.path.join(PKG, "csrc", f) for f in
                     ("api.cu", "digest.cu", "score_topk.cu", "sparse_attn.cu", "merge.cu", "predict_q.cu",
                      "recall.cu", "lists.cu", "tables.cu", "append8.cu", "digest8.cu", "sparse_attn8.cu",
-                     "cpu_attend.cpp")],
+                     "rotate.cu", "rotate8.cu", "read.cu", "add_norm.cu", "rope.cpp", "cpu_attend.cpp")],
     "libscoutgen.so": [os.path.join(PKG, "workload", "gen.cu")],
 }
 # the native part of the Python binding: plain C++ against PyTorch's and Python's headers

@@ -37,6 +37,21 @@ CUresult encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, uint32_t rank, v
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+void* mapped_address(const void* p, size_t bytes) {
+  cudaPointerAttributes first, last;
+  const uint8_t* end = static_cast<const uint8_t*>(p) + bytes - 1;
+  if (cudaPointerGetAttributes(&first, p) != cudaSuccess || cudaPointerGetAttributes(&last, end) != cudaSuccess) {
+    cudaGetLastError();  // the lookup's error is this call's answer, not a sticky launch error
+    return nullptr;
+  }
+  if (first.type != cudaMemoryTypeHost || last.type != cudaMemoryTypeHost || first.devicePointer == nullptr ||
+      last.devicePointer == nullptr ||
+      static_cast<const uint8_t*>(last.devicePointer) - static_cast<const uint8_t*>(first.devicePointer) !=
+          static_cast<ptrdiff_t>(bytes - 1))
+    return nullptr;
+  return first.devicePointer;
+}
+
 }  // namespace scout
 
 extern "C" const char* scout_status_string(int status) {

@@ -1,4 +1,4 @@
-// The Python side of the tables, the cache writes and the 8-bit cache: arguments checked and handed to
+// The Python side of the tables, the cache writes, the 8-bit cache and a layer's row operators: arguments checked and handed to
 // the C ABI in one native call each.  A decode step's calls are short (3 to 7 us on the device), so
 // what their checks cost counts: with ctypes and a Python check per tensor they took 8 to 11 us of
 // host time and the attention 21, here 2.6 to 3.2 and 7 to 8 (two allocations and a launch of 2 us among
@@ -142,6 +142,42 @@ class Args {
     }
     *ld = *n > 1 ? t->stride(0) : Hkv * D;
     return t->data_ptr();
+  }
+  // rows [n][heads][D] with any number of heads
+  void* rows(const at::Tensor* t, const char* name, int64_t* n, int* heads, int64_t* D, int64_t* ld) {
+    if (!ok_) return nullptr;
+    if (t->scalar_type() != at::kBFloat16 || t->dim() != 3 || t->size(0) != (int)t->size(0) ||
+        t->size(1) != (int)t->size(1) || t->size(2) != (int)t->size(2)) {
+      fail("%s must be a bf16 CUDA tensor [n_tokens][heads][D] of 32-bit sizes", name);
+      return nullptr;
+    }
+    *n = t->size(0);
+    *heads = (int)t->size(1);
+    *D = t->size(2);
+    if (t->numel() > 0 && ((*D > 1 && t->stride(2) != 1) || (*heads > 1 && t->stride(1) != *D))) {
+      fail("%s: the heads of a token must be contiguous", name);
+      return nullptr;
+    }
+    *ld = *n > 1 ? t->stride(0) : *heads * *D;
+    return t->data_ptr();
+  }
+  // a matrix [M][N] whose rows are contiguous; ld: elements from a row to the next
+  void* matrix(const at::Tensor* t, const char* name, at::ScalarType type, int64_t M, int64_t N, int64_t* ld) {
+    if (!ok_ || t == nullptr) return nullptr;
+    if (t->scalar_type() != type || t->dim() != 2 || t->size(0) != M || t->size(1) != N ||
+        (M > 0 && N > 1 && t->stride(1) != 1)) {
+      fail("%s must be a %s CUDA tensor [%lld][%lld] with contiguous rows", name, c10::toString(type), (long long)M,
+           (long long)N);
+      return nullptr;
+    }
+    *ld = M > 1 ? t->stride(0) : N;
+    return t->data_ptr();
+  }
+  // A tensor on the call's device or in host memory.  (What kind of host memory the C ABI looks at.)
+  const at::Tensor* anywhere(const char* name) {
+    if (!ok_) return nullptr;
+    if (THPVariable_Check(*at_) && THPVariable_Unpack(*at_).is_cpu()) return &THPVariable_Unpack(*at_++);
+    return tensor(name);
   }
   // None (the current stream of the call's device) or a torch.cuda.Stream; the last argument
   cudaStream_t stream(bool* given = nullptr) {
@@ -429,6 +465,340 @@ PyObject* sparse_attn8(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// turns, rot_dim, layout, amplitude
+scout_rope rope_of(Args& a) {
+  scout_rope r = {};
+  const at::Tensor* t = a.tensor("rope.turns");
+  r.rot_dim = a.i32();
+  r.layout = a.i32();
+  r.amplitude = (float)a.real();
+  r.turns = static_cast<const uint64_t*>(a.sized(t, "rope.turns", at::kLong, r.rot_dim / 2));
+  return r;
+}
+
+// Outputs made here come from the stream they are written on (`named`: one that was given).
+at::Tensor make(const at::Tensor* like, at::IntArrayRef sizes, at::ScalarType type, bool named, cudaStream_t st,
+                int device) {
+  c10::cuda::OptionalCUDAStreamGuard on;
+  if (named) on.reset_stream(c10::cuda::getStreamFromExternal(st, (c10::DeviceIndex)device));
+  return at::empty(sizes, at::TensorOptions().device(like->device()).dtype(type));
+}
+
+// (x, positions, turns, rot_dim, layout, amplitude, norm | None, eps, out | None, stream | None) -> out
+PyObject* rotate(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Args a(args, n, 10);
+    const at::Tensor* x = a.tensor("x");
+    int64_t rows = 0, D = 0, ld_x = 0, rows_o = 0, D_o = 0, ld_o = 0;
+    int heads = 0, heads_o = 0;
+    const void* x_p = a.rows(x, "x", &rows, &heads, &D, &ld_x);
+    auto pos = static_cast<const int32_t*>(a.sized("positions", at::kInt, rows));
+    const scout_rope rope = rope_of(a);
+    const void* norm = a.optional("norm", at::kBFloat16, D);
+    const float eps = (float)a.real();
+    const at::Tensor* given = a.optional("out");
+    if (given != nullptr) {
+      a.rows(given, "out", &rows_o, &heads_o, &D_o, &ld_o);
+      if (rows_o != rows || heads_o != heads || D_o != D) a.fail("out must have the shape of x");
+    }
+    bool named = false;
+    const cudaStream_t st = a.stream(&named);
+    if (!a.ok()) return nullptr;
+    const at::Tensor out = given != nullptr ? *given : make(x, {rows, heads, D}, at::kBFloat16, named, st, a.device());
+    if (given == nullptr) ld_o = (int64_t)heads * D;
+    if (rows > 0) {
+      void* o_p = out.data_ptr();
+      int rc;
+      Py_BEGIN_ALLOW_THREADS;
+      rc = scout_rotate(x_p, ld_x, o_p, ld_o, pos, (int)rows, heads, (int)D, &rope, norm, eps, st);
+      Py_END_ALLOW_THREADS;
+      if (rc != SCOUT_OK) return done(rc, "scout_rotate");
+    }
+    return THPVariable_Wrap(out);
+  });
+}
+
+// The queries beside a write: q | None, q_norm | None, q_out | None, of n tokens.
+struct Queries {
+  const at::Tensor *q = nullptr, *given = nullptr;
+  const void *p = nullptr, *norm = nullptr;
+  at::Tensor out;
+  int64_t ld = 0, ld_out = 0;
+  int heads = 0;
+  void read(Args& a, int64_t tokens, int64_t D) {
+    q = a.optional("q");
+    int64_t n = tokens, d = D, n_o = 0, d_o = 0;
+    int h_o = 0;
+    if (q != nullptr) {
+      p = a.rows(q, "q", &n, &heads, &d, &ld);
+      if (n != tokens || d != D || heads == 0) a.fail("q must hold the tokens of K_new, with heads of their size");
+    }
+    norm = a.optional("q_norm", at::kBFloat16, D);
+    given = a.optional("q_out");
+    if (q == nullptr && (norm != nullptr || given != nullptr)) a.fail("q_norm and q_out need q");
+    if (given != nullptr) {
+      a.rows(given, "q_out", &n_o, &h_o, &d_o, &ld_out);
+      if (n_o != n || h_o != heads || d_o != d) a.fail("q_out must have the shape of q");
+    }
+  }
+  // after the stream is known
+  void* output(Args& a, int64_t tokens, int64_t D, bool named, cudaStream_t st) {
+    if (q == nullptr) return nullptr;
+    out = given != nullptr ? *given : make(q, {tokens, heads, D}, at::kBFloat16, named, st, a.device());
+    if (given == nullptr) ld_out = (int64_t)heads * D;
+    return out.data_ptr();
+  }
+  PyObject* result(int rc, const char* what) {
+    if (rc != SCOUT_OK || q == nullptr) return done(rc, what);
+    return THPVariable_Wrap(out);
+  }
+};
+
+// (K_pool, V_pool, Hkv, P, K_new, V_new, positions, turns, rot_dim, layout, amplitude, k_norm | None, eps, slot_map,
+//  q | None, q_norm | None, q_out | None, status | None, stream | None) -> q_out | None
+PyObject* append_rotated_kv(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Args a(args, n, 19);
+    const at::Tensor *kp = a.tensor("K_pool"), *vp = a.tensor("V_pool");
+    const int Hkv = a.i32(), P = a.i32();
+    if (a.ok() && (kp->dim() != 3 || kp->size(2) != (int)kp->size(2)))
+      a.fail("K_pool must be a CUDA tensor [n_slots][%d][D]", P);
+    if (!a.ok()) return nullptr;
+    const int64_t slots = kp->size(0), D = kp->size(2), pool = count(slots, P, D);
+    void *kpp = a.sized(kp, "K_pool", at::kBFloat16, pool), *vpp = a.sized(vp, "V_pool", at::kBFloat16, pool);
+    int64_t nk = 0, nv = 0, ld_k = 0, ld_v = 0;
+    void *k = a.rows("K_new", Hkv, D, &nk, &ld_k), *v = a.rows("V_new", Hkv, D, &nv, &ld_v);
+    if (nk != nv) a.fail("K_new and V_new must hold the same tokens");
+    auto pos = static_cast<const int32_t*>(a.sized("positions", at::kInt, nk));
+    const scout_rope rope = rope_of(a);
+    const void* k_norm = a.optional("k_norm", at::kBFloat16, D);
+    const float eps = (float)a.real();
+    auto map = static_cast<const int64_t*>(a.sized("slot_map", at::kLong, count(nk, Hkv)));
+    Queries q;
+    q.read(a, nk, D);
+    auto status = static_cast<int32_t*>(a.optional("status", at::kInt, 1));
+    bool named = false;
+    const cudaStream_t st = a.stream(&named);
+    if (!a.ok()) return nullptr;
+    void* q_out = q.output(a, nk, D, named, st);
+    int rc = SCOUT_OK;
+    if (nk > 0) {
+      Py_BEGIN_ALLOW_THREADS;
+      rc = scout_append_rotated_kv(k, ld_k, v, ld_v, pos, &rope, k_norm, eps, map, (int)nk, Hkv, (int)D, P, kpp, vpp,
+                                   slots, q.p, q.ld, q.heads, q.norm, q_out, q.ld_out, status, st);
+      Py_END_ALLOW_THREADS;
+    }
+    return q.result(rc, "scout_append_rotated_kv");
+  });
+}
+
+// (K_pool, V_pool, B, Hkv, P, K_new, V_new, turns, rot_dim, layout, amplitude, k_norm | None, eps, page_table, seq_len,
+//  K_scale, V_scale, prev_len | None, positions | None, q | None, q_norm | None, q_out | None, status | None,
+//  stream | None) -> q_out | None
+PyObject* append_rotated_kv8(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Args a(args, n, 24);
+    const at::Tensor *kp = a.tensor("K_pool"), *vp = a.tensor("V_pool");
+    const int B = a.i32(), Hkv = a.i32(), P = a.i32();
+    const int fmt = format_of(a, kp, vp, P);
+    if (!a.ok()) return nullptr;
+    const at::ScalarType type = kp->scalar_type();
+    const int64_t slots = kp->size(0), D = kp->size(2), pool = count(slots, P, D);
+    void *kpp = a.sized(kp, "K_pool", type, pool), *vpp = a.sized(vp, "V_pool", type, pool);
+    int64_t nk = 0, nv = 0, ld_k = 0, ld_v = 0;
+    void *k = a.rows("K_new", Hkv, D, &nk, &ld_k), *v = a.rows("V_new", Hkv, D, &nv, &ld_v);
+    if (nk != nv) a.fail("K_new and V_new must hold the same tokens");
+    const scout_rope rope = rope_of(a);
+    const void* k_norm = a.optional("k_norm", at::kBFloat16, D);
+    const float eps = (float)a.real();
+    const at::Tensor* pt = a.tensor("page_table");
+    const int cap = last_size(a, pt, "page_table");
+    auto pt_p = static_cast<const int32_t*>(a.sized(pt, "page_table", at::kInt, count(B, Hkv, cap)));
+    auto seq = static_cast<const int32_t*>(a.sized("seq_len", at::kInt, B));
+    auto ks = static_cast<float*>(a.sized("K_scale", at::kFloat, slots));
+    auto vs = static_cast<float*>(a.sized("V_scale", at::kFloat, slots));
+    auto prev = static_cast<const int32_t*>(a.optional("prev_len", at::kInt, B));
+    auto pos = static_cast<const int32_t*>(a.optional("positions", at::kInt, nk));
+    Queries q;
+    q.read(a, nk, D);
+    auto status = static_cast<int32_t*>(a.optional("status", at::kInt, 1));
+    bool named = false;
+    const cudaStream_t st = a.stream(&named);
+    if (!a.ok()) return nullptr;
+    void* q_out = q.output(a, nk, D, named, st);
+    int rc;
+    Py_BEGIN_ALLOW_THREADS;
+    rc = scout_append_rotated_kv8(fmt, k, ld_k, v, ld_v, (int)nk, pos, &rope, k_norm, eps, prev, seq, pt_p, B, Hkv, (int)D,
+                                  P, cap, kpp, vpp, ks, vs, slots, q.p, q.ld, q.heads, q.norm, q_out, q.ld_out, status, st);
+    Py_END_ALLOW_THREADS;
+    return q.result(rc, "scout_append_rotated_kv8");
+  });
+}
+
+// (X, W, positions, turns, rot_dim, layout, amplitude, norm | None, eps, Q | None, status | None, max_ctas | None,
+//  stream | None) -> Q
+PyObject* predict_q_rotated(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Args a(args, n, 13);
+    const at::Tensor *x = a.tensor("X"), *w = a.tensor("W");
+    if (a.ok() && (x->dim() != 2 || w->dim() != 2 || x->size(0) != (int)x->size(0) || x->size(1) != (int)x->size(1) ||
+                   w->size(0) != (int)w->size(0)))
+      a.fail("X must be [M][K] and W [N][K], of 32-bit sizes");
+    if (!a.ok()) return nullptr;
+    const int64_t M = x->size(0), K = x->size(1), N = w->size(0);
+    const void *x_p = a.sized(x, "X", at::kBFloat16, count(M, K)), *w_p = a.sized(w, "W", at::kBFloat16, count(N, K));
+    auto pos = static_cast<const int32_t*>(a.sized("positions", at::kInt, M));
+    const scout_rope rope = rope_of(a);
+    const void* norm = a.optional("norm", at::kBFloat16, 128);
+    const float eps = (float)a.real();
+    const at::Tensor* given = a.optional("Q");
+    if (given != nullptr) a.sized(given, "Q", at::kBFloat16, count(M, N));
+    auto status = static_cast<int32_t*>(a.optional("status", at::kInt, 1));
+    PyObject* max_ctas = a.raw();
+    bool named = false;
+    const cudaStream_t st = a.stream(&named);
+    scout_launch launch = {};
+    if (a.ok() && max_ctas != Py_None) {
+      const long m = PyLong_AsLong(max_ctas);
+      if (m == -1 && PyErr_Occurred()) return nullptr;
+      if (m < 0 || m != (int)m) a.fail("max_ctas must be >= 0");
+      launch.max_ctas = (int)m;
+    }
+    if (!a.ok()) return nullptr;
+    const at::Tensor Q = given != nullptr ? *given : make(x, {M, N}, at::kBFloat16, named, st, a.device());
+    void* q_p = Q.data_ptr();
+    int rc;
+    Py_BEGIN_ALLOW_THREADS;
+    rc = scout_predict_q_rotated(x_p, w_p, q_p, (int)M, (int)N, (int)K, pos, &rope, norm, eps, status, &launch, st);
+    Py_END_ALLOW_THREADS;
+    return rc != SCOUT_OK ? done(rc, "scout_predict_q_rotated") : THPVariable_Wrap(Q);
+  });
+}
+
+// (K_pool, V_pool, B, Hkv, P, K_scale | None, V_scale | None, page_table, seq_len, K_out, V_out, block_list | None,
+//  status | None, stream | None).  Without scales the pools are bf16.
+PyObject* read_kv(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Args a(args, n, 14);
+    const at::Tensor *kp = a.tensor("K_pool"), *vp = a.tensor("V_pool");
+    const int B = a.i32(), Hkv = a.i32(), P = a.i32();
+    const at::Tensor *ks = a.optional("K_scale"), *vs = a.optional("V_scale");
+    const bool codes = ks != nullptr || vs != nullptr;
+    if (codes && (ks == nullptr || vs == nullptr)) a.fail("K_scale and V_scale must be CUDA tensors");
+    if (a.ok() && (kp->dim() != 3 || kp->size(2) != (int)kp->size(2)))
+      a.fail("K_pool must be a CUDA tensor [n_slots][%d][D]", P);
+    const int fmt = codes ? format_of(a, kp, vp, P) : 0;
+    if (!a.ok()) return nullptr;
+    const at::ScalarType type = codes ? kp->scalar_type() : at::kBFloat16;
+    const int64_t slots = kp->size(0), D = kp->size(2), pool = count(slots, P, D);
+    const void *kpp = a.sized(kp, "K_pool", type, pool), *vpp = a.sized(vp, "V_pool", type, pool);
+    auto ks_p = static_cast<const float*>(codes ? a.sized(ks, "K_scale", at::kFloat, slots) : nullptr);
+    auto vs_p = static_cast<const float*>(codes ? a.sized(vs, "V_scale", at::kFloat, slots) : nullptr);
+    const at::Tensor* pt = a.tensor("page_table");
+    const int cap = last_size(a, pt, "page_table");
+    auto pt_p = static_cast<const int32_t*>(a.sized(pt, "page_table", at::kInt, count(B, Hkv, cap)));
+    auto seq = static_cast<const int32_t*>(a.sized("seq_len", at::kInt, B));
+    const at::Tensor* out[2] = {a.anywhere("K_out"), a.anywhere("V_out")};
+    int64_t stride[3] = {0, 0, 0}, T = 0;
+    if (a.ok()) {
+      const at::Tensor &k = *out[0], &v = *out[1];
+      if (k.scalar_type() != at::kBFloat16 || v.scalar_type() != at::kBFloat16 || k.dim() != 4 || k.size(0) != B ||
+          k.size(1) != Hkv || k.size(3) != D || v.sizes() != k.sizes() || k.is_cuda() != v.is_cuda())
+        a.fail("K_out and V_out must be bf16 tensors [%d][%d][T][%lld] alike", B, Hkv, (long long)D);
+      else if (k.numel() > 0)
+        for (int i = 0; i < 4; ++i) {
+          if (k.size(i) == 1) continue;
+          if (k.stride(i) != v.stride(i) || k.stride(i) == 0 || (i == 3 && k.stride(3) != 1))
+            a.fail("K_out and V_out must have the same strides, with contiguous rows that do not overlap");
+          else if (i < 3)
+            stride[i] = k.stride(i);
+        }
+      T = k.dim() == 4 ? k.size(2) : 0;
+    }
+    const at::Tensor* list = a.optional("block_list");
+    const int n_list = first_size(a, list, "block_list");
+    auto list_p =
+        static_cast<const int32_t*>(list != nullptr ? a.sized(list, "block_list", at::kInt, count(n_list, 2)) : nullptr);
+    auto status = static_cast<int32_t*>(a.optional("status", at::kInt, 1));
+    const cudaStream_t st = a.stream();
+    if (!a.ok()) return nullptr;
+    if (list != nullptr && n_list == 0) Py_RETURN_NONE;  // an empty list, which has no address, is not "all blocks"
+    void *ko = out[0]->data_ptr(), *vo = out[1]->data_ptr();
+    const int host = out[0]->is_cuda() ? 0 : 1;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS;
+    rc = codes ? scout_read_kv8(fmt, kpp, vpp, ks_p, vs_p, slots, pt_p, seq, B, Hkv, (int)D, P, cap, list_p, n_list, ko, vo,
+                                stride[0], stride[1], stride[2], T, host, status, st)
+               : scout_read_kv(kpp, vpp, slots, pt_p, seq, B, Hkv, (int)D, P, cap, list_p, n_list, ko, vo, stride[0],
+                               stride[1], stride[2], T, host, status, st);
+    Py_END_ALLOW_THREADS;
+    return done(rc, codes ? "scout_read_kv8" : "scout_read_kv");
+  });
+}
+
+// (kind, Y | None, H, w, eps, b | None, w_post | None, b_post | None, gate | None, alpha, H_out | None, X | None,
+//  w_ahead | None, b_ahead | None, X_ahead | None, stream | None) -> (H_out, X) or (H_out, X, X_ahead)
+PyObject* add_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Args a(args, n, 16);
+    const int kind = a.i32();
+    const at::Tensor *y = a.optional("Y"), *h = a.tensor("H"), *w = a.tensor("w");
+    const float eps = (float)a.real();
+    if (a.ok() && (h->dim() != 2 || h->size(0) != (int)h->size(0) || h->size(1) != (int)h->size(1)))
+      a.fail("H must be [M][N], of 32-bit sizes");
+    if (!a.ok()) return nullptr;
+    const int64_t M = h->size(0), N = h->size(1);
+    const at::ScalarType wide = h->scalar_type();
+    if (wide != at::kBFloat16 && wide != at::kFloat) a.fail("H must be bf16 or fp32, got %s", c10::toString(wide));
+    int64_t ld_y = N, ld_h = N, ld_o = N, ld_g = 0;
+    const void* y_p = a.matrix(y, "Y", at::kBFloat16, M, N, &ld_y);
+    const void* h_p = a.matrix(h, "H", wide, M, N, &ld_h);
+    const void* w_p = a.sized(w, "w", at::kBFloat16, N);
+    const void* b_p = a.optional("b", at::kBFloat16, N);
+    const void *wp_p = a.optional("w_post", at::kBFloat16, N), *bp_p = a.optional("b_post", at::kBFloat16, N);
+    const at::Tensor* gate = a.optional("gate");
+    const void* g_p = nullptr;
+    if (a.ok() && gate != nullptr) {
+      g_p = gate->dim() == 1 ? a.sized(gate, "gate", at::kBFloat16, N)
+                             : a.matrix(gate, "gate", at::kBFloat16, M, N, &ld_g);
+      if (gate->dim() == 1) ld_g = 0;
+    }
+    const float alpha = (float)a.real();
+    const at::Tensor *h_out = a.optional("H_out"), *x = a.optional("X");
+    a.matrix(h_out, "H_out", wide, M, N, &ld_o);
+    if (h_out != nullptr && y == nullptr) a.fail("H_out needs Y: without it the stream stays as it is");
+    if (x != nullptr) a.sized(x, "X", at::kBFloat16, count(M, N));
+    const void* wa_p = a.optional("w_ahead", at::kBFloat16, N);
+    const void* ba_p = a.optional("b_ahead", at::kBFloat16, N);
+    const at::Tensor* xa = a.optional("X_ahead");
+    if (xa != nullptr) a.sized(xa, "X_ahead", at::kBFloat16, count(M, N));
+    if (wa_p == nullptr && (ba_p != nullptr || xa != nullptr)) a.fail("b_ahead and X_ahead need w_ahead");
+    bool named = false;
+    const cudaStream_t st = a.stream(&named);
+    if (!a.ok()) return nullptr;
+    at::Tensor H_out, X, XA;
+    H_out = h_out != nullptr ? *h_out : y == nullptr ? *h : make(h, {M, N}, wide, named, st, a.device());
+    X = x != nullptr ? *x : make(h, {M, N}, at::kBFloat16, named, st, a.device());
+    if (wa_p != nullptr) XA = xa != nullptr ? *xa : make(h, {M, N}, at::kBFloat16, named, st, a.device());
+    if (M > 0) {
+      void *ho_p = y != nullptr ? H_out.data_ptr() : nullptr, *x_p = X.data_ptr(),
+           *xa_p = wa_p != nullptr ? XA.data_ptr() : nullptr;
+      int rc;
+      Py_BEGIN_ALLOW_THREADS;
+      rc = scout_add_norm(kind, y_p, ld_y, wp_p, bp_p, g_p, ld_g, alpha, wide == at::kFloat ? SCOUT_FP32 : SCOUT_BF16, h_p,
+                          ld_h, ho_p, ld_o, w_p, b_p, x_p, wa_p, ba_p, xa_p, (int)M, (int)N, eps, st);
+      Py_END_ALLOW_THREADS;
+      if (rc != SCOUT_OK) return done(rc, "scout_add_norm");
+    }
+    PyObject* out[3] = {THPVariable_Wrap(H_out), THPVariable_Wrap(X), wa_p != nullptr ? THPVariable_Wrap(XA) : nullptr};
+    PyObject* all = nullptr;
+    if (out[0] != nullptr && out[1] != nullptr && (wa_p == nullptr || out[2] != nullptr))
+      all = wa_p != nullptr ? PyTuple_Pack(3, out[0], out[1], out[2]) : PyTuple_Pack(2, out[0], out[1]);
+    for (PyObject* o : out) Py_XDECREF(o);
+    return all;
+  });
+}
+
 // (ScoutError, torch.OutOfMemoryError)
 PyObject* set_errors(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != 2) {
@@ -449,6 +819,12 @@ PyMethodDef g_methods[] = {{"build_tables", fast(build_tables), METH_FASTCALL, n
                            {"append_kv8", fast(append_kv8), METH_FASTCALL, nullptr},
                            {"build_digest8", fast(build_digest8), METH_FASTCALL, nullptr},
                            {"sparse_attn8", fast(sparse_attn8), METH_FASTCALL, nullptr},
+                           {"rotate", fast(rotate), METH_FASTCALL, nullptr},
+                           {"append_rotated_kv", fast(append_rotated_kv), METH_FASTCALL, nullptr},
+                           {"append_rotated_kv8", fast(append_rotated_kv8), METH_FASTCALL, nullptr},
+                           {"predict_q_rotated", fast(predict_q_rotated), METH_FASTCALL, nullptr},
+                           {"read_kv", fast(read_kv), METH_FASTCALL, nullptr},
+                           {"add_norm", fast(add_norm), METH_FASTCALL, nullptr},
                            {"set_errors", fast(set_errors), METH_FASTCALL, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -65,6 +65,37 @@ __device__ __forceinline__ uint32_t scale_exponent(float amax) {
 }
 __device__ __forceinline__ float pow2_biased(uint32_t e) { return __uint_as_float(e << 23); }
 
+// Magnitudes of bf16 pairs, and the codes of bf16 values and of codes at another scale, for the writers.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t x) {
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                   __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x)));  // passes over NaN
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// the same with infinities (and NaN) as zero
+__device__ __forceinline__ uint32_t finite2(uint32_t x) {
+  return (((x & 0x7f80u) == 0x7f80u) ? 0u : (x & 0xffffu)) |
+         (((x & 0x7f800000u) == 0x7f800000u) ? 0u : (x & 0xffff0000u));
+}
+
+template <int F>
+__device__ __forceinline__ uint2 encode8(const uint4& v, float inv) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = Fp8<F>::pack(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// Codes at the old scale -> codes at the new one; ratio = old / new.
+template <int F>
+__device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
+  uint32_t lo, hi;
+  unpack4<F>(w, lo, hi);
+  const float2 a = half2_floats(lo), b = half2_floats(hi);
+  return (uint32_t)Fp8<F>::pack(a.x * ratio, a.y * ratio) |
+         ((uint32_t)Fp8<F>::pack(b.x * ratio, b.y * ratio) << 16);
+}
+
 inline bool valid_fp8(int fmt) { return fmt == SCOUT_FP8_E4M3 || fmt == SCOUT_FP8_E5M2; }
 
 // ---------------------------------------------------------------------------

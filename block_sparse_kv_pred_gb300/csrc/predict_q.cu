@@ -16,7 +16,13 @@
 // (distributed shared memory), then sums the partials of its own columns and writes
 // them as bf16 Q.  No global scratch is used.
 
-#include "common.cuh"
+//
+// scout_predict_q_rotated is the same kernel with another last step: a tile is one head, so a
+// CTA holds whole heads of its batch columns.  The sums go to shared memory in fp32, eight lanes
+// take a head (rotate.cuh), normalise and turn it, and store it rounded once, 16 bytes a lane.
+// The cosines and sines are made while W streams in.
+
+#include "rotate.cuh"
 
 namespace scout {
 namespace {
@@ -28,6 +34,7 @@ constexpr int kStages = 16;  // upper bound; the ring takes what shared memory h
 constexpr int kThreadsQ = 128;
 constexpr int kMaxN = 256;    // padded batch (MMA N) limit
 constexpr int kWTileBytes = kBM * kBK * 2;  // 16 KiB
+constexpr int kRingBytes = 224 * 1024;      // of shared memory, at most
 
 // --- cluster PTX --------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -57,7 +64,14 @@ struct GemmArgs {
   int M, N, n_pad, tmem_cols, kblocks, stages, x_tile_bytes;
   int kps;  // k-blocks per ring stage
   int32_t* status;
+  // of the rotated form
+  const int32_t* positions;
+  const __nv_bfloat16* norm;
+  Rope rope;
+  float eps;
 };
+
+constexpr int kPlain = -1;  // no rotary layout: the sums are the result
 
 // A ring stage holds nk <= kps consecutive k-blocks: their W tiles first, then their X tiles.
 // One arrival expects both; the W and the X copies may be issued apart.
@@ -72,6 +86,7 @@ __device__ __forceinline__ void load_x(uint8_t* st, const CUtensorMap* tmX, cons
     tma_load_2d(st + a.kps * kWTileBytes + j * a.x_tile_bytes, tmX, (kb + j) * kBK, 0, bar);
 }
 
+template <int LAYOUT>
 __global__ void __launch_bounds__(kThreadsQ, 1) predict_q_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                  const __grid_constant__ CUtensorMap tmX,
                                                                  const GemmArgs a) {
@@ -110,6 +125,17 @@ __global__ void __launch_bounds__(kThreadsQ, 1) predict_q_kernel(const __grid_co
     for (int i = 0; i < first; ++i) load_x(base + i * stage_bytes, &tmX, a, kb0 + i * a.kps, nk_of(i), &full_bar[i]);
   }
   if (warp == 2) tmem_alloc(&tmem_slot, (uint32_t)a.tmem_cols);
+  // rotated: the CTA's column k (of its groups, in order) is batch row m_of(k); eight lanes take one
+  const int sub = lane & 7;
+  auto m_of = [&](int k) { return ((int)rank + (k >> 3) * (int)S) * 8 + (k & 7); };
+  int pos = -1;  // and turn: of the lane's column among the CTA's first 16
+  Turn turn;
+  if constexpr (LAYOUT != kPlain) {
+    wait_prerequisites();  // the positions may be an earlier kernel's, as X
+    const int m = m_of(warp * 4 + (lane >> 3));
+    pos = m < a.M ? a.positions[m] : -1;
+    turn = lane_turn(a.rope, sub, (uint32_t)max(pos, 0));
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -169,6 +195,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) predict_q_kernel(const __grid_co
   const int ngroups = a.n_pad / 8;
   const int owned = (ngroups + (int)S - 1) / (int)S;
   float* recv = reinterpret_cast<float*>(base);  // the stage ring is idle now
+  float* mine = recv + (int)rank * owned * 8 * kBM;  // this CTA's own slots: no peer writes them
   float v[8];
   if (S > 1) {
     cluster_sync();  // every CTA of the cluster is done with its ring: it may be written
@@ -191,10 +218,52 @@ __global__ void __launch_bounds__(kThreadsQ, 1) predict_q_kernel(const __grid_co
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += src[e * kBM];
     }
+    if constexpr (LAYOUT == kPlain) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int m = g * 8 + e;
-      if (m < a.M && row < a.N) a.Q[(int64_t)m * a.N + row] = __float2bfloat16_rn(v[e]);
+      for (int e = 0; e < 8; ++e) {
+        const int m = g * 8 + e;
+        if (m < a.M && row < a.N) a.Q[(int64_t)m * a.N + row] = __float2bfloat16_rn(v[e]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mine[((g / (int)S) * 8 + e) * kBM + r_local] = v[e];
+    }
+  }
+  if constexpr (LAYOUT != kPlain) {
+    __syncthreads();
+    const int2 at = lane_chunks<LAYOUT>(sub, a.rope.n);
+    float w[16];
+    if (a.norm != nullptr)
+      unpack16(__ldg(reinterpret_cast<const uint4*>(a.norm + at.x)), __ldg(reinterpret_cast<const uint4*>(a.norm + at.y)),
+               w);
+    const int columns = (ngroups - (int)rank + (int)S - 1) / (int)S * 8;  // of this CTA
+    for (int k0 = 0; k0 < columns; k0 += 16) {
+      const int k = k0 + warp * 4 + (lane >> 3);
+      const int m = m_of(k);
+      const bool live = k < columns && m < a.M;
+      if (k0 > 0) {
+        pos = live ? a.positions[m] : -1;
+        turn = lane_turn(a.rope, sub, (uint32_t)max(pos, 0));
+      }
+      float x[16];
+      const float4* src = reinterpret_cast<const float4*>(mine + (live ? k : 0) * kBM);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 f = src[((i < 2 ? at.x : at.y) >> 2) + (i & 1)];
+        x[4 * i] = f.x;
+        x[4 * i + 1] = f.y;
+        x[4 * i + 2] = f.z;
+        x[4 * i + 3] = f.w;
+      }
+      if (a.norm != nullptr) norm_head(x, w, a.eps);
+      turn_head<LAYOUT>(x, turn, sub < a.rope.n);
+      uint4 lo, hi;
+      pack16(x, lo, hi);
+      if (live && pos >= 0) {
+        __nv_bfloat16* dst = a.Q + (int64_t)m * a.N + tile * kBM;
+        *reinterpret_cast<uint4*>(dst + at.x) = lo;
+        *reinterpret_cast<uint4*>(dst + at.y) = hi;
+      }
     }
   }
   tc_fence_before();
@@ -211,17 +280,14 @@ bool make_map(CUtensorMap* map, const void* ptr, int rows, int cols, int box_row
                       CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
 }
 
-}  // namespace
-}  // namespace scout
-
-extern "C" int scout_predict_q(const void* X, const void* W, void* Q, int M, int N, int K, int32_t* dev_status,
-                               const scout_launch* launch, cudaStream_t stream) {
-  using namespace scout;
+template <int LAYOUT>
+int predict(const void* X, const void* W, void* Q, int M, int N, int K, const int32_t* positions, const scout_rope* rope,
+            const void* norm, float eps, int32_t* dev_status, const scout_launch* launch, cudaStream_t stream) {
   if (X == nullptr || W == nullptr || Q == nullptr || M <= 0 || N <= 0 || K <= 0) return SCOUT_ERR_INVALID_ARG;
   if (launch != nullptr && launch->max_ctas < 0) return SCOUT_ERR_INVALID_ARG;
   if (M > kMaxN || N % kBM != 0 || K % kBK != 0 || !aligned16(X) || !aligned16(W) || !aligned16(Q))
     return SCOUT_ERR_UNSUPPORTED;
-  GemmArgs a;
+  GemmArgs a = {};
   a.Q = static_cast<__nv_bfloat16*>(Q);
   a.M = M;
   a.N = N;
@@ -232,11 +298,16 @@ extern "C" int scout_predict_q(const void* X, const void* W, void* Q, int M, int
   a.x_tile_bytes = (a.n_pad * 128 + 1023) / 1024 * 1024;
   // ~220 KB in flight per SM, in stages of up to kMaxKps k-blocks (the fewer the stages, the
   // fewer barrier round trips per byte) but at least two, so that copies and MMAs overlap
-  constexpr int kRingBytes = 224 * 1024;
   a.kps = max(1, min(kMaxKps, kRingBytes / 2 / (kWTileBytes + a.x_tile_bytes)));
   const int stage_bytes = a.kps * (kWTileBytes + a.x_tile_bytes);
   a.stages = min(kStages, kRingBytes / stage_bytes);
   a.status = dev_status;
+  if constexpr (LAYOUT != kPlain) {
+    a.positions = positions;
+    a.norm = static_cast<const __nv_bfloat16*>(norm);
+    a.rope = rope_of(rope);
+    a.eps = eps;
+  }
   const int tiles = N / kBM;
   const int cap = launch != nullptr && launch->max_ctas > 0 ? launch->max_ctas : sm_count();
   const int S = max(1, min(min(8, a.kblocks), cap / tiles));  // split-K so tiles x S fits the CTA budget
@@ -244,7 +315,11 @@ extern "C" int scout_predict_q(const void* X, const void* W, void* Q, int M, int
   const size_t smem = 1024 + (size_t)max(a.stages * stage_bytes, S * owned * 8 * kBM * 4);
   CUtensorMap tmW, tmX;
   if (!make_map(&tmW, W, N, K, kBM) || !make_map(&tmX, X, M, K, a.n_pad)) return SCOUT_ERR_UNSUPPORTED;
-  if (cudaFuncSetAttribute(predict_q_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  // the same limit for every call: calls on several host threads do not lower it for one another (the
+  // exchange, at most (n_pad / 8 + S - 1) * 4 KB, is smaller than the ring's bound)
+  static_assert((kMaxN / 8 + 7) * 8 * kBM * 4 <= kRingBytes, "the exchange fits where the ring does");
+  if (cudaFuncSetAttribute(predict_q_kernel<LAYOUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kRingBytes) !=
+      cudaSuccess)
     return SCOUT_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)tiles, (unsigned)S, 1);
@@ -258,6 +333,25 @@ extern "C" int scout_predict_q(const void* X, const void* W, void* Q, int M, int
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = early_start_attrs(launch, attr, 1);
-  if (cudaLaunchKernelEx(&cfg, predict_q_kernel, tmW, tmX, a) != cudaSuccess) return SCOUT_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, predict_q_kernel<LAYOUT>, tmW, tmX, a) != cudaSuccess) return SCOUT_ERR_CUDA;
   return launch_status();
+}
+
+}  // namespace
+}  // namespace scout
+
+extern "C" int scout_predict_q(const void* X, const void* W, void* Q, int M, int N, int K, int32_t* dev_status,
+                               const scout_launch* launch, cudaStream_t stream) {
+  return scout::predict<scout::kPlain>(X, W, Q, M, N, K, nullptr, nullptr, nullptr, 0.f, dev_status, launch, stream);
+}
+
+extern "C" int scout_predict_q_rotated(const void* X, const void* W, void* Q, int M, int N, int K,
+                                       const int32_t* positions, const scout_rope* rope, const void* norm, float eps,
+                                       int32_t* dev_status, const scout_launch* launch, cudaStream_t stream) {
+  using namespace scout;
+  if (positions == nullptr || !valid_rope(rope) || !valid_eps(eps)) return SCOUT_ERR_INVALID_ARG;
+  if (!supported_rope(rope) || !aligned16(norm) || (reinterpret_cast<uintptr_t>(positions) & 3u))
+    return SCOUT_ERR_UNSUPPORTED;
+  auto* const call = rope->layout == SCOUT_ROPE_HALF ? predict<SCOUT_ROPE_HALF> : predict<SCOUT_ROPE_INTERLEAVED>;
+  return call(X, W, Q, M, N, K, positions, rope, norm, eps, dev_status, launch, stream);
 }

@@ -71,22 +71,6 @@ __global__ void __launch_bounds__(256) recall_gather_kernel(const scout_recall_o
   }
 }
 
-// Device address of a host range [p, p + bytes) in pinned, mapped host memory, or nullptr.
-void* mapped_address(const void* p, size_t bytes) {
-  cudaPointerAttributes first, last;
-  const uint8_t* end = static_cast<const uint8_t*>(p) + bytes - 1;
-  if (cudaPointerGetAttributes(&first, p) != cudaSuccess || cudaPointerGetAttributes(&last, end) != cudaSuccess) {
-    cudaGetLastError();  // the lookup's error is this call's answer, not a sticky launch error
-    return nullptr;
-  }
-  if (first.type != cudaMemoryTypeHost || last.type != cudaMemoryTypeHost || first.devicePointer == nullptr ||
-      last.devicePointer == nullptr ||
-      static_cast<const uint8_t*>(last.devicePointer) - static_cast<const uint8_t*>(first.devicePointer) !=
-          static_cast<ptrdiff_t>(bytes - 1))
-    return nullptr;
-  return first.devicePointer;
-}
-
 int check_recall(int n_ops, const void* ops, const void* host_K, const void* host_V, const void* K_pool,
                  const void* V_pool, int64_t n_slots, int B, int Hkv, int D, int P, int nblk_cap,
                  const scout_launch* launch) {

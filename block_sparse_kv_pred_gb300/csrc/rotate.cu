@@ -1,0 +1,176 @@
+// scout_rotate and scout_append_rotated_kv: heads normalised and turned by their positions, and keys
+// on their way into a bf16 paged cache with their values.
+#include "rotate.cuh"
+
+namespace scout {
+namespace {
+
+constexpr int kRotThreads = 128;
+constexpr int kRotHeads = 2;  // heads of a lane in flight together
+
+struct HeadRows {  // heads of a token side by side, tokens ld elements apart
+  const __nv_bfloat16* src;
+  int64_t ld;
+  __nv_bfloat16* dst;
+  int64_t ld_dst;
+  const __nv_bfloat16* norm;
+  int heads;
+};
+
+struct RotArgs {
+  HeadRows q;             // rows to rows
+  HeadRows kv[2];         // K and V rows to the pools (dst), by slot_map; V is copied
+  const int64_t* slot_map;
+  int64_t pool_rows;
+  const int32_t* positions;
+  int n_tokens;
+  int per;                // heads of a warp
+  int parts_q, parts_kv;  // warps of a group of four tokens: of the queries, of K and of V each
+  Rope rope;
+  float eps;
+  int32_t* status;
+};
+
+// A warp takes four tokens and `per` of their heads of one kind.
+template <int LAYOUT>
+__global__ void __launch_bounds__(kRotThreads) rotate_kernel(const RotArgs a) {
+  const int lane = threadIdx.x & 31, sub = lane & 7;
+  const int parts = a.parts_q + 2 * a.parts_kv;
+  const int64_t w = (int64_t)blockIdx.x * (kRotThreads / 32) + (threadIdx.x >> 5);
+  const int64_t group = w / parts;
+  int part = (int)(w - group * parts);
+  const int64_t i = group * 4 + (lane >> 3);
+  if (group * 4 >= a.n_tokens) return;
+  const int pos = i < a.n_tokens ? a.positions[i] : -1;
+  const bool is_q = part < a.parts_q;
+  const bool is_v = part >= a.parts_q + a.parts_kv;
+  part -= is_q ? 0 : is_v ? a.parts_q + a.parts_kv : a.parts_q;
+  const HeadRows& r = is_q ? a.q : a.kv[is_v];
+  const int h0 = part * a.per, h1 = min(r.heads, h0 + a.per);
+  const int2 at = is_v ? make_int2(sub * 8, 64 + sub * 8) : lane_chunks<LAYOUT>(sub, a.rope.n);
+  const __nv_bfloat16* src = r.src + i * r.ld;
+  Turn t;
+  float wt[16];
+  const bool norm = r.norm != nullptr;
+  if (!is_v) {
+    t = lane_turn(a.rope, sub, (uint32_t)max(pos, 0));
+    if (norm)
+      unpack16(__ldg(reinterpret_cast<const uint4*>(r.norm + at.x)), __ldg(reinterpret_cast<const uint4*>(r.norm + at.y)),
+               wt);
+  }
+  for (int h = h0; h < h1; h += kRotHeads) {
+    uint4 x[kRotHeads], y[kRotHeads];
+    int64_t to[kRotHeads];
+#pragma unroll
+    for (int u = 0; u < kRotHeads; ++u) {
+      to[u] = -1;
+      if (pos < 0 || h + u >= h1) continue;
+      to[u] = is_q ? i * r.ld_dst + (h + u) * kD : a.slot_map[i * r.heads + h + u];
+      x[u] = ld_stream(src + (h + u) * kD + at.x);
+      y[u] = ld_stream(src + (h + u) * kD + at.y);
+    }
+#pragma unroll
+    for (int u = 0; u < kRotHeads; ++u) {
+      if (!is_q) {
+        if (to[u] >= a.pool_rows) {
+          if (sub == 0) report(a.status, SCOUT_DEV_BAD_INDEX);
+          to[u] = -1;
+        }
+        if (to[u] >= 0) to[u] *= kD;
+      }
+      if (!is_v) {
+        float v[16];
+        unpack16(x[u], y[u], v);
+        if (norm) norm_head(v, wt, a.eps);
+        turn_head<LAYOUT>(v, t, sub < a.rope.n);
+        pack16(v, x[u], y[u]);
+      }
+      if (to[u] < 0) continue;
+      *reinterpret_cast<uint4*>(r.dst + to[u] + at.x) = x[u];
+      *reinterpret_cast<uint4*>(r.dst + to[u] + at.y) = y[u];
+    }
+  }
+}
+
+int launch_rotate(RotArgs& a, int layout, cudaStream_t st) {
+  const int64_t groups = ((int64_t)a.n_tokens + 3) / 4;
+  a.per = 8;
+  a.parts_q = (a.q.heads + a.per - 1) / a.per;
+  a.parts_kv = (a.kv[0].heads + a.per - 1) / a.per;
+  const int64_t warps = groups * (a.parts_q + 2 * a.parts_kv);
+  const int64_t grid = (warps + kRotThreads / 32 - 1) / (kRotThreads / 32);
+  if (grid > 0x7fffffffLL) return SCOUT_ERR_UNSUPPORTED;
+  if (layout == SCOUT_ROPE_HALF)
+    rotate_kernel<SCOUT_ROPE_HALF><<<(unsigned)grid, kRotThreads, 0, st>>>(a);
+  else
+    rotate_kernel<SCOUT_ROPE_INTERLEAVED><<<(unsigned)grid, kRotThreads, 0, st>>>(a);
+  return launch_status();
+}
+
+}  // namespace
+
+int check_heads(const void* x, int64_t ld_x, const void* out, int64_t ld_out, int heads, int D, const scout_rope* rope,
+                const void* norm, float eps) {
+  if (x == nullptr || out == nullptr || heads <= 0 || !valid_rope(rope) || !valid_eps(eps) ||
+      ld_x < (int64_t)heads * D || ld_out < (int64_t)heads * D)
+    return SCOUT_ERR_INVALID_ARG;
+  if (D != kD || !supported_rope(rope) || ld_x % 8 != 0 || ld_out % 8 != 0 || !aligned16(x) || !aligned16(out) ||
+      !aligned16(norm))
+    return SCOUT_ERR_UNSUPPORTED;
+  return SCOUT_OK;
+}
+
+}  // namespace scout
+
+extern "C" int scout_rotate(const void* x, int64_t ld_x, void* out, int64_t ld_out, const int32_t* positions,
+                            int n_tokens, int heads, int D, const scout_rope* rope, const void* norm, float eps,
+                            cudaStream_t stream) {
+  using namespace scout;
+  if (positions == nullptr || n_tokens < 0) return SCOUT_ERR_INVALID_ARG;
+  const int rc = check_heads(x, ld_x, out, ld_out, heads, D, rope, norm, eps);
+  if (rc != SCOUT_OK) return rc;
+  if (reinterpret_cast<uintptr_t>(positions) & 3u) return SCOUT_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return SCOUT_OK;
+  RotArgs a = {};
+  a.q = HeadRows{static_cast<const __nv_bfloat16*>(x), ld_x, static_cast<__nv_bfloat16*>(out), ld_out,
+                 static_cast<const __nv_bfloat16*>(norm), heads};
+  a.positions = positions;
+  a.n_tokens = n_tokens;
+  a.rope = rope_of(rope);
+  a.eps = eps;
+  return launch_rotate(a, rope->layout, stream);
+}
+
+extern "C" int scout_append_rotated_kv(const void* K_new, int64_t ld_k, const void* V_new, int64_t ld_v,
+                                       const int32_t* positions, const scout_rope* rope, const void* k_norm, float eps,
+                                       const int64_t* slot_map, int n_tokens, int Hkv, int D, int P, void* K_pool,
+                                       void* V_pool, int64_t n_slots, const void* q, int64_t ld_q, int Hq,
+                                       const void* q_norm, void* q_out, int64_t ld_q_out, int32_t* dev_status,
+                                       cudaStream_t stream) {
+  using namespace scout;
+  if (V_new == nullptr || positions == nullptr || slot_map == nullptr || V_pool == nullptr) return SCOUT_ERR_INVALID_ARG;
+  if (n_tokens < 0 || Hkv <= 0 || Hq < 0 || n_slots <= 0 || ld_v < (int64_t)Hkv * D) return SCOUT_ERR_INVALID_ARG;
+  int rc = check_heads(K_new, ld_k, K_pool, ld_k, Hkv, D, rope, k_norm, eps);
+  if (rc == SCOUT_OK && Hq > 0) rc = check_heads(q, ld_q, q_out, ld_q_out, Hq, D, rope, q_norm, eps);
+  if (rc != SCOUT_OK) return rc;
+  if (!valid_P(P) || !aligned16(V_new) || !aligned16(V_pool) || ld_v % 8 != 0 ||
+      (reinterpret_cast<uintptr_t>(slot_map) & 7u) || (reinterpret_cast<uintptr_t>(positions) & 3u) ||
+      n_slots > 0x7fffffffLL)
+    return SCOUT_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return SCOUT_OK;
+  RotArgs a = {};
+  if (Hq > 0)
+    a.q = HeadRows{static_cast<const __nv_bfloat16*>(q), ld_q, static_cast<__nv_bfloat16*>(q_out), ld_q_out,
+                   static_cast<const __nv_bfloat16*>(q_norm), Hq};
+  a.kv[0] = HeadRows{static_cast<const __nv_bfloat16*>(K_new), ld_k, static_cast<__nv_bfloat16*>(K_pool), 0,
+                     static_cast<const __nv_bfloat16*>(k_norm), Hkv};
+  a.kv[1] = HeadRows{static_cast<const __nv_bfloat16*>(V_new), ld_v, static_cast<__nv_bfloat16*>(V_pool), 0, nullptr, Hkv};
+  a.slot_map = slot_map;
+  a.pool_rows = n_slots * P;
+  a.positions = positions;
+  a.n_tokens = n_tokens;
+  a.rope = rope_of(rope);
+  a.eps = eps;
+  a.status = dev_status;
+  return launch_rotate(a, rope->layout, stream);
+}

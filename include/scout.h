@@ -12,8 +12,8 @@
  *   a rejected call launches nothing.  A launch failure reported by the CUDA
  *   runtime returns SCOUT_ERR_CUDA.
  * - The host-side entry points (scout_plan_recall, scout_plan_recall_pages,
- *   scout_recall_intervals, scout_cpu_attend(_scalar), scout_cpu_pool_*,
- *   scout_cpu_attend_async) are the exception: host pointers only, no GPU
+ *   scout_recall_intervals, scout_rope_turns, scout_cpu_attend(_scalar),
+ *   scout_cpu_pool_*, scout_cpu_attend_async) are the exception: host pointers only, no GPU
  *   involved, synchronous except scout_cpu_attend_async.  scout_cpu_attend runs on
  *   worker threads it starts and joins within the call; the pool calls run on the
  *   caller's pool.
@@ -381,6 +381,119 @@ int scout_append_kv(const void* K_new, int64_t ld_k, const void* V_new, int64_t 
                     int32_t* dev_status, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ *
+ * Residual stream and norms around a layer's blocks.
+ * The input X of the query prediction (ScoutAttention (arXiv HTML), section 3.3) is the
+ * normalised residual stream; predicting one layer ahead, the same stream is normalised with
+ * two layers' weights, so both come from one pass.
+ *
+ *   p  = Y, or norm(Y) * w_post + b_post where w_post is given
+ *   H' = H + alpha * gate * p
+ *   X  = norm(H') * w + b,   X_ahead = norm(H') * w_ahead + b_ahead
+ * norm(v) = v * (mean v^2 + eps)^(-1/2) (SCOUT_NORM_RMS), or (v - mean v) * (mean (v - mean v)^2 + eps)^(-1/2)
+ * (SCOUT_NORM_LAYER), over a row.  In fp32; X and X_ahead come from the H' that is not yet rounded.
+ *
+ * Y        bf16 [M] rows of N, ld_y elements apart; NULL: H' = H (gate, w_post and H_out then have to be NULL)
+ * H, H_out bf16 (h_type SCOUT_BF16) or fp32 (SCOUT_FP32), rows ld_h and ld_h_out elements apart; H_out may be H, with the same
+ *          stride
+ * gate     bf16 rows ld_gate elements apart, 0 for one row that serves all, or NULL: 1
+ * w, w_ahead, w_post, b, b_ahead, b_post bf16 [N]; the biases may be NULL (and are with RMS)
+ * X        bf16 [M][N], as scout_predict_q reads it; X_ahead the same, with w_ahead, or both NULL
+ * X may be Y where ld_y is N (a row is read before it is written); no other overlap.
+ * Requires N % 8 == 0, N <= 32768, ld >= N, ld % 8 == 0, eps >= 0 and finite, alpha finite and 16-byte aligned tensors.
+ * ------------------------------------------------------------------------ */
+typedef enum scout_norm_kind { SCOUT_NORM_RMS = 0, SCOUT_NORM_LAYER = 1 } scout_norm_kind;
+typedef enum scout_float { SCOUT_BF16 = 0, SCOUT_FP32 = 1 } scout_float;
+int scout_add_norm(int kind, const void* Y, int64_t ld_y, const void* w_post, const void* b_post, const void* gate,
+                   int64_t ld_gate, float alpha, int h_type, const void* H, int64_t ld_h, void* H_out, int64_t ld_h_out,
+                   const void* w, const void* b, void* X, const void* w_ahead, const void* b_ahead, void* X_ahead, int M,
+                   int N, float eps, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * Rotary positions.
+ * The pages take the queries and keys of a layer as given and write Q_pred as a bare
+ * product (ScoutAttention (arXiv HTML), section 3.3); models whose attention turns its
+ * heads by their tokens' positions hold turned keys in the cache, so the digests select
+ * by turned queries.  The entry points below make both.
+ *
+ * A head's first rot_dim channels are pairs, pair i of the channels (i, i + rot_dim / 2)
+ * (SCOUT_ROPE_HALF) or (2i, 2i + 1) (SCOUT_ROPE_INTERLEAVED).  At position p it becomes
+ *   (a, b) -> amplitude * (a cos(p f_i) - b sin(p f_i), b cos(p f_i) + a sin(p f_i));
+ * the other channels stay as they are.  turns[i] is f_i in turns, f_i / (2 pi) modulo 1, as
+ * a fraction of 2^64: p * turns[i] modulo 2^64 is the pair's angle to 2^-33 of a turn at any
+ * position, in integers.
+ *
+ * turns      uint64 [rot_dim / 2], DEVICE memory, 16-byte aligned
+ * rot_dim    a multiple of 16, at most D
+ * amplitude  finite; usually 1
+ * ------------------------------------------------------------------------ */
+typedef enum scout_rope_layout { SCOUT_ROPE_HALF = 0, SCOUT_ROPE_INTERLEAVED = 1 } scout_rope_layout;
+typedef struct scout_rope {
+  const uint64_t* turns;
+  int rot_dim;
+  int layout;
+  float amplitude;
+} scout_rope;
+
+/* The turns of a geometric set of frequencies (host code, HOST memory out): f_i = base^(-2i / rot_dim),
+ * changed for contexts longer than those a model was trained on as scaling (NULL: not at all) says.
+ *   LINEAR     f / factor
+ *   NTK        base * factor^(rot_dim / (rot_dim - 2)) for base
+ *   ROTATIONS  keep * f + (1 - keep) * f / factor, keep = (original f / (2 pi) - low) / (high - low)
+ *              cut to [0, 1]: by the turns a pair makes over the original length
+ *   INDEX      (1 - slow) * f + slow * f / factor, slow = (i - a) / (b - a) cut to [0, 1], with
+ *              a = max(floor(x(high)), 0), b = min(ceil(x(low)), rot_dim - 1) (b - a at least 0.001) and
+ *              x(n) = rot_dim ln(original / (2 pi n)) / (2 ln base), the pair that makes n turns
+ *   DIVISORS   f_i / divisors[i] (host double [rot_dim / 2])
+ * *amplitude: scaling's, or where that is 0 the kind's own: 0.1 ln(factor) + 1 for INDEX with a factor above 1,
+ * otherwise 1.
+ * SCOUT_ERR_INVALID_ARG (nothing written): a NULL pointer, base not finite or not above 1, an unknown kind, a factor,
+ * original, low, divisor that is not finite or not positive where the kind uses it, high not above low, a
+ * negative or not finite amplitude.  SCOUT_ERR_UNSUPPORTED: rot_dim not a multiple of 16 in [16, 128]. */
+typedef enum scout_rope_kind {
+  SCOUT_ROPE_LINEAR = 1,
+  SCOUT_ROPE_NTK = 2,
+  SCOUT_ROPE_ROTATIONS = 3,
+  SCOUT_ROPE_INDEX = 4,
+  SCOUT_ROPE_DIVISORS = 5
+} scout_rope_kind;
+typedef struct scout_rope_scaling {
+  int kind;
+  double factor, original, low, high, amplitude;
+  const double* divisors;
+} scout_rope_scaling;
+int scout_rope_turns(double base, int rot_dim, const scout_rope_scaling* scaling, uint64_t* turns, float* amplitude);
+
+/* Heads normalised and turned.
+ * x, out     bf16: head (i, h) of D values at i * ld_x (ld_out) + h * D elements; out may be x itself, with the
+ *            same stride (no other overlap)
+ * positions  int32 [n_tokens]; a negative one marks a padding row, which is neither read nor written
+ * norm       bf16 [D], or NULL for no norm: the head is first divided by its root mean square,
+ *            x * (sum x^2 / D + eps)^(-1/2) * norm
+ * In fp32, rounded to bf16 once.  Requires ld >= heads * D, ld % 8 == 0, eps >= 0 and finite, and 16-byte aligned
+ * tensors (positions 4-byte). */
+int scout_rotate(const void* x, int64_t ld_x, void* out, int64_t ld_out, const int32_t* positions, int n_tokens,
+                 int heads, int D, const scout_rope* rope, const void* norm, float eps, cudaStream_t stream);
+
+/* scout_append_kv with the keys normalised and turned on their way into the cache, and the same tokens' queries
+ * beside them (scout_rotate from q to q_out), in one launch.
+ * K_new, V_new, slot_map, K_pool, V_pool, dev_status: as scout_append_kv.  positions int32 [n_tokens]: a
+ * negative one marks a padding row (nothing of it is read or written, whatever its slots).
+ * k_norm, q_norm bf16 [D] or NULL; Hq 0 (q and q_out then unused) or the query heads.  q_out may be q. */
+int scout_append_rotated_kv(const void* K_new, int64_t ld_k, const void* V_new, int64_t ld_v,
+                            const int32_t* positions, const scout_rope* rope, const void* k_norm, float eps,
+                            const int64_t* slot_map, int n_tokens, int Hkv, int D, int P, void* K_pool, void* V_pool,
+                            int64_t n_slots, const void* q, int64_t ld_q, int Hq, const void* q_norm, void* q_out,
+                            int64_t ld_q_out, int32_t* dev_status, cudaStream_t stream);
+
+/* scout_predict_q with the heads of its product normalised and turned before they are rounded: row m of X W^T, N / D
+ * heads of D = 128, each normalised by norm (bf16 [D], or NULL) and turned by positions[m] as scout_rotate does.  A row
+ * whose position is negative (padding) is computed but not written.  Arguments, limits, launch options and early
+ * starts as scout_predict_q, which waits before it reads X; this waits before it reads X and positions. */
+int scout_predict_q_rotated(const void* X, const void* W, void* Q, int M, int N, int K, const int32_t* positions,
+                            const scout_rope* rope, const void* norm, float eps, int32_t* dev_status,
+                            const scout_launch* launch, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ *
  * 8-bit paged caches.
  *
  * A pool holds one byte per value, [n_slots][P][D], with one fp32 scale per slot (a block of
@@ -419,6 +532,20 @@ int scout_append_kv8(int fmt, const void* K_new, int64_t ld_k, const void* V_new
                      const int32_t* prev_len, const int32_t* seq_len, const int32_t* page_table, int B, int Hkv,
                      int D, int P, int nblk_cap, void* K_pool, void* V_pool, float* K_scale, float* V_scale,
                      int64_t n_slots, int32_t* dev_status, cudaStream_t stream);
+
+/* scout_append_kv8 with the keys normalised and turned first, and the same tokens' queries beside them, in one
+ * launch.  The turned keys are rounded to bf16 before they are quantised, so that a key's code is the one that
+ * scout_rotate and scout_append_kv8 give it: a block that is written again from bf16 rows (a
+ * recalled one) comes out the same.
+ * positions  int32 [n_tokens], or NULL: each token's index in its sequence.  A negative one counts as 0
+ *            and sets SCOUT_DEV_BAD_INDEX.  Rows past the last new token (a padded batch's) are left alone, q_out's too.
+ * Everything else as scout_append_kv8 and scout_append_rotated_kv. */
+int scout_append_rotated_kv8(int fmt, const void* K_new, int64_t ld_k, const void* V_new, int64_t ld_v, int n_tokens,
+                             const int32_t* positions, const scout_rope* rope, const void* k_norm, float eps,
+                             const int32_t* prev_len, const int32_t* seq_len, const int32_t* page_table, int B,
+                             int Hkv, int D, int P, int nblk_cap, void* K_pool, void* V_pool, float* K_scale,
+                             float* V_scale, int64_t n_slots, const void* q, int64_t ld_q, int Hq, const void* q_norm,
+                             void* q_out, int64_t ld_q_out, int32_t* dev_status, cudaStream_t stream);
 
 /* Block digests of an 8-bit cache: scout_build_digest over the values code * scale, with the
  * same outputs, so that scout_score_topk selects from either cache.  The minima are rounded
@@ -459,6 +586,33 @@ int scout_sparse_attn8_merge(int fmt, const void* q, const void* K_pool, const v
                              int nblk_cap, int k, float scale, const float* O_cpu, const float* lse_cpu, void* O_out,
                              float* lse_out, void* workspace, size_t workspace_bytes, int32_t* dev_status,
                              const scout_launch* launch, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * Blocks of a paged cache back as bf16 rows in token order: the host copy that
+ * scout_cpu_attend and the recalls read (ScoutAttention (arXiv HTML), sections 3.2 and 3.4),
+ * after a prompt or block by block as a sequence grows, or contiguous K/V for another kernel.
+ *
+ * K_out, V_out bf16: token t of unit (b, kvh) at b * stride_b + kvh * stride_h + t * stride_t elements, T tokens a
+ *              unit: [B][Hkv][T][D] in any order of its axes but the last.  host_out 0: device memory; 1: pinned host
+ *              memory mapped into the device's address space (as for scout_recall_gather_async).
+ * block_list   int32 [n_list][2] of (u, j), or NULL for every valid block.  A (-1, -1) entry is padding; any other entry
+ *              outside the tables, or without a slot of the pool, is skipped and sets SCOUT_DEV_BAD_INDEX.  With NULL, blocks
+ *              whose page-table entry is -1 (those not on the GPU) are skipped without a report.
+ * Of a block, the rows t < seq_len[b] are written; everything else in K_out and V_out is left as it was.  Rows with
+ * t >= T are left out and set SCOUT_DEV_OVERFLOW.
+ * scout_read_kv copies; scout_read_kv8 writes code * scale, rounded to bf16 (exact where the scale is a power of two).
+ * No workspace.  Requires P in {16, 32, 64}, D = 128, T >= 1, strides >= 0 and multiples of 8, block_list 8-byte, the
+ * other tensors 16-byte aligned, nblk_cap <= 8192, n_slots, B * Hkv * nblk_cap < 2^31; with host_out K_out and V_out must be mapped from
+ * their first byte to their last (else SCOUT_ERR_UNSUPPORTED). */
+int scout_read_kv(const void* K_pool, const void* V_pool, int64_t n_slots, const int32_t* page_table,
+                  const int32_t* seq_len, int B, int Hkv, int D, int P, int nblk_cap, const int32_t* block_list,
+                  int n_list, void* K_out, void* V_out, int64_t stride_b, int64_t stride_h, int64_t stride_t, int64_t T,
+                  int host_out, int32_t* dev_status, cudaStream_t stream);
+int scout_read_kv8(int fmt, const void* K_pool, const void* V_pool, const float* K_scale, const float* V_scale,
+                   int64_t n_slots, const int32_t* page_table, const int32_t* seq_len, int B, int Hkv, int D, int P,
+                   int nblk_cap, const int32_t* block_list, int n_list, void* K_out, void* V_out, int64_t stride_b,
+                   int64_t stride_h, int64_t stride_t, int64_t T, int host_out, int32_t* dev_status,
+                   cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ *
  * Asynchronous periodic recall (host side).
