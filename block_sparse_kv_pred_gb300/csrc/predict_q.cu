@@ -232,10 +232,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1) predict_q_kernel(const __grid_co
   if constexpr (LAYOUT != kPlain) {
     __syncthreads();
     const int2 at = lane_chunks<LAYOUT>(sub, a.rope.n);
-    float w[16];
-    if (a.norm != nullptr)
-      unpack16(__ldg(reinterpret_cast<const uint4*>(a.norm + at.x)), __ldg(reinterpret_cast<const uint4*>(a.norm + at.y)),
-               w);
+    Weights w;
+    if (a.norm != nullptr) w = lane_weights(a.norm, at);
     const int columns = (ngroups - (int)rank + (int)S - 1) / (int)S * 8;  // of this CTA
     for (int k0 = 0; k0 < columns; k0 += 16) {
       const int k = k0 + warp * 4 + (lane >> 3);

@@ -6,7 +6,6 @@ namespace scout {
 namespace {
 
 constexpr int kRotThreads = 128;
-constexpr int kRotHeads = 2;  // heads of a lane in flight together
 
 struct HeadRows {  // heads of a token side by side, tokens ld elements apart
   const __nv_bfloat16* src;
@@ -31,16 +30,15 @@ struct RotArgs {
   int32_t* status;
 };
 
-// A warp takes four tokens and `per` of their heads of one kind.
-template <int LAYOUT>
-__global__ void __launch_bounds__(kRotThreads) rotate_kernel(const RotArgs a) {
+// A warp takes four tokens and `per` of their heads of one kind, the warps of a CTA consecutive tokens.
+// U heads are in flight together.
+template <int LAYOUT, int U>
+__global__ void __launch_bounds__(kRotThreads, 5) rotate_kernel(const RotArgs a) {
   const int lane = threadIdx.x & 31, sub = lane & 7;
-  const int parts = a.parts_q + 2 * a.parts_kv;
-  const int64_t w = (int64_t)blockIdx.x * (kRotThreads / 32) + (threadIdx.x >> 5);
-  const int64_t group = w / parts;
-  int part = (int)(w - group * parts);
-  const int64_t i = group * 4 + (lane >> 3);
-  if (group * 4 >= a.n_tokens) return;
+  const unsigned parts = (unsigned)a.parts_q + 2 * (unsigned)a.parts_kv;
+  const unsigned block = blockIdx.x / parts;
+  int part = (int)(blockIdx.x - block * parts);
+  const int64_t i = ((int64_t)block * (kRotThreads / 32) + (threadIdx.x >> 5)) * 4 + (lane >> 3);
   const int pos = i < a.n_tokens ? a.positions[i] : -1;
   const bool is_q = part < a.parts_q;
   const bool is_v = part >= a.parts_q + a.parts_kv;
@@ -50,19 +48,17 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const RotArgs a) {
   const int2 at = is_v ? make_int2(sub * 8, 64 + sub * 8) : lane_chunks<LAYOUT>(sub, a.rope.n);
   const __nv_bfloat16* src = r.src + i * r.ld;
   Turn t;
-  float wt[16];
+  Weights w;
   const bool norm = r.norm != nullptr;
   if (!is_v) {
     t = lane_turn(a.rope, sub, (uint32_t)max(pos, 0));
-    if (norm)
-      unpack16(__ldg(reinterpret_cast<const uint4*>(r.norm + at.x)), __ldg(reinterpret_cast<const uint4*>(r.norm + at.y)),
-               wt);
+    if (norm) w = lane_weights(r.norm, at);
   }
-  for (int h = h0; h < h1; h += kRotHeads) {
-    uint4 x[kRotHeads], y[kRotHeads];
-    int64_t to[kRotHeads];
+  for (int h = h0; h < h1; h += U) {
+    uint4 x[U], y[U];
+    int64_t to[U];
 #pragma unroll
-    for (int u = 0; u < kRotHeads; ++u) {
+    for (int u = 0; u < U; ++u) {
       to[u] = -1;
       if (pos < 0 || h + u >= h1) continue;
       to[u] = is_q ? i * r.ld_dst + (h + u) * kD : a.slot_map[i * r.heads + h + u];
@@ -70,7 +66,7 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const RotArgs a) {
       y[u] = ld_stream(src + (h + u) * kD + at.y);
     }
 #pragma unroll
-    for (int u = 0; u < kRotHeads; ++u) {
+    for (int u = 0; u < U; ++u) {
       if (!is_q) {
         if (to[u] >= a.pool_rows) {
           if (sub == 0) report(a.status, SCOUT_DEV_BAD_INDEX);
@@ -81,7 +77,7 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const RotArgs a) {
       if (!is_v) {
         float v[16];
         unpack16(x[u], y[u], v);
-        if (norm) norm_head(v, wt, a.eps);
+        if (norm) norm_head(v, w, a.eps);
         turn_head<LAYOUT>(v, t, sub < a.rope.n);
         pack16(v, x[u], y[u]);
       }
@@ -92,19 +88,35 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const RotArgs a) {
   }
 }
 
-int launch_rotate(RotArgs& a, int layout, cudaStream_t st) {
+// Heads of a warp.  The fewer, the shorter a call of few rows (a warp's heads follow one another, four at a time) and
+// the more often a token's cosines are made.  GB300, 40 (8) heads, us, with 1 / 4 / 8 / 16 a warp:
+//   200 tokens 3.2 / 3.7 / 5.0 / 8.0 (2.5 / 3.5 / 4.9), 800: 6.5 / 5.0 / 5.8 / 8.1, 3,200 (8 heads): 5.5 / 4.3 / 5.7,
+//   6,400: 40.7 / 25.1 / 23.9 / 25.5, 20,000: 132 / 79.8 / 71.0 / 70.6
+// One where its warps are one wave (20 of them an SM at its registers), four likewise, then eight, and sixteen where
+// there are many or where that is all the heads (9,001 tokens of 12 heads: 14.2 us with eight, 12.9 with all).
+inline int heads_of_warp(int64_t steps, int heads) {
+  const int64_t wave = 20 * (int64_t)sm_count();
+  return steps <= wave ? 1 : steps <= 4 * wave ? 4 : steps <= 32 * wave && heads > 16 ? 8 : 16;
+}
+
+template <int LAYOUT>
+int launch_rotate(RotArgs& a, cudaStream_t st) {
   const int64_t groups = ((int64_t)a.n_tokens + 3) / 4;
-  a.per = 8;
+  const int most = max(a.q.heads, a.kv[0].heads);
+  a.per = heads_of_warp(groups * ((int64_t)a.q.heads + 2 * (int64_t)a.kv[0].heads), most);
   a.parts_q = (a.q.heads + a.per - 1) / a.per;
   a.parts_kv = (a.kv[0].heads + a.per - 1) / a.per;
-  const int64_t warps = groups * (a.parts_q + 2 * a.parts_kv);
-  const int64_t grid = (warps + kRotThreads / 32 - 1) / (kRotThreads / 32);
+  const int64_t grid = (groups + kRotThreads / 32 - 1) / (kRotThreads / 32) * ((int64_t)a.parts_q + 2 * (int64_t)a.parts_kv);
   if (grid > 0x7fffffffLL) return SCOUT_ERR_UNSUPPORTED;
-  if (layout == SCOUT_ROPE_HALF)
-    rotate_kernel<SCOUT_ROPE_HALF><<<(unsigned)grid, kRotThreads, 0, st>>>(a);
+  if (a.per == 1)
+    rotate_kernel<LAYOUT, 1><<<(unsigned)grid, kRotThreads, 0, st>>>(a);
   else
-    rotate_kernel<SCOUT_ROPE_INTERLEAVED><<<(unsigned)grid, kRotThreads, 0, st>>>(a);
+    rotate_kernel<LAYOUT, 4><<<(unsigned)grid, kRotThreads, 0, st>>>(a);
   return launch_status();
+}
+
+int launch_rotate(RotArgs& a, int layout, cudaStream_t st) {
+  return layout == SCOUT_ROPE_HALF ? launch_rotate<SCOUT_ROPE_HALF>(a, st) : launch_rotate<SCOUT_ROPE_INTERLEAVED>(a, st);
 }
 
 }  // namespace

@@ -7,7 +7,7 @@
 // every head of the token.
 //
 // The angle is an integer product modulo 2^64 (turns as fractions of 2^64), so a far position costs no
-// precision; its upper 32 bits go to sincospi, which needs no reduction of its argument.  Every rounding is
+// precision and no reduction.  Every rounding is
 // written out (no contraction is left to the compiler), so that each kernel that turns a head gets the same bits.
 #pragma once
 
@@ -39,6 +39,25 @@ __device__ __forceinline__ int2 lane_chunks(int sub, int n) {
   return make_int2(sub * 16, sub * 16 + 8);
 }
 
+// sin and cos of a turn given as a fraction of 2^32: the nearest quarter turn by integers, and polynomials
+// in the square of the rest, |rest| <= 1/8 turn (minimax, fitted by exchange: the sine's quotient by the rest to
+// 2^-28, the cosine to 2^-34).  Off by at most 1.7 and 1.2 roundings of fp32 over 2 million angles, with a
+// third of the instructions of sincospi, whose code a short launch has to fetch.
+__device__ __forceinline__ void sincos_turn(uint32_t turn, float& s, float& c) {
+  const uint32_t quarter = (turn + 0x20000000u) & 0xc0000000u;
+  const float x = __fmul_rn((float)(int32_t)(turn - quarter), 0x1p-32f), z = __fmul_rn(x, x);
+  float p = __fmaf_rn(-75.40206909179688f, z, 81.5925521850586f);
+  p = __fmaf_rn(p, z, -41.3416633605957f);
+  p = __fmul_rn(__fmaf_rn(p, z, 6.2831854820251465f), x);
+  float q = __fmaf_rn(59.22040557861328f, z, -85.44285583496094f);
+  q = __fmaf_rn(q, z, 64.93931579589844f);
+  q = __fmaf_rn(q, z, -19.739208221435547f);
+  q = __fmaf_rn(q, z, 1.f);
+  const bool odd = quarter & 0x40000000u;  // a quarter turn further: (s, c) -> (c, -s)
+  s = __uint_as_float(__float_as_uint(odd ? q : p) ^ (quarter & 0x80000000u));
+  c = __uint_as_float(__float_as_uint(odd ? p : q) ^ ((quarter + 0x40000000u) & 0x80000000u));
+}
+
 // cos and sin (times the amplitude) of a lane's eight pairs at a position; lanes past n get none.
 struct Turn {
   float c[8], s[8];
@@ -53,11 +72,10 @@ __device__ __forceinline__ Turn lane_turn(const Rope& r, int sub, uint32_t pos) 
       const uint64_t w[2] = {v.x, v.y};
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint64_t a = (uint64_t)pos * w[j] + 0x80000000ull;
-        // half turns in [-1, 1): exact up to the conversion of 32 bits to 24
-        sincospif((float)(int32_t)(a >> 32) * 4.656612873077393e-10f, &t.s[2 * i + j], &t.c[2 * i + j]);
-        t.s[2 * i + j] = __fmul_rn(t.s[2 * i + j], r.amplitude);
-        t.c[2 * i + j] = __fmul_rn(t.c[2 * i + j], r.amplitude);
+        float s, c;
+        sincos_turn((uint32_t)(((uint64_t)pos * w[j] + 0x80000000ull) >> 32), s, c);
+        t.s[2 * i + j] = __fmul_rn(s, r.amplitude);
+        t.c[2 * i + j] = __fmul_rn(c, r.amplitude);
       }
     }
   }
@@ -78,14 +96,24 @@ __device__ __forceinline__ void pack16(const float (&x)[16], uint4& a, uint4& b)
   b = make_uint4(pack_bf16(x[8], x[9]), pack_bf16(x[10], x[11]), pack_bf16(x[12], x[13]), pack_bf16(x[14], x[15]));
 }
 
-// The head's norm: by the eight lanes that hold it, all of them.  w: the lane's weights.
-__device__ __forceinline__ void norm_head(float (&x)[16], const float (&w)[16], float eps) {
+// A lane's 16 weights of a norm, packed.
+struct Weights {
+  uint4 a, b;
+};
+__device__ __forceinline__ Weights lane_weights(const __nv_bfloat16* norm, const int2& at) {
+  return Weights{__ldg(reinterpret_cast<const uint4*>(norm + at.x)), __ldg(reinterpret_cast<const uint4*>(norm + at.y))};
+}
+
+// The head's norm: by the eight lanes that hold it, all of them.
+__device__ __forceinline__ void norm_head(float (&x)[16], const Weights& weights, float eps) {
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) ss = __fmaf_rn(x[i], x[i], ss);
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   const float r = rsqrtf(__fmaf_rn(ss, 1.f / kD, eps));
+  float w[16];
+  unpack16(weights.a, weights.b, w);
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), w[i]);
 }

@@ -1,11 +1,21 @@
 // scout_append_rotated_kv8: new keys normalised, turned and quantised on their way into 8-bit pools with
 // their values, and the same tokens' queries normalised and turned beside them.
 //
-// A CTA takes a touched block and a part of its heads: kHeads KV heads, K and V, or up to kQHeads query heads.
-// Eight lanes hold a token's row (rotate.cuh), so its P / 4 warps hold a whole block of each of those
-// heads in registers: read once, turned, rounded to bf16, the block's maximum joined through shared
-// memory, and the codes made from the registers.  A lane's token is the same for every head, so its cosines and sines
-// are made once a block.  A range of consecutive (block, part) items goes to each CTA.
+// Eight lanes hold a token's row (rotate.cuh).  A warp takes the K or the V of a touched block of one KV head: its new rows
+// sit in registers, four a step, are read once, turned, rounded to bf16, their maximum is taken, and the codes are made
+// from the registers.  Two kernels, by how many new tokens a sequence has:
+//
+// Many: a CTA takes a block and some or all of its KV heads.  Its cosines and sines, which all heads share, are made
+// once, into shared memory, while the first heads' rows are on their way.  Other CTAs take the queries, a warp four
+// tokens and up to 16 heads, their cosines in registers.
+//
+// Few (a decode step): a warp takes one head of a block, or one query head of four tokens, with no barrier and little code.
+//
+// GB300, 8 prompts of up to 16K tokens, 8 KV and 32 query heads: 265 us for 1.57 GB (5.9 TB/s, 0.88 of the measured
+// copy bandwidth; blocks of 16 tokens 260, of 64 270), bound by how well 16 warps an SM overlap arithmetic and
+// loads (the keys and values alone: 95 us, against 70 of scout_append_kv8 without turns).  A warp that made its own rows'
+// cosines for each head: 351 us; a CTA's warps holding four rows each of all heads, joined by its barrier: 302.  A decode
+// step of 40 sequences: 3.8 us, a chain of dependent reads (lengths, slot and rows, scale).
 #include "fp8.cuh"
 #include "rotate.cuh"
 
@@ -16,8 +26,16 @@ int check_heads(const void* x, int64_t ld_x, const void* out, int64_t ld_out, in
 
 namespace {
 
-constexpr int kHeads = 2;   // KV heads of an item
-constexpr int kQHeads = 8;  // query heads of an item
+constexpr int kR8Warps = 4;
+constexpr int kR8PerSm = 4;  // CTAs of the first kernel an SM (128 registers)
+// GB300, 8 prompts of up to 16K tokens (8 KV, 32 query heads): 265 us with four times as many CTAs as run at a time, for the
+// hardware to deal out; 294 with once, 267 with sixteen times.
+constexpr int kR8Waves = 4;
+constexpr int kR8Heads = 16;  // query heads of a warp, one turn made for them
+// New tokens a sequence up to which a call is the second kernel's.  40 sequences (8 KV, 40 query heads), us, first / second
+// kernel: 8 tokens 13.1 / 7.5, 16: 14.7 / 12.5, 32: 18.1 / 23.3; one token 9.6 / 4.0.
+constexpr int kFewTokens = 16;
+constexpr int kHold = 8;  // row steps that a warp holds: a larger block is a pair of warps'
 
 struct Rot8Args {
   const __nv_bfloat16 *kv[2], *q;  // new rows
@@ -28,229 +46,382 @@ struct Rot8Args {
   float* scale[2];
   const int32_t *positions, *prev_len, *seq_len, *page_table;
   int n_tokens, B, Hkv, Hq, nblk_cap;
-  int kv_parts, q_parts;
+  int kv_heads, kv_ctas;  // KV heads of a CTA's item, CTAs that take them
+  int q_per, q_parts;     // query heads of a warp, warps of four tokens
   int64_t n_slots;
   Rope rope;
   float eps;
   int32_t* status;
 };
 
-template <int P, int F, int LAYOUT>
-__global__ void __launch_bounds__(P * 8) rotate8_kernel(const Rot8Args a) {
-  constexpr int kWarps = P / 4, kSets = 2 * kHeads;
-  extern __shared__ int sm[];
-  __shared__ int partial[2 * 32];
-  __shared__ uint32_t top[2][kSets][kWarps];  // largest magnitudes, a buffer for every other item
-  const int B = a.B;
-  int* tok = sm;            // [B + 1] new tokens before sequence b
-  int* tou = sm + (B + 1);  // [B + 1] touched blocks (of one KV head) before it
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane & 7;
+// The lane's position of token row i (its index in the sequence where none are given).
+__device__ __forceinline__ uint32_t position_of(const Rot8Args& a, int64_t i, int index, bool live, int sub) {
+  if (a.positions == nullptr || !live) return (uint32_t)max(index, 0);
+  const int pos = a.positions[i];
+  if (pos < 0 && sub == 0) report(a.status, SCOUT_DEV_BAD_INDEX);
+  return (uint32_t)max(pos, 0);
+}
+
+__device__ __forceinline__ uint32_t max_finite(uint32_t m, const uint4& x) {
+  return max_abs2(max_abs2(max_abs2(max_abs2(m, finite2(x.x)), finite2(x.y)), finite2(x.z)), finite2(x.w));
+}
+__device__ __forceinline__ uint32_t max_all(uint32_t m, const uint4& x) {
+  return max_abs2(max_abs2(max_abs2(max_abs2(m, x.x), x.y), x.z), x.w);
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t m) {
+  return __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+}
+
+// A touched block: its sequence's part, the same for all its heads.
+struct Block {
+  int b, j, r0, r1;  // new rows [r0, r1)
+  int64_t i0;        // token row of its row 0
+};
+template <int P>
+__device__ __forceinline__ Block block_of(const Rot8Args& a, const int* tok, const int* tou, int blk) {
+  Block k;
+  k.b = owner_of(tou, a.B, blk);
+  const SeqSpan s = seq_span(a.prev_len, a.seq_len, k.b, a.nblk_cap * P);
+  k.j = s.prev / P + blk - tou[k.b];
+  k.r0 = max(s.prev - k.j * P, 0);
+  k.r1 = min(s.seq - k.j * P, P);
+  k.i0 = (int64_t)tok[k.b] + (k.j * P - s.prev);
+  return k;
+}
+
+// The two warps of a pair meet (their own barrier: pairs do not wait for one another).
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + (int)(threadIdx.x >> 6)) : "memory");
+}
+
+// The K or V of one head of a block, by a warp, or by a pair (`top`: its warps' maxima, two sets of them) that holds a half of
+// it each.  H: steps held (of four rows each, from row `first`); with MORE the others, up to `steps`, are read again.
+// load(g, x, y) reads the rows of a step (zeros for rows that are not new), turn(g, x, y) turns them.
+template <int P, int F, int H, bool MORE, bool PAIR, class Load, class Turner>
+__device__ __forceinline__ void quantise(const Rot8Args& a, const Block& k, bool is_v, int slot, const int2& at, int first,
+                                         int steps, uint4 (&x)[H], uint4 (&y)[H], uint32_t* top, Load load, Turner turn) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 7;
+  const bool in_pool = slot >= 0 && slot < a.n_slots;
+  float* scale_at = a.scale[is_v] + (in_pool ? slot : 0);
+  const float old = in_pool && k.r0 > 0 ? *scale_at : 0.f;
+  if (!is_v) {
+#pragma unroll
+    for (int g = 0; g < H; ++g) turn(g, x[g], y[g]);
+  }
+  // rows that are not new hold zeros, or what a norm without eps makes of them (NaN, which the maxima pass over)
+  uint32_t m = 0u, fin = 0u;
+#pragma unroll
+  for (int g = 0; g < H; ++g) m = max_all(max_all(m, x[g]), y[g]);
+  for (int g = H; MORE && g < steps; ++g) {
+    uint4 lo, hi;
+    load(g, lo, hi);
+    if (!is_v) turn(g, lo, hi);
+    m = max_all(max_all(m, lo), hi);
+    fin = max_finite(max_finite(fin, lo), hi);
+  }
+  auto join = [&](uint32_t v, int set) {
+    v = warp_max(v);
+    if (PAIR) {
+      if (lane == 0) top[set * kR8Warps + warp] = v;
+      pair_sync();
+      v = max(v, top[set * kR8Warps + (warp ^ 1)]);
+    }
+    return v;
+  };
+  uint32_t big = join(m, 0);
+  if (big == 0x7f80u) {  // an infinity among them: the largest of the others (rare)
+#pragma unroll
+    for (int g = 0; g < H; ++g) fin = max_finite(max_finite(fin, x[g]), y[g]);
+    big = join(fin, 1);
+  }
+  if (!in_pool) {
+    if (lane == 0) report(a.status, SCOUT_DEV_BAD_INDEX);
+  } else {
+    uint8_t* page = a.pool[is_v] + (int64_t)slot * (P * kD);
+    const float need = pow2_biased(scale_exponent<F>(__uint_as_float(big << 16)));
+    const bool grows = k.r0 > 0 && need > old;  // the scale of a block with cached tokens never shrinks
+    const float scale = k.r0 > 0 && !grows ? old : need;
+    const float inv = 1.f / scale;  // exact where the scale is a power of two (1 / 2^-126 = 2^126 is finite)
+    if (grows) {
+      const float ratio = old / need;
+      const int part = PAIR ? warp & 1 : 0;
+#pragma unroll 1
+      for (int r = part * 4 + (lane >> 3); r < k.r0; r += PAIR ? 8 : 4) {
+        uint4* p = reinterpret_cast<uint4*>(page + r * kD + sub * 16);
+        const uint4 c = *p;
+        *p = make_uint4(recode4<F>(c.x, ratio), recode4<F>(c.y, ratio), recode4<F>(c.z, ratio), recode4<F>(c.w, ratio));
+      }
+    }
+    auto store = [&](int g, const uint4& lo, const uint4& hi) {
+      const int r = first + 4 * g + (lane >> 3);
+      if (r < k.r0 || r >= k.r1) return;
+      *reinterpret_cast<uint2*>(page + r * kD + at.x) = encode8<F>(lo, inv);
+      *reinterpret_cast<uint2*>(page + r * kD + at.y) = encode8<F>(hi, inv);
+    };
+#pragma unroll
+    for (int g = 0; g < H; ++g) store(g, x[g], y[g]);
+    for (int g = H; MORE && g < steps; ++g) {
+      uint4 lo, hi;
+      load(g, lo, hi);
+      if (!is_v) turn(g, lo, hi);
+      store(g, lo, hi);
+    }
+    __syncwarp();  // every lane has read the old scale, and a pair's other warp before it met this one
+    if (lane == 0 && (!PAIR || (warp & 1) == 0) && (k.r0 == 0 || grows)) *scale_at = scale;
+  }
+  if (PAIR) pair_sync();  // the maxima have been read: the next ones may be written
+}
+
+// Query rows: four tokens of a warp, heads [h0, h1), U of them in flight together.
+template <int LAYOUT, int U>
+__device__ __forceinline__ void turn_queries(const Rot8Args& a, const int* tok, int64_t i, int rows, int h0, int h1,
+                                             int cap_tokens) {
+  const int sub = threadIdx.x & 7;
+  const bool live = i < rows;
+  const int2 at = lane_chunks<LAYOUT>(sub, a.rope.n);
+  const __nv_bfloat16* src = a.q + i * a.ld_q;
+  __nv_bfloat16* dst = a.q_out + i * a.ld_q_out;
+  int index = 0;
+  if (a.positions == nullptr && live) {
+    const int b = owner_of(tok, a.B, (int)i);
+    index = seq_span(a.prev_len, a.seq_len, b, cap_tokens).prev + (int)i - tok[b];
+  }
+  const Turn t = lane_turn(a.rope, sub, position_of(a, i, index, live, sub));
+  Weights w;
+  if (a.q_norm != nullptr) w = lane_weights(a.q_norm, at);
+  for (int h = h0; h < h1; h += U) {
+    uint4 x[U], y[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!live || h + u >= h1) continue;
+      x[u] = ld_stream(src + (h + u) * kD + at.x);
+      y[u] = ld_stream(src + (h + u) * kD + at.y);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float v[16];
+      unpack16(x[u], y[u], v);
+      if (a.q_norm != nullptr) norm_head(v, w, a.eps);
+      turn_head<LAYOUT>(v, t, sub < a.rope.n);
+      pack16(v, x[u], y[u]);
+      if (!live || h + u >= h1) continue;
+      *reinterpret_cast<uint4*>(dst + (h + u) * kD + at.x) = x[u];
+      *reinterpret_cast<uint4*>(dst + (h + u) * kD + at.y) = y[u];
+    }
+  }
+}
+
+// tok [B + 1]: new tokens before sequence b; tou [B + 1]: touched blocks (of one KV head) before it.
+template <int P>
+__device__ __forceinline__ void prefixes(const Rot8Args& a, int* tok, int* tou, int* partial) {
   const int cap_tokens = a.nblk_cap * P;
   int* const out[2] = {tok, tou};
-  cta_prefixes<2>(B, out, partial, [&](int b, int (&x)[2]) {
+  cta_prefixes<2>(a.B, out, partial, [&](int b, int (&x)[2]) {
     const SeqSpan s = seq_span(a.prev_len, a.seq_len, b, cap_tokens);
     x[0] = s.seq - s.prev;
     x[1] = s.seq > s.prev ? (s.seq + P - 1) / P - s.prev / P : 0;
   });
   if (blockIdx.x == 0)
-    for (int b = tid; b < B; b += blockDim.x) report_span(a.status, a.prev_len, a.seq_len, b, cap_tokens);
-  const int parts = a.kv_parts + a.q_parts;
-  const int64_t items = (int64_t)tou[B] * parts;
-  const int64_t first = items * blockIdx.x / gridDim.x, last = items * (blockIdx.x + 1) / gridDim.x;
-  const int r = warp * 4 + (lane >> 3);  // the lane's row of a block
-  const int2 at_k = lane_chunks<LAYOUT>(sub, a.rope.n), at_v = make_int2(sub * 16, sub * 16 + 8);
-  const bool turns = sub < a.rope.n;
-  int blk = (int)(first / parts), part = (int)(first - (int64_t)blk * parts) - 1;
-  int b = 0, j = 0, r0 = 0, r1 = 0, buf = 0;
-  int64_t row = 0;
-  bool rows_ok = false, fresh = false;
-  Turn t;
-  for (int64_t it = first; it < last; ++it) {
-    bool enter = it == first;
-    if (++part == parts) {
-      part = 0;
-      ++blk;
-      enter = true;
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x) report_span(a.status, a.prev_len, a.seq_len, b, cap_tokens);
+}
+
+template <int P, int F, int LAYOUT>
+__global__ void __launch_bounds__(kR8Warps * 32, kR8PerSm) rotate8_kernel(const Rot8Args a) {
+  constexpr int H = P / 4 < kHold ? P / 4 : kHold, kSet = P / 4 / H;  // warps of one head's K or V
+  extern __shared__ int sm[];
+  __shared__ int partial[2 * 32];
+  __shared__ uint32_t top[2 * kR8Warps];
+  __shared__ float4 table[4][P][8];  // [quarter of a lane's pairs: c, c, s, s][row][lane]
+  int *tok = sm, *tou = sm + (a.B + 1);
+  prefixes<P>(a, tok, tou, partial);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane & 7;
+  const int rows = min(tok[a.B], a.n_tokens), first = warp % kSet * (4 * H);  // the warp's first row of a block
+  if ((int)blockIdx.x >= a.kv_ctas) {  // queries
+    const int64_t wn = (int64_t)(gridDim.x - a.kv_ctas) * kR8Warps;
+    const int64_t items = (int64_t)((rows + 3) / 4) * a.q_parts;
+    for (int64_t it = (int64_t)(blockIdx.x - a.kv_ctas) * kR8Warps + warp; it < items; it += wn) {
+      const int64_t group = (uint64_t)it / (unsigned)a.q_parts;
+      const int h0 = (int)(it - group * a.q_parts) * a.q_per;
+      turn_queries<LAYOUT, 4>(a, tok, group * 4 + (lane >> 3), rows, h0, min(a.Hq, h0 + a.q_per), a.nblk_cap * P);
     }
-    if (enter) {
-      b = owner_of(tou, B, blk);
-      const SeqSpan s = seq_span(a.prev_len, a.seq_len, b, cap_tokens);
-      j = s.prev / P + blk - tou[b];
-      r0 = max(s.prev - j * P, 0), r1 = min(s.seq - j * P, P);  // the block's new rows
-      const int64_t i0 = (int64_t)tok[b] + (j * P - s.prev);     // token row of its row 0
-      row = i0 + r;
-      rows_ok = i0 + r1 <= a.n_tokens;
-      fresh = rows_ok && r >= r0 && r < r1;
-      int pos = j * P + r;
-      if (a.positions != nullptr && fresh) {
-        pos = a.positions[row];
-        if (pos < 0) {
-          if (sub == 0) report(a.status, SCOUT_DEV_BAD_INDEX);
-          pos = 0;
-        }
-      }
-      t = lane_turn(a.rope, sub, (uint32_t)pos);
-    }
-    if (!rows_ok) {
+    return;
+  }
+  const unsigned parts = ((unsigned)a.Hkv + a.kv_heads - 1) / a.kv_heads;
+  const int64_t items = (int64_t)tou[a.B] * parts;
+  for (int64_t it = blockIdx.x; it < items; it += a.kv_ctas) {
+    const int blk = (int)((uint64_t)it / parts), part = (int)(it - (int64_t)blk * parts);
+    const Block k = block_of<P>(a, tok, tou, blk);
+    if (k.i0 + k.r1 > a.n_tokens) {  // the same for the CTA
       if (tid == 0) report(a.status, SCOUT_DEV_BAD_INDEX);
-      break;  // the rows are packed: those of the items that follow end no earlier
-    }
-    if (part >= a.kv_parts) {  // query heads
-      const int h0 = (part - a.kv_parts) * kQHeads, h1 = min(a.Hq, h0 + kQHeads);
-      float w[16];
-      if (a.q_norm != nullptr)
-        unpack16(__ldg(reinterpret_cast<const uint4*>(a.q_norm + at_k.x)),
-                 __ldg(reinterpret_cast<const uint4*>(a.q_norm + at_k.y)), w);
-      for (int h = h0; h < h1; h += 2) {
-        uint4 x[2], y[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (!fresh || h + u >= h1) continue;
-          const __nv_bfloat16* src = a.q + row * a.ld_q + (h + u) * kD;
-          x[u] = ld_stream(src + at_k.x);
-          y[u] = ld_stream(src + at_k.y);
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float v[16];
-          unpack16(x[u], y[u], v);
-          if (a.q_norm != nullptr) norm_head(v, w, a.eps);
-          turn_head<LAYOUT>(v, t, turns);
-          pack16(v, x[u], y[u]);
-          if (!fresh || h + u >= h1) continue;
-          __nv_bfloat16* dst = a.q_out + row * a.ld_q_out + (h + u) * kD;
-          *reinterpret_cast<uint4*>(dst + at_k.x) = x[u];
-          *reinterpret_cast<uint4*>(dst + at_k.y) = y[u];
-        }
-      }
       continue;
     }
-    // K and V of kHeads heads: set 2 u + s is head u's K (s = 0) or V
-    const int h0 = part * kHeads;
-    uint4 x[kSets], y[kSets];
-    int slot[kHeads];
-    float old[kSets];
+    // K and V of the part's heads, dealt to the warps (or pairs) so that each gets as many of either
+    const int p1 = 2 * min(a.Hkv, (part + 1) * a.kv_heads);
+    bool made = false;
+    for (int p = 2 * part * a.kv_heads + warp / kSet; p < p1 || !made; p += kR8Warps / kSet) {
+      const bool mine = p < p1;
+      const int h = p >> 1;
+      const bool is_v = (p + p / (kR8Warps / kSet)) & 1;
+      const int2 at = is_v ? make_int2(sub * 16, sub * 16 + 8) : lane_chunks<LAYOUT>(sub, a.rope.n);
+      const int64_t ld = a.ld[is_v];
+      const __nv_bfloat16* src = a.kv[is_v] + k.i0 * ld + h * kD;
+      auto load = [&](int g, uint4& lo, uint4& hi) {
+        const int r = first + 4 * g + (lane >> 3);
+        lo = hi = make_uint4(0u, 0u, 0u, 0u);
+        if (r < k.r0 || r >= k.r1) return;
+        lo = ldg_stream(src + r * ld + at.x);
+        hi = ldg_stream(src + r * ld + at.y);
+      };
+      uint4 x[H], y[H];
+      int slot = -1;
+      if (mine) {
+        slot = a.page_table[((int64_t)k.b * a.Hkv + h) * a.nblk_cap + k.j];  // in flight with the rows
 #pragma unroll
-    for (int u = 0; u < kHeads; ++u) {
-      slot[u] = -2;
-      if (h0 + u < a.Hkv) slot[u] = a.page_table[((int64_t)b * a.Hkv + h0 + u) * a.nblk_cap + j];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int2 at = s ? at_v : at_k;
-        x[2 * u + s] = y[2 * u + s] = make_uint4(0u, 0u, 0u, 0u);
-        if (!fresh || h0 + u >= a.Hkv) continue;
-        const __nv_bfloat16* src = a.kv[s] + row * a.ld[s] + (h0 + u) * kD;
-        x[2 * u + s] = ldg_stream(src + at.x);
-        y[2 * u + s] = ldg_stream(src + at.y);
+        for (int g = 0; g < H; ++g) load(g, x[g], y[g]);
       }
-    }
+      if (!made) {
+        made = true;
+        __syncthreads();  // the last item's table has been read
+        for (int g = warp; g < P / 4; g += kR8Warps) {
+          const int r = 4 * g + (lane >> 3);
+          const bool live = r >= k.r0 && r < k.r1;
+          const Turn t = lane_turn(a.rope, sub, position_of(a, k.i0 + r, k.j * P + r, live, sub));
 #pragma unroll
-    for (int u = 0; u < kHeads; ++u) {
-      if (slot[u] < 0 || slot[u] >= a.n_slots) {
-        if (tid == 0 && h0 + u < a.Hkv) report(a.status, SCOUT_DEV_BAD_INDEX);
-        slot[u] = -1;
+          for (int i = 0; i < 2; ++i) {
+            table[i][r][sub] = make_float4(t.c[4 * i], t.c[4 * i + 1], t.c[4 * i + 2], t.c[4 * i + 3]);
+            table[2 + i][r][sub] = make_float4(t.s[4 * i], t.s[4 * i + 1], t.s[4 * i + 2], t.s[4 * i + 3]);
+          }
+        }
+        __syncthreads();
+        if (!mine) break;
       }
-#pragma unroll
-      for (int s = 0; s < 2; ++s) old[2 * u + s] = r0 > 0 && slot[u] >= 0 ? a.scale[s][slot[u]] : 0.f;
-    }
-    {
-      float w[16];
-      if (a.k_norm != nullptr)
-        unpack16(__ldg(reinterpret_cast<const uint4*>(a.k_norm + at_k.x)),
-                 __ldg(reinterpret_cast<const uint4*>(a.k_norm + at_k.y)), w);
-#pragma unroll
-      for (int u = 0; u < kHeads; ++u) {
+      Weights w;
+      const bool norm = !is_v && a.k_norm != nullptr;
+      if (norm) w = lane_weights(a.k_norm, at);
+      auto turn = [&](int g, uint4& lo, uint4& hi) {
+        const int r = first + 4 * g + (lane >> 3);
         float v[16];
-        unpack16(x[2 * u], y[2 * u], v);
-        if (a.k_norm != nullptr) norm_head(v, w, a.eps);
-        turn_head<LAYOUT>(v, t, turns);
-        pack16(v, x[2 * u], y[2 * u]);
-      }
-    }
-    bool infinite = false;
+        unpack16(lo, hi, v);
+        if (norm) norm_head(v, w, a.eps);
+        if (sub < a.rope.n) {
+          Turn t;
 #pragma unroll
-    for (int i = 0; i < kSets; ++i) {
-      uint32_t m = max_abs2(max_abs2(max_abs2(max_abs2(0u, x[i].x), x[i].y), x[i].z), x[i].w);
-      m = max_abs2(max_abs2(max_abs2(max_abs2(m, y[i].x), y[i].y), y[i].z), y[i].w);
-      // rows that are not new hold zeros (a zero stays zero through norm and turn)
-      const uint32_t big = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-      if (lane == 0) top[buf][i][warp] = big;
-    }
-    __syncthreads();  // also: every thread has read the old scales
-    uint32_t big[kSets];
-#pragma unroll
-    for (int i = 0; i < kSets; ++i) {
-      big[i] = 0u;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) big[i] = max(big[i], top[buf][i][k]);
-      infinite |= big[i] == 0x7f80u;
-    }
-    buf ^= 1;
-    if (infinite) {  // the same for the CTA: the largest of the finite values (rare)
-#pragma unroll
-      for (int i = 0; i < kSets; ++i) {
-        uint32_t m = max_abs2(max_abs2(max_abs2(max_abs2(0u, finite2(x[i].x)), finite2(x[i].y)), finite2(x[i].z)), finite2(x[i].w));
-        m = max_abs2(max_abs2(max_abs2(max_abs2(m, finite2(y[i].x)), finite2(y[i].y)), finite2(y[i].z)), finite2(y[i].w));
-        const uint32_t v = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-        if (lane == 0) top[buf][i][warp] = v;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kSets; ++i) {
-        big[i] = 0u;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) big[i] = max(big[i], top[buf][i][k]);
-      }
-      buf ^= 1;
-    }
-#pragma unroll
-    for (int u = 0; u < kHeads; ++u) {
-      if (slot[u] < 0) continue;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int i = 2 * u + s;
-        const int2 at = s ? at_v : at_k;
-        const float need = pow2_biased(scale_exponent<F>(__uint_as_float(big[i] << 16)));
-        // the scale of a block with cached tokens never shrinks
-        const bool grows = r0 > 0 && need > old[i];
-        const float scale = r0 > 0 && !grows ? old[i] : need;
-        uint8_t* page = a.pool[s] + (int64_t)slot[u] * (P * kD) + r * kD;
-        if (r < r0 && grows) {
-          const float ratio = old[i] / need;
-          uint2 *p0 = reinterpret_cast<uint2*>(page + at.x), *p1 = reinterpret_cast<uint2*>(page + at.y);
-          const uint2 c0 = *p0, c1 = *p1;
-          *p0 = make_uint2(recode4<F>(c0.x, ratio), recode4<F>(c0.y, ratio));
-          *p1 = make_uint2(recode4<F>(c1.x, ratio), recode4<F>(c1.y, ratio));
+          for (int i = 0; i < 2; ++i) {
+            const float4 c = table[i][r][sub], s = table[2 + i][r][sub];
+            t.c[4 * i] = c.x, t.c[4 * i + 1] = c.y, t.c[4 * i + 2] = c.z, t.c[4 * i + 3] = c.w;
+            t.s[4 * i] = s.x, t.s[4 * i + 1] = s.y, t.s[4 * i + 2] = s.z, t.s[4 * i + 3] = s.w;
+          }
+          turn_head<LAYOUT>(v, t, true);
         }
-        if (fresh) {
-          const float inv = 1.f / scale;  // exact where the scale is a power of two (1 / 2^-126 = 2^126 is finite)
-          *reinterpret_cast<uint2*>(page + at.x) = encode8<F>(x[i], inv);
-          *reinterpret_cast<uint2*>(page + at.y) = encode8<F>(y[i], inv);
-        }
-        if (tid == 0 && (r0 == 0 || grows)) a.scale[s][slot[u]] = scale;
-      }
+        pack16(v, lo, hi);
+      };
+      quantise<P, F, H, false, (kSet > 1)>(a, k, is_v, slot, at, first, H, x, y, top, load, turn);
     }
   }
 }
 
-// the two rows of the largest batch, the prefixes' part and the maxima: within what needs no request
-static_assert((2 * 32 + 2 * kMaxBatch + 2 + 4 * kHeads * 16) * sizeof(int) <= 48 * 1024, "48 KB of shared memory");
+template <int P, int F, int LAYOUT>
+__global__ void __launch_bounds__(kR8Warps * 32, 4) rotate8_few_kernel(const Rot8Args a) {
+  extern __shared__ int sm[];
+  __shared__ int partial[2 * 32];
+  int *tok = sm, *tou = sm + (a.B + 1);
+  prefixes<P>(a, tok, tou, partial);
+  const int lane = threadIdx.x & 31, sub = lane & 7;
+  const int64_t wn = (int64_t)gridDim.x * kR8Warps;
+  const unsigned sets = 2 * (unsigned)a.Hkv;
+  const int64_t n_kv = (int64_t)tou[a.B] * sets;
+  const int rows = min(tok[a.B], a.n_tokens);
+  const int64_t items = n_kv + (int64_t)((rows + 3) / 4) * a.Hq;
+  for (int64_t it = (int64_t)blockIdx.x * kR8Warps + (threadIdx.x >> 5); it < items; it += wn) {
+    if (it >= n_kv) {
+      const int64_t group = (uint64_t)(it - n_kv) / (unsigned)a.Hq;
+      const int h = (int)(it - n_kv - group * a.Hq);
+      turn_queries<LAYOUT, 1>(a, tok, group * 4 + (lane >> 3), rows, h, h + 1, a.nblk_cap * P);
+      continue;
+    }
+    const int blk = (int)((uint64_t)it / sets), p = (int)(it - (int64_t)blk * sets);
+    const int h = p >> 1;
+    const bool is_v = p & 1;
+    const Block k = block_of<P>(a, tok, tou, blk);
+    if (k.i0 + k.r1 > a.n_tokens) {
+      if (lane == 0) report(a.status, SCOUT_DEV_BAD_INDEX);
+      continue;
+    }
+    const int slot = a.page_table[((int64_t)k.b * a.Hkv + h) * a.nblk_cap + k.j];  // in flight with the rows
+    const int2 at = is_v ? make_int2(sub * 16, sub * 16 + 8) : lane_chunks<LAYOUT>(sub, a.rope.n);
+    const int64_t ld = a.ld[is_v];
+    const __nv_bfloat16* src = a.kv[is_v] + k.i0 * ld + h * kD;
+    Weights w;
+    const bool norm = !is_v && a.k_norm != nullptr;
+    if (norm) w = lane_weights(a.k_norm, at);
+    auto load = [&](int g, uint4& lo, uint4& hi) {
+      const int r = k.r0 + 4 * g + (lane >> 3);
+      lo = hi = make_uint4(0u, 0u, 0u, 0u);
+      if (r >= k.r1) return;
+      lo = ldg_stream(src + r * ld + at.x);
+      hi = ldg_stream(src + r * ld + at.y);
+    };
+    auto turn = [&](int g, uint4& lo, uint4& hi) {
+      const int r = k.r0 + 4 * g + (lane >> 3);
+      const Turn t = lane_turn(a.rope, sub, position_of(a, k.i0 + r, k.j * P + r, r < k.r1, sub));
+      float v[16];
+      unpack16(lo, hi, v);
+      if (norm) norm_head(v, w, a.eps);
+      turn_head<LAYOUT>(v, t, sub < a.rope.n);
+      pack16(v, lo, hi);
+    };
+    uint4 x[1], y[1];
+    load(0, x[0], y[0]);
+    quantise<P, F, 1, true, false>(a, k, is_v, slot, at, k.r0, (k.r1 - k.r0 + 3) / 4, x, y, nullptr, load, turn);
+  }
+}
 
-template <int P, int F>
-int launch_rotate8(int layout, const Rot8Args& a, int grid, size_t smem, cudaStream_t st) {
-  if (layout == SCOUT_ROPE_HALF)
-    rotate8_kernel<P, F, SCOUT_ROPE_HALF><<<grid, P * 8, smem, st>>>(a);
-  else
-    rotate8_kernel<P, F, SCOUT_ROPE_INTERLEAVED><<<grid, P * 8, smem, st>>>(a);
+// the prefixes' static part, the two rows of the largest batch and the largest table: what a CTA may have without a request
+constexpr size_t kStatic8 = (2 * 32 + 2 * kR8Warps) * sizeof(int), kTable8 = 4 * 8 * 16;
+
+template <int P, int F, int LAYOUT>
+int launch_rotate8(Rot8Args& a, cudaStream_t st) {
+  // at most n_tokens / P + 2 B blocks of a head are touched (each span's two ends partly)
+  const int64_t blocks = (int64_t)a.n_tokens / P + 2 * (int64_t)(a.B < a.n_tokens ? a.B : a.n_tokens);
+  const size_t smem = (size_t)(2 * a.B + 2) * sizeof(int);
+  const int64_t groups = ((int64_t)a.n_tokens + 3) / 4, none = a.n_tokens == 0;  // (without rows: the report alone)
+  if (a.n_tokens <= kFewTokens * (int64_t)a.B) {
+    const int64_t want = (blocks * 2 * a.Hkv + groups * a.Hq + kR8Warps - 1) / kR8Warps + none;
+    const int64_t most = (int64_t)sm_count() * 8;
+    rotate8_few_kernel<P, F, LAYOUT><<<(int)(want < most ? want : most), kR8Warps * 32, smem, st>>>(a);
+    return launch_status();
+  }
+  if (smem + kStatic8 + kTable8 * P > 48 * 1024 &&
+      cudaFuncSetAttribute(rotate8_kernel<P, F, LAYOUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (2 * kMaxBatch + 2) * (int)sizeof(int)) != cudaSuccess)
+    return SCOUT_ERR_CUDA;
+  const int64_t most = (int64_t)sm_count() * kR8PerSm;  // CTAs at a time
+  // the CTAs by the bytes that the keys and values, and the queries, move
+  const float share = 768.f * a.Hkv / (768.f * a.Hkv + 512.f * a.Hq);
+  const int64_t kv_most = (int64_t)max(1, (int)(most * share));
+  a.kv_heads = max(1, (int)(a.Hkv / max((int64_t)1, kv_most / blocks)));
+  const int64_t kv_want = blocks * ((a.Hkv + a.kv_heads - 1) / a.kv_heads);
+  a.kv_ctas = (int)(kv_want < kv_most * kR8Waves ? kv_want : kv_most * kR8Waves);
+  a.q_per = kR8Heads;
+  a.q_parts = (a.Hq + a.q_per - 1) / a.q_per;
+  const int64_t q_want = (groups * a.q_parts + kR8Warps - 1) / kR8Warps, q_most = max((int64_t)1, most - kv_most) * kR8Waves;
+  const int grid = a.kv_ctas + (int)(q_want < q_most ? q_want : q_most);
+  rotate8_kernel<P, F, LAYOUT><<<grid, kR8Warps * 32, smem, st>>>(a);
   return launch_status();
 }
 
+template <int P, int F>
+int dispatch_rotate8(int layout, Rot8Args& a, cudaStream_t st) {
+  return layout == SCOUT_ROPE_HALF ? launch_rotate8<P, F, SCOUT_ROPE_HALF>(a, st)
+                                   : launch_rotate8<P, F, SCOUT_ROPE_INTERLEAVED>(a, st);
+}
+
 template <int F>
-int dispatch_rotate8(int P, int layout, const Rot8Args& a, int grid, size_t smem, cudaStream_t st) {
+int dispatch_rotate8(int P, int layout, Rot8Args& a, cudaStream_t st) {
   switch (P) {
-    case 16: return launch_rotate8<16, F>(layout, a, grid, smem, st);
-    case 32: return launch_rotate8<32, F>(layout, a, grid, smem, st);
-    default: return launch_rotate8<64, F>(layout, a, grid, smem, st);
+    case 16: return dispatch_rotate8<16, F>(layout, a, st);
+    case 32: return dispatch_rotate8<32, F>(layout, a, st);
+    default: return dispatch_rotate8<64, F>(layout, a, st);
   }
 }
 
@@ -304,18 +475,10 @@ extern "C" int scout_append_rotated_kv8(int fmt, const void* K_new, int64_t ld_k
   a.Hkv = Hkv;
   a.Hq = Hq;
   a.nblk_cap = nblk_cap;
-  a.kv_parts = (Hkv + kHeads - 1) / kHeads;
-  a.q_parts = (Hq + kQHeads - 1) / kQHeads;
   a.n_slots = n_slots;
   a.rope = rope_of(rope);
   a.eps = eps;
   a.status = dev_status;
-  // at most n_tokens / P + 2 B blocks of a head are touched (each span's two ends partly)
-  const int64_t blocks = (int64_t)n_tokens / P + 2 * (int64_t)(B < n_tokens ? B : n_tokens);
-  const int64_t want = blocks * (a.kv_parts + a.q_parts) + (n_tokens == 0);  // (without rows: the report alone)
-  const int most = sm_count() * (1024 / (P * 8));
-  const int grid = (int)(want < most ? want : most);
-  const size_t smem = (size_t)(2 * B + 2) * sizeof(int);
-  return fmt == SCOUT_FP8_E4M3 ? dispatch_rotate8<SCOUT_FP8_E4M3>(P, rope->layout, a, grid, smem, stream)
-                               : dispatch_rotate8<SCOUT_FP8_E5M2>(P, rope->layout, a, grid, smem, stream);
+  return fmt == SCOUT_FP8_E4M3 ? dispatch_rotate8<SCOUT_FP8_E4M3>(P, rope->layout, a, stream)
+                               : dispatch_rotate8<SCOUT_FP8_E5M2>(P, rope->layout, a, stream);
 }

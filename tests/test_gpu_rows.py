@@ -408,7 +408,7 @@ def test_append8_bad_blocks_are_skipped_and_reported():
     for a, b in zip(one, two):
         assert same(a, b)
     assert int(st[0]) == int(st[1]) == 1 and same(q, w.turned(rope, w.q, None))
-    # rows that end early: the blocks before are written, the others and their queries not
+    # rows that end early: the blocks before are written, the others not, and the queries of the rows there are
     st = word()
     q_out = torch.full((60, 2, D), 7.0, dtype=torch.bfloat16, device="cuda")
     one, two = ([x.clone() for x in (K[0], V[0], K[1], V[1])] for _ in range(2))
@@ -416,7 +416,7 @@ def test_append8_bad_blocks_are_skipped_and_reported():
     bs.append_kv8(w.turned(rope, w.K, None)[:60], w.V[:60], w.table, w.seq_t, 2, 2, 32, *two)
     for a, b in zip(one, two):
         assert same(a, b)
-    assert int(st) == 1 and same(q_out[:50], w.turned(rope, w.q, None)[:50]) and torch.all(q_out[50:] == 7.0)
+    assert int(st) == 1 and same(q_out, w.turned(rope, w.q, None)[:60])
     # a negative position counts as 0
     st = word()
     pos = w.pos.copy()
