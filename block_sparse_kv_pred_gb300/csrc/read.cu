@@ -1,13 +1,19 @@
 // scout_read_kv and scout_read_kv8: blocks of a paged cache back as bf16 rows in token order.
 //
-// A warp takes a block of one KV head, its K or its V.  Sixteen lanes hold a row (16 bytes of bf16, 8 of codes a lane), all of
-// the block's loads are in flight together, and 16-byte stores write whole rows.
+// A warp takes 16 or 32 rows of a block of one KV head, of its K or its V.  Eight lanes hold a row, 32 bytes of bf16 each: all
+// of the item's loads are in flight together, and a lane stores its 32 bytes at once, a whole sector (with two 16-byte
+// stores the prompts below take 81 us, with sixteen lanes and 16-byte accesses 73).  One item a warp: a grid of resident
+// CTAs that stride over the items takes 10% longer.
+//
+// Bound by DRAM: GB300, 8 prompts of up to 16K tokens, 8 KV heads, out of an 8-bit cache: 66.3 us for 428 MB (6.5 TB/s, 0.96 of
+// the measured copy bandwidth), out of a bf16 one 85.5 us for 570 MB; 320 blocks by list: 2.9 us, the launch and two dependent reads.
 #include "fp8.cuh"
 
 namespace scout {
 namespace {
 
-constexpr int kReadWarps = 8;
+constexpr int kReadWarps = 2;
+constexpr int kMaxItems = 1 << 29;  // blocks of a call
 
 struct ReadArgs {
   const uint8_t* pool[2];
@@ -40,79 +46,107 @@ __device__ __forceinline__ uint4 widen8(const uint2& c, float scale) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-template <int P, int F>
+// 32 bytes at an address that is a multiple of 32
+__device__ __forceinline__ void ld32(const void* p, uint4& x, uint4& y) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w), "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+               : "l"(p));
+}
+__device__ __forceinline__ void st32(void* p, const uint4& x, const uint4& y) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w),
+               "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+               : "memory");
+}
+
+// R: rows of a warp's item.
+template <int P, int F, int R>
 __global__ void __launch_bounds__(kReadWarps * 32) read_kernel(const ReadArgs a) {
-  const int lane = threadIdx.x & 31, half = lane >> 4, chunk = lane & 15;
-  const int64_t wn = (int64_t)gridDim.x * kReadWarps;
-  for (int64_t w = (int64_t)blockIdx.x * kReadWarps + (threadIdx.x >> 5); w < 2 * a.n_items; w += wn) {
-    const int64_t it = w >> 1;
-    const int kv = (int)(w & 1);
-    int b, h, j;
-    if (a.block_list != nullptr) {
-      const int2 e = __ldg(reinterpret_cast<const int2*>(a.block_list) + it);
-      if (e.x == -1 && e.y == -1) continue;
-      if (e.x < 0 || e.x >= a.B * a.Hkv || e.y < 0 || e.y >= a.nblk_cap) {
-        if (lane == 0) report(a.status, SCOUT_DEV_BAD_INDEX);
-        continue;
-      }
-      b = e.x / a.Hkv;
-      h = e.x - b * a.Hkv;
-      j = e.y;
-    } else {
-      const unsigned n = (unsigned)it, heads = (unsigned)a.Hkv, cap = (unsigned)a.nblk_cap;
-      const unsigned q = a.heads_inner ? n / heads : n / cap, m = a.heads_inner ? n - q * heads : n - q * cap;
-      b = (int)(a.heads_inner ? q / cap : q / heads);
-      h = (int)(a.heads_inner ? m : q - b * heads);
-      j = (int)(a.heads_inner ? q - b * cap : m);
+  constexpr int kParts = P / R;  // items of a block's K or V
+  const int lane = threadIdx.x & 31, quad = lane >> 3, sub = lane & 7;
+  const int64_t w = (int64_t)blockIdx.x * kReadWarps + (threadIdx.x >> 5);
+  if (w >= 2 * kParts * a.n_items) return;
+  const int64_t it = w / (2 * kParts);
+  const int kv = (int)(w & 1), part = (int)(w / 2 % kParts);
+  int b, h, j;
+  if (a.block_list != nullptr) {
+    const int2 e = __ldg(reinterpret_cast<const int2*>(a.block_list) + it);
+    if (e.x == -1 && e.y == -1) return;
+    if (e.x < 0 || e.x >= a.B * a.Hkv || e.y < 0 || e.y >= a.nblk_cap) {
+      if (lane == 0) report(a.status, SCOUT_DEV_BAD_INDEX);
+      return;
     }
-    const int64_t t0 = (int64_t)j * P, n = a.seq_len[b];
-    if (t0 >= n) continue;
-    const int slot = a.page_table[((int64_t)b * a.Hkv + h) * a.nblk_cap + j];
-    if (slot < 0 || slot >= a.n_slots) {
-      if (lane == 0 && (a.block_list != nullptr || slot != -1)) report(a.status, SCOUT_DEV_BAD_INDEX);
-      continue;
-    }
-    int rows = (int)(n - t0 < P ? n - t0 : P);
-    if (t0 + rows > a.T) {
-      if (lane == 0) report(a.status, SCOUT_DEV_OVERFLOW);
-      rows = (int)(a.T > t0 ? a.T - t0 : 0);
-    }
-    __nv_bfloat16* dst = a.out[kv] + b * a.stride_b + h * a.stride_h + (t0 + half) * a.stride_t + chunk * 8;
-    const int64_t step = 2 * a.stride_t;
-    if constexpr (F == kCopy) {
-      const uint4* src = reinterpret_cast<const uint4*>(a.pool[kv]) + (int64_t)slot * (P * 16) + lane;
-      uint4 v[P / 2];
-#pragma unroll
-      for (int i = 0; i < P / 2; ++i)
-        if (2 * i + half < rows) v[i] = ldg_stream(src + i * 32);
-#pragma unroll
-      for (int i = 0; i < P / 2; ++i)
-        if (2 * i + half < rows) *reinterpret_cast<uint4*>(dst + i * step) = v[i];
-    } else {
-      const uint2* src = reinterpret_cast<const uint2*>(a.pool[kv]) + (int64_t)slot * (P * 16) + lane;
-      const float scale = a.scale[kv][slot];
-      uint2 v[P / 2];
-#pragma unroll
-      for (int i = 0; i < P / 2; ++i)
-        if (2 * i + half < rows) v[i] = __ldg(src + i * 32);
-#pragma unroll
-      for (int i = 0; i < P / 2; ++i)
-        if (2 * i + half < rows) *reinterpret_cast<uint4*>(dst + i * step) = widen8<F>(v[i], scale);
-    }
+    b = e.x / a.Hkv;
+    h = e.x - b * a.Hkv;
+    j = e.y;
+  } else {
+    const unsigned n = (unsigned)it, heads = (unsigned)a.Hkv, cap = (unsigned)a.nblk_cap;
+    const unsigned q = a.heads_inner ? n / heads : n / cap, m = a.heads_inner ? n - q * heads : n - q * cap;
+    b = (int)(a.heads_inner ? q / cap : q / heads);
+    h = (int)(a.heads_inner ? m : q - b * heads);
+    j = (int)(a.heads_inner ? q - b * cap : m);
   }
+  const int64_t t0 = (int64_t)j * P + part * R, n = a.seq_len[b];
+  if (t0 >= n) return;
+  const int slot = a.page_table[((int64_t)b * a.Hkv + h) * a.nblk_cap + j];
+  if (slot < 0 || slot >= a.n_slots) {
+    if (lane == 0 && (a.block_list != nullptr || slot != -1)) report(a.status, SCOUT_DEV_BAD_INDEX);
+    return;
+  }
+  int rows = (int)(n - t0 < R ? n - t0 : R);
+  if (t0 + rows > a.T) {
+    if (lane == 0) report(a.status, SCOUT_DEV_OVERFLOW);
+    rows = (int)(a.T > t0 ? a.T - t0 : 0);
+  }
+  __nv_bfloat16* dst = a.out[kv] + b * a.stride_b + h * a.stride_h + (t0 + quad) * a.stride_t + sub * 16;
+  const int64_t step = 4 * a.stride_t, row = (int64_t)slot * P + part * R + quad;
+  if constexpr (F == kCopy) {
+    const uint8_t* src = a.pool[kv] + row * (kD * 2) + sub * 32;
+    uint4 x[R / 4], y[R / 4];
+#pragma unroll
+    for (int i = 0; i < R / 4; ++i)
+      if (4 * i + quad < rows) ld32(src + i * (4 * kD * 2), x[i], y[i]);
+#pragma unroll
+    for (int i = 0; i < R / 4; ++i)
+      if (4 * i + quad < rows) st32(dst + i * step, x[i], y[i]);
+  } else {
+    const uint8_t* src = a.pool[kv] + row * kD + sub * 16;
+    const float scale = a.scale[kv][slot];
+    uint4 v[R / 4];
+#pragma unroll
+    for (int i = 0; i < R / 4; ++i)
+      if (4 * i + quad < rows) v[i] = ldg_stream(src + i * (4 * kD));
+#pragma unroll
+    for (int i = 0; i < R / 4; ++i)
+      if (4 * i + quad < rows)
+        st32(dst + i * step, widen8<F>(make_uint2(v[i].x, v[i].y), scale), widen8<F>(make_uint2(v[i].z, v[i].w), scale));
+  }
+}
+
+template <int P, int F, int R>
+int launch_read(const ReadArgs& a, cudaStream_t st) {
+  const int64_t grid = (2 * (P / R) * a.n_items + kReadWarps - 1) / kReadWarps;  // at most twice kMaxItems
+  read_kernel<P, F, R><<<(unsigned)grid, kReadWarps * 32, 0, st>>>(a);
+  return launch_status();
+}
+
+template <int P, int F>
+int launch_read(const ReadArgs& a, cudaStream_t st) {
+  // Items of 16 rows where they are few (320 blocks: 2.9 us against 3.1 of 32 rows), otherwise of 32 (all blocks into
+  // [B][T][Hkv][D] rows: 67.2 us against 69.0).
+  if (P == 16 || 2 * (P / 16) * a.n_items <= 32 * (int64_t)sm_count()) return launch_read<P, F, 16>(a, st);
+  return launch_read<P, F, P == 16 ? 16 : 32>(a, st);
 }
 
 template <int F>
 int launch_read(int P, const ReadArgs& a, cudaStream_t st) {
-  const int64_t want = (2 * a.n_items + kReadWarps - 1) / kReadWarps;
-  const int grid = (int)(want < sm_count() * 8 ? want : sm_count() * 8);
   switch (P) {
-    case 16: read_kernel<16, F><<<grid, kReadWarps * 32, 0, st>>>(a); break;
-    case 32: read_kernel<32, F><<<grid, kReadWarps * 32, 0, st>>>(a); break;
-    default: read_kernel<64, F><<<grid, kReadWarps * 32, 0, st>>>(a); break;
+    case 16: return launch_read<16, F>(a, st);
+    case 32: return launch_read<32, F>(a, st);
+    default: return launch_read<64, F>(a, st);
   }
-  return launch_status();
 }
+
+inline bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 int read_blocks(int fmt, const void* K_pool, const void* V_pool, const float* K_scale, const float* V_scale,
                 int64_t n_slots, const int32_t* page_table, const int32_t* seq_len, int B, int Hkv, int D, int P,
@@ -125,8 +159,9 @@ int read_blocks(int fmt, const void* K_pool, const void* V_pool, const float* K_
       (block_list != nullptr && n_list < 0) || host_out < 0 || host_out > 1)
     return SCOUT_ERR_INVALID_ARG;
   if (D != kD || !valid_P(P) || nblk_cap > kMaxNblk || n_slots > 0x7fffffffLL ||
-      (int64_t)B * Hkv > 0x7fffffffLL / nblk_cap || stride_b % 8 != 0 || stride_h % 8 != 0 || stride_t % 8 != 0 ||
-      !aligned16(K_pool) || !aligned16(V_pool) || !aligned16(K_out) || !aligned16(V_out) ||
+      (int64_t)B * Hkv > kMaxItems / nblk_cap || (block_list != nullptr && n_list > kMaxItems) || stride_b % 16 != 0 || stride_h % 16 != 0 || stride_t % 16 != 0 ||
+      !aligned(K_pool, fmt == kCopy ? 32 : 16) || !aligned(V_pool, fmt == kCopy ? 32 : 16) || !aligned(K_out, 32) ||
+      !aligned(V_out, 32) ||
       (reinterpret_cast<uintptr_t>(block_list) & 7u))
     return SCOUT_ERR_UNSUPPORTED;
   if (block_list != nullptr && n_list == 0) return SCOUT_OK;

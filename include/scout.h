@@ -601,9 +601,10 @@ int scout_sparse_attn8_merge(int fmt, const void* q, const void* K_pool, const v
  * Of a block, the rows t < seq_len[b] are written; everything else in K_out and V_out is left as it was.  Rows with
  * t >= T are left out and set SCOUT_DEV_OVERFLOW.
  * scout_read_kv copies; scout_read_kv8 writes code * scale, rounded to bf16 (exact where the scale is a power of two).
- * No workspace.  Requires P in {16, 32, 64}, D = 128, T >= 1, strides >= 0 and multiples of 8, block_list 8-byte, the
- * other tensors 16-byte aligned, nblk_cap <= 8192, n_slots, B * Hkv * nblk_cap < 2^31; with host_out K_out and V_out must be mapped from
- * their first byte to their last (else SCOUT_ERR_UNSUPPORTED). */
+ * No workspace.  Requires P in {16, 32, 64}, D = 128, T >= 1, strides >= 0 and multiples of 16, block_list 8-byte, K_out,
+ * V_out and bf16 pools 32-byte, 8-bit pools 16-byte aligned, nblk_cap <= 8192, n_slots < 2^31, n_list and
+ * B * Hkv * nblk_cap <= 2^29; with host_out K_out and V_out must be mapped from their first byte to their last (else
+ * SCOUT_ERR_UNSUPPORTED). */
 int scout_read_kv(const void* K_pool, const void* V_pool, int64_t n_slots, const int32_t* page_table,
                   const int32_t* seq_len, int B, int Hkv, int D, int P, int nblk_cap, const int32_t* block_list,
                   int n_list, void* K_out, void* V_out, int64_t stride_b, int64_t stride_h, int64_t stride_t, int64_t T,

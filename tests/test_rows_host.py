@@ -195,7 +195,7 @@ READS = [({}, OK), (dict(Kp=None), INVALID), (dict(Vp=None), INVALID), (dict(tab
          (dict(Hkv=0), INVALID), (dict(cap=0), INVALID), (dict(T=0), INVALID), (dict(sb=-8), INVALID), (dict(sh=-8), INVALID),
          (dict(st=-8), INVALID), (dict(n_list=-1), INVALID), (dict(host=2), INVALID), (dict(D=64), UNSUPPORTED),
          (dict(P=24), UNSUPPORTED), (dict(cap=8193), UNSUPPORTED), (dict(B=1 << 20, cap=1 << 12), UNSUPPORTED),
-         (dict(n_slots=1 << 31), UNSUPPORTED), (dict(st=132), UNSUPPORTED), (dict(sh=4), UNSUPPORTED), (dict(sb=12), UNSUPPORTED),
+         (dict(n_slots=1 << 31), UNSUPPORTED), (dict(st=132), UNSUPPORTED), (dict(sh=8), UNSUPPORTED), (dict(sb=24), UNSUPPORTED), (dict(Ko=ctypes.c_void_p(4112)), UNSUPPORTED),
          (dict(Kp=ODD), UNSUPPORTED), (dict(Vo=ODD), UNSUPPORTED), (dict(list=ctypes.c_void_p(4100)), UNSUPPORTED)]
 
 
