@@ -8,7 +8,7 @@
 // W and X tiles (64 k-columns, 128-byte swizzle) stream in by TMA through a ring of
 // shared-memory stages guarded by mbarriers, up to four k-blocks per stage (measured on
 // GB300: one k-block per stage streams ~25% slower, the barrier round trip of a stage
-// being paid per 22 KB instead of per 88 KB); one thread issues tcgen05.mma into a
+// being paid per 22 KB instead of per 67 to 88 KB); one thread issues tcgen05.mma into a
 // TMEM accumulator and frees each stage with tcgen05.commit.  The K dimension is
 // split over the CTAs of a thread-block cluster so that about one CTA runs per SM.
 // The batch columns of the accumulator are dealt out over the cluster's CTAs: each
@@ -34,7 +34,8 @@ constexpr int kStages = 16;  // upper bound; the ring takes what shared memory h
 constexpr int kThreadsQ = 128;
 constexpr int kMaxN = 256;    // padded batch (MMA N) limit
 constexpr int kWTileBytes = kBM * kBK * 2;  // 16 KiB
-constexpr int kRingBytes = 224 * 1024;      // of shared memory, at most
+constexpr int kRingBytes = 224 * 1024;      // of shared memory, at most, the exchange included
+constexpr int kApartBytes = 32 * 1024;      // an exchange that lies beside the ring, at most
 
 // --- cluster PTX --------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -42,8 +43,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 __device__ __forceinline__ uint32_t map_peer(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -62,7 +66,8 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int n) {
 struct GemmArgs {
   __nv_bfloat16* Q;
   int M, N, n_pad, tmem_cols, kblocks, stages, x_tile_bytes;
-  int kps;  // k-blocks per ring stage
+  int kps;     // k-blocks per ring stage
+  int recv_at; // bytes from the ring's start to what peers write: past the ring, or 0 where it does not fit beside it
   int32_t* status;
   // of the rotated form
   const int32_t* positions;
@@ -140,6 +145,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) predict_q_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  if (S > 1) cluster_arrive();  // this CTA runs: its shared memory may be written
 
   if (warp == 0 && lane == 0) {
     // TMA producer: the rest of the k range, each stage once the MMAs have freed it
@@ -194,11 +200,12 @@ __global__ void __launch_bounds__(kThreadsQ, 1) predict_q_kernel(const __grid_co
   const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
   const int ngroups = a.n_pad / 8;
   const int owned = (ngroups + (int)S - 1) / (int)S;
-  float* recv = reinterpret_cast<float*>(base);  // the stage ring is idle now
+  float* recv = reinterpret_cast<float*>(base + a.recv_at);
   float* mine = recv + (int)rank * owned * 8 * kBM;  // this CTA's own slots: no peer writes them
   float v[8];
   if (S > 1) {
-    cluster_sync();  // every CTA of the cluster is done with its ring: it may be written
+    cluster_wait();
+    if (a.recv_at == 0) cluster_sync();  // every CTA of the cluster is done with its ring: it may be written
     for (int g = 0; g < ngroups; ++g) {
       const uint32_t owner = (uint32_t)g % S;
       if (owner == rank) continue;
@@ -294,11 +301,6 @@ int predict(const void* X, const void* W, void* Q, int M, int N, int K, const in
   while (a.tmem_cols < a.n_pad) a.tmem_cols <<= 1;
   a.kblocks = K / kBK;
   a.x_tile_bytes = (a.n_pad * 128 + 1023) / 1024 * 1024;
-  // ~220 KB in flight per SM, in stages of up to kMaxKps k-blocks (the fewer the stages, the
-  // fewer barrier round trips per byte) but at least two, so that copies and MMAs overlap
-  a.kps = max(1, min(kMaxKps, kRingBytes / 2 / (kWTileBytes + a.x_tile_bytes)));
-  const int stage_bytes = a.kps * (kWTileBytes + a.x_tile_bytes);
-  a.stages = min(kStages, kRingBytes / stage_bytes);
   a.status = dev_status;
   if constexpr (LAYOUT != kPlain) {
     a.positions = positions;
@@ -310,7 +312,19 @@ int predict(const void* X, const void* W, void* Q, int M, int N, int K, const in
   const int cap = launch != nullptr && launch->max_ctas > 0 ? launch->max_ctas : sm_count();
   const int S = max(1, min(min(8, a.kblocks), cap / tiles));  // split-K so tiles x S fits the CTA budget
   const int owned = (a.n_pad / 8 + S - 1) / S;                  // column groups per CTA in the reduction
-  const size_t smem = 1024 + (size_t)max(a.stages * stage_bytes, S * owned * 8 * kBM * 4);
+  // ~200 KB in flight per SM, in stages of up to kMaxKps k-blocks (the fewer the stages, the fewer barrier round
+  // trips per byte): three of them where they hold two k-blocks each (GB300, 40 x 5120 x 5120: 14.7 us, 14.9 with two
+  // stages of four, 15.7 with five of two), otherwise at least two, so that copies and MMAs overlap.  What the cluster's
+  // CTAs exchange lies beside the ring where it is small: a CTA then sends without waiting for its peers' rings (16.8 -> 15.5
+  // us of the rotated form).
+  const int exchange = S * owned * 8 * kBM * 4, tile_bytes = kWTileBytes + a.x_tile_bytes;
+  const int room = kRingBytes - (S > 1 && exchange <= kApartBytes ? exchange : 0);
+  a.kps = room / 3 / tile_bytes >= 2 ? min(kMaxKps, room / 3 / tile_bytes) : max(1, min(kMaxKps, room / 2 / tile_bytes));
+  const int stage_bytes = a.kps * tile_bytes;
+  a.stages = min(kStages, room / stage_bytes);
+  const int ring = a.stages * stage_bytes;
+  a.recv_at = room < kRingBytes ? ring : 0;
+  const size_t smem = 1024 + (size_t)(a.recv_at > 0 ? ring + exchange : max(ring, exchange));
   CUtensorMap tmW, tmX;
   if (!make_map(&tmW, W, N, K, kBM) || !make_map(&tmX, X, M, K, a.n_pad)) return SCOUT_ERR_UNSUPPORTED;
   // the same limit for every call: calls on several host threads do not lower it for one another (the
