@@ -47,6 +47,31 @@ inline unsigned early_start_attrs(const scout_launch* launch, cudaLaunchAttribut
 // dependents start (counted per CTA; a CTA that exits counts as well).
 __device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void release_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Launches a kernel that may be scheduled while the one before it on the stream ends: it begins with
+// start_dependent(), which waits for that one's completion (and the visibility of its writes) before anything is read
+// or written, and lets the next such kernel be scheduled in turn.
+template <class... P, class... A>
+int launch_dependent(void (*kernel)(P...), int64_t grid, int block, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3((unsigned)block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return SCOUT_ERR_CUDA;
+  }
+  return SCOUT_OK;
+}
+__device__ __forceinline__ void start_dependent() {
+  wait_prerequisites();
+  release_dependents();
+}
 int sm_count();  // SMs of the current device
 // device address of a host range [p, p + bytes) in pinned, mapped host memory, or nullptr
 void* mapped_address(const void* p, size_t bytes);
@@ -208,6 +233,18 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
                : "l"(p)
                : "memory");
   return r;
+}
+
+// 32 bytes at an address that is a multiple of 32
+__device__ __forceinline__ void ld32(const void* p, uint4& x, uint4& y) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w), "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+               : "l"(p));
+}
+__device__ __forceinline__ void st32(void* p, const uint4& x, const uint4& y) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w),
+               "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+               : "memory");
 }
 
 }  // namespace scout

@@ -8,7 +8,7 @@
 // W and X tiles (64 k-columns, 128-byte swizzle) stream in by TMA through a ring of
 // shared-memory stages guarded by mbarriers, up to four k-blocks per stage (measured on
 // GB300: one k-block per stage streams ~25% slower, the barrier round trip of a stage
-// being paid per 22 KB instead of per 67 to 88 KB); one thread issues tcgen05.mma into a
+// being paid per 22 KB instead of per 88 KB); one thread issues tcgen05.mma into a
 // TMEM accumulator and frees each stage with tcgen05.commit.  The K dimension is
 // split over the CTAs of a thread-block cluster so that about one CTA runs per SM.
 // The batch columns of the accumulator are dealt out over the cluster's CTAs: each
@@ -20,7 +20,8 @@
 // scout_predict_q_rotated is the same kernel with another last step: a tile is one head, so a
 // CTA holds whole heads of its batch columns.  The sums go to shared memory in fp32, eight lanes
 // take a head (rotate.cuh), normalise and turn it, and store it rounded once, 16 bytes a lane.
-// The cosines and sines are made while W streams in.
+// The cosines and sines are made while W streams in.  GB300: 15.8 us for 40 x 5120 x 5120, 11.9 us for 8 x 4096 x 4096 in a
+// row of calls (3.4 and 2.8 TB/s of W: ~1.5 us to the first tile, the stream, ~1 us of exchange and 1.3 us of last step).
 
 #include "rotate.cuh"
 
@@ -67,13 +68,14 @@ struct GemmArgs {
   __nv_bfloat16* Q;
   int M, N, n_pad, tmem_cols, kblocks, stages, x_tile_bytes;
   int kps;     // k-blocks per ring stage
-  int recv_at; // bytes from the ring's start to what peers write: past the ring, or 0 where it does not fit beside it
+  int recv_at; // bytes from the ring's start to what peers write: past the ring, or 0 (in it, once it is idle)
   int32_t* status;
   // of the rotated form
   const int32_t* positions;
   const __nv_bfloat16* norm;
   Rope rope;
   float eps;
+  bool early;  // W may be read before the kernel before this one has finished
 };
 
 constexpr int kPlain = -1;  // no rotary layout: the sums are the result
@@ -124,6 +126,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) predict_q_kernel(const __grid_co
     fence_mbar_init();
     prefetch_tmap(&tmW);
     prefetch_tmap(&tmX);
+    if (LAYOUT != kPlain && !a.early) wait_prerequisites();
     for (int i = 0; i < first; ++i)
       load_w(base + i * stage_bytes, &tmW, a, tile, kb0 + i * a.kps, nk_of(i), &full_bar[i]);
     wait_prerequisites();
@@ -145,7 +148,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1) predict_q_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  if (S > 1) cluster_arrive();  // this CTA runs: its shared memory may be written
+  const bool apart = LAYOUT != kPlain && a.recv_at > 0;
+  if (apart) cluster_arrive();  // this CTA runs: its shared memory may be written
 
   if (warp == 0 && lane == 0) {
     // TMA producer: the rest of the k range, each stage once the MMAs have freed it
@@ -204,8 +208,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1) predict_q_kernel(const __grid_co
   float* mine = recv + (int)rank * owned * 8 * kBM;  // this CTA's own slots: no peer writes them
   float v[8];
   if (S > 1) {
-    cluster_wait();
-    if (a.recv_at == 0) cluster_sync();  // every CTA of the cluster is done with its ring: it may be written
+    if (apart) cluster_wait();
+    else cluster_sync();  // every CTA of the cluster is done with its ring: it may be written
     for (int g = 0; g < ngroups; ++g) {
       const uint32_t owner = (uint32_t)g % S;
       if (owner == rank) continue;
@@ -307,19 +311,22 @@ int predict(const void* X, const void* W, void* Q, int M, int N, int K, const in
     a.norm = static_cast<const __nv_bfloat16*>(norm);
     a.rope = rope_of(rope);
     a.eps = eps;
+    a.early = launch != nullptr && launch->pdl;
   }
   const int tiles = N / kBM;
   const int cap = launch != nullptr && launch->max_ctas > 0 ? launch->max_ctas : sm_count();
   const int S = max(1, min(min(8, a.kblocks), cap / tiles));  // split-K so tiles x S fits the CTA budget
   const int owned = (a.n_pad / 8 + S - 1) / S;                  // column groups per CTA in the reduction
-  // ~200 KB in flight per SM, in stages of up to kMaxKps k-blocks (the fewer the stages, the fewer barrier round
-  // trips per byte): three of them where they hold two k-blocks each (GB300, 40 x 5120 x 5120: 14.7 us, 14.9 with two
-  // stages of four, 15.7 with five of two), otherwise at least two, so that copies and MMAs overlap.  What the cluster's
-  // CTAs exchange lies beside the ring where it is small: a CTA then sends without waiting for its peers' rings (16.8 -> 15.5
-  // us of the rotated form).
+  // ~180 to 220 KB in flight per SM, in stages of up to kMaxKps k-blocks (the fewer the stages, the fewer
+  // barrier round trips per byte) but at least two, so that copies and MMAs overlap.  The rotated form keeps what the
+  // cluster's CTAs exchange beside the ring, where it is small, so that a CTA sends without waiting for its peers' rings, and
+  // takes three stages where they hold two k-blocks each.  Alone that is faster (GB300, 40 x 5120 x 5120: 16.8 -> 15.3 us,
+  // without turns 14.7, of which the stages 0.2), but not beside the other kernels of a decode step (57.0 us a step
+  // against 56.9, 57.4 with the stages), which calls the plain form.
   const int exchange = S * owned * 8 * kBM * 4, tile_bytes = kWTileBytes + a.x_tile_bytes;
-  const int room = kRingBytes - (S > 1 && exchange <= kApartBytes ? exchange : 0);
-  a.kps = room / 3 / tile_bytes >= 2 ? min(kMaxKps, room / 3 / tile_bytes) : max(1, min(kMaxKps, room / 2 / tile_bytes));
+  const int room = kRingBytes - (LAYOUT != kPlain && S > 1 && exchange <= kApartBytes ? exchange : 0);
+  a.kps = max(1, min(kMaxKps, room / 2 / tile_bytes));
+  if (LAYOUT != kPlain && room / 3 / tile_bytes >= 2) a.kps = min(kMaxKps, room / 3 / tile_bytes);
   const int stage_bytes = a.kps * tile_bytes;
   a.stages = min(kStages, room / stage_bytes);
   const int ring = a.stages * stage_bytes;
@@ -345,6 +352,11 @@ int predict(const void* X, const void* W, void* Q, int M, int N, int K, const in
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = early_start_attrs(launch, attr, 1);
+  if (LAYOUT != kPlain && !a.early) {  // scheduled, and set up, while the kernel before it ends
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
   if (cudaLaunchKernelEx(&cfg, predict_q_kernel<LAYOUT>, tmW, tmX, a) != cudaSuccess) return SCOUT_ERR_CUDA;
   return launch_status();
 }

@@ -46,22 +46,11 @@ __device__ __forceinline__ uint4 widen8(const uint2& c, float scale) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// 32 bytes at an address that is a multiple of 32
-__device__ __forceinline__ void ld32(const void* p, uint4& x, uint4& y) {
-  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w), "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
-               : "l"(p));
-}
-__device__ __forceinline__ void st32(void* p, const uint4& x, const uint4& y) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w),
-               "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
-               : "memory");
-}
-
 // R: rows of a warp's item.
 template <int P, int F, int R>
 __global__ void __launch_bounds__(kReadWarps * 32) read_kernel(const ReadArgs a) {
   constexpr int kParts = P / R;  // items of a block's K or V
+  start_dependent();
   const int lane = threadIdx.x & 31, quad = lane >> 3, sub = lane & 7;
   const int64_t w = (int64_t)blockIdx.x * kReadWarps + (threadIdx.x >> 5);
   if (w >= 2 * kParts * a.n_items) return;
@@ -125,8 +114,7 @@ __global__ void __launch_bounds__(kReadWarps * 32) read_kernel(const ReadArgs a)
 template <int P, int F, int R>
 int launch_read(const ReadArgs& a, cudaStream_t st) {
   const int64_t grid = (2 * (P / R) * a.n_items + kReadWarps - 1) / kReadWarps;  // at most twice kMaxItems
-  read_kernel<P, F, R><<<(unsigned)grid, kReadWarps * 32, 0, st>>>(a);
-  return launch_status();
+  return launch_dependent(read_kernel<P, F, R>, grid, kReadWarps * 32, 0, st, a);
 }
 
 template <int P, int F>

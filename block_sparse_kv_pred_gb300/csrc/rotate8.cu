@@ -228,6 +228,7 @@ __device__ __forceinline__ void prefixes(const Rot8Args& a, int* tok, int* tou, 
 template <int P, int F, int LAYOUT>
 __global__ void __launch_bounds__(kR8Warps * 32, kR8PerSm) rotate8_kernel(const Rot8Args a) {
   constexpr int H = P / 4 < kHold ? P / 4 : kHold, kSet = P / 4 / H;  // warps of one head's K or V
+  start_dependent();
   extern __shared__ int sm[];
   __shared__ int partial[2 * 32];
   __shared__ uint32_t top[2 * kR8Warps];
@@ -322,6 +323,7 @@ __global__ void __launch_bounds__(kR8Warps * 32, kR8PerSm) rotate8_kernel(const 
 
 template <int P, int F, int LAYOUT>
 __global__ void __launch_bounds__(kR8Warps * 32, 4) rotate8_few_kernel(const Rot8Args a) {
+  start_dependent();
   extern __shared__ int sm[];
   __shared__ int partial[2 * 32];
   int *tok = sm, *tou = sm + (a.B + 1);
@@ -388,8 +390,7 @@ int launch_rotate8(Rot8Args& a, cudaStream_t st) {
   if (a.n_tokens <= kFewTokens * (int64_t)a.B) {
     const int64_t want = (blocks * 2 * a.Hkv + groups * a.Hq + kR8Warps - 1) / kR8Warps + none;
     const int64_t most = (int64_t)sm_count() * 8;
-    rotate8_few_kernel<P, F, LAYOUT><<<(int)(want < most ? want : most), kR8Warps * 32, smem, st>>>(a);
-    return launch_status();
+    return launch_dependent(rotate8_few_kernel<P, F, LAYOUT>, want < most ? want : most, kR8Warps * 32, smem, st, a);
   }
   if (smem + kStatic8 + kTable8 * P > 48 * 1024 &&
       cudaFuncSetAttribute(rotate8_kernel<P, F, LAYOUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -406,8 +407,7 @@ int launch_rotate8(Rot8Args& a, cudaStream_t st) {
   a.q_parts = (a.Hq + a.q_per - 1) / a.q_per;
   const int64_t q_want = (groups * a.q_parts + kR8Warps - 1) / kR8Warps, q_most = max((int64_t)1, most - kv_most) * kR8Waves;
   const int grid = a.kv_ctas + (int)(q_want < q_most ? q_want : q_most);
-  rotate8_kernel<P, F, LAYOUT><<<grid, kR8Warps * 32, smem, st>>>(a);
-  return launch_status();
+  return launch_dependent(rotate8_kernel<P, F, LAYOUT>, grid, kR8Warps * 32, smem, st, a);
 }
 
 template <int P, int F>
