@@ -129,7 +129,7 @@ int check_heads(const void* x, int64_t ld_x, const void* out, int64_t ld_out, in
   if (x == nullptr || out == nullptr || heads <= 0 || !valid_rope(rope) || !valid_eps(eps) ||
       ld_x < (int64_t)heads * D || ld_out < (int64_t)heads * D)
     return SCOUT_ERR_INVALID_ARG;
-  if (D != kD || !supported_rope(rope) || ld_x % 8 != 0 || ld_out % 8 != 0 || !aligned16(x) || !aligned16(out) ||
+  if (D != kD || heads > (1 << 20) || !supported_rope(rope) || ld_x % 8 != 0 || ld_out % 8 != 0 || !aligned16(x) || !aligned16(out) ||
       !aligned16(norm))
     return SCOUT_ERR_UNSUPPORTED;
   return SCOUT_OK;

@@ -81,7 +81,7 @@ typedef enum scout_digest_kind {
  * scout_predict_q it bounds the split-K factor S so that
  * (N / 128) * S <= max_ctas; the grid keeps at least one CTA per 128-row tile of W.
  *
- * Early starts (programmatic dependent launch), for scout_predict_q,
+ * Early starts (programmatic dependent launch), for scout_predict_q(_rotated),
  * scout_score_topk and scout_sparse_attn(_merge), and scout_sparse_attn8(_merge), which does as
  * scout_sparse_attn does.  Each of these kernels may start
  * before the kernel it depends on has finished, do the part of its work that does
@@ -103,7 +103,10 @@ typedef enum scout_digest_kind {
  *                    starts early as above.  Anything else that waits for the event
  *                    (a copy, a host wait, another library's kernel) is NOT ordered
  *                    after the primary's writes: record a plain event after the call
- *                    for those.  NULL: no programmatic event. */
+ *                    for those.  NULL: no programmatic event.
+ * scout_rotate, scout_append_rotated_kv(8), scout_add_norm, scout_read_kv(8) and, without pdl, scout_predict_q_rotated
+ * take no part in this: they are always scheduled while the kernel before them on the stream ends, and wait for it
+ * before they read or write anything.  The last of them streams W before that wait with pdl = 1. */
 typedef struct scout_launch {
   int max_ctas;
   int pdl;
@@ -469,8 +472,8 @@ int scout_rope_turns(double base, int rot_dim, const scout_rope_scaling* scaling
  * positions  int32 [n_tokens]; a negative one marks a padding row, which is neither read nor written
  * norm       bf16 [D], or NULL for no norm: the head is first divided by its root mean square,
  *            x * (sum x^2 / D + eps)^(-1/2) * norm
- * In fp32, rounded to bf16 once.  Requires ld >= heads * D, ld % 8 == 0, eps >= 0 and finite, and 16-byte aligned
- * tensors (positions 4-byte). */
+ * In fp32, rounded to bf16 once.  Requires ld >= heads * D, ld % 8 == 0, at most 2^20 heads (here and in the calls
+ * below), eps >= 0 and finite, and 16-byte aligned tensors (positions 4-byte). */
 int scout_rotate(const void* x, int64_t ld_x, void* out, int64_t ld_out, const int32_t* positions, int n_tokens,
                  int heads, int D, const scout_rope* rope, const void* norm, float eps, cudaStream_t stream);
 

@@ -363,6 +363,47 @@ def test_append8_token_by_token_is_append8_at_once_where_scales_agree(P):
         assert same(a, b)
 
 
+def check_write8(rng, w, fmt, rope, **kw):
+    """append_rotated_kv8 against rotate and append_kv8, bit for bit."""
+    K, V = pools8(rng, w, fmt), pools8(rng, w, fmt)
+    one = [K[0], V[0], K[1], V[1]]
+    two = [t.clone() for t in one]
+    st = word()
+    q = bs.append_rotated_kv8(w.K, w.V, rope, w.table, w.seq_t, w.B, w.Hkv, w.P, *one, prev_len=w.prev_t, k_norm=w.kw, q=w.q,
+                              q_norm=w.qw if w.Hq else None, status=st, **kw)
+    bs.append_kv8(w.turned(rope, w.K, w.kw), w.V.contiguous(), w.table, w.seq_t, w.B, w.Hkv, w.P, *two, prev_len=w.prev_t)
+    for a, b in zip(one, two):
+        assert same(a, b)
+    assert int(st) == 0 and (q is None or same(q, w.turned(rope, w.q, w.qw)))
+
+
+@pytest.mark.parametrize("P", [16, 32, 64])
+@pytest.mark.parametrize("new", [1, 3, 4, 5, 15, 16, 17, 31, 40])
+def test_append8_around_the_number_of_tokens_that_chooses_the_kernel(P, new):
+    rng = np.random.default_rng(P + new)
+    prev = [0, P - 1, 2 * P + 3, 7]
+    check_write8(rng, Write(rng, prev, [p + new for p in prev], 3, 5, P), "e4m3", bs.rope(1e4, 96))
+
+
+@pytest.mark.parametrize("P,Hkv,Hq,seq", [
+    (16, 2, 1, [30011, 9, 20000]), (32, 1, 0, [70000]), (64, 3, 17, [9000, 1, 63, 64, 65]), (16, 40, 40, [700, 100]),
+    (64, 1, 33, [40000, 3]), (32, 11, 2, [1000] * 3)])
+def test_append8_prompts_over_the_whole_grid(P, Hkv, Hq, seq):
+    rng = np.random.default_rng(P + Hkv)
+    check_write8(rng, Write(rng, [0] * len(seq), seq, Hkv, Hq, P), "e5m2", bs.rope(1e6, 128))
+
+
+@pytest.mark.parametrize("B,P", [(1500, 64), (4096, 32)])
+def test_append8_prompts_of_many_sequences(B, P):
+    """More shared memory than needs no request: the prefixes of a large batch beside a block's cosines."""
+    rng = np.random.default_rng(B)
+    seq = rng.integers(0, 40, B)
+    prev = np.minimum(seq, rng.integers(0, 3, B))
+    w = Write(rng, prev.tolist(), seq.tolist(), 1, 1, P)
+    assert w.n > 16 * B
+    check_write8(rng, w, "e4m3", bs.rope(1e4, 128, layout="interleaved"))
+
+
 def test_append8_values_that_are_not_finite():
     rng = np.random.default_rng(4)
     w = Write(rng, [3, 0], [60, 20], 3, 0, 32)

@@ -134,7 +134,8 @@ ROPES = [(dict(rope=None), INVALID), (dict(rope=rope(0)), INVALID), (dict(rope=r
     ({}, OK), (dict(x=None), INVALID), (dict(out=None), INVALID), (dict(pos=None), INVALID), (dict(n=-1), INVALID),
     (dict(heads=0), INVALID), (dict(ld_x=248), INVALID), (dict(ld_o=128), INVALID), (dict(ld_x=260), UNSUPPORTED),
     (dict(ld_o=260), UNSUPPORTED), (dict(D=64), UNSUPPORTED), (dict(x=ODD), UNSUPPORTED), (dict(out=ODD), UNSUPPORTED),
-    (dict(norm=ODD), UNSUPPORTED), (dict(pos=ctypes.c_void_p(4098)), UNSUPPORTED)])
+    (dict(norm=ODD), UNSUPPORTED), (dict(pos=ctypes.c_void_p(4098)), UNSUPPORTED),
+    (dict(heads=(1 << 20) + 1, ld_x=1 << 28, ld_o=1 << 28), UNSUPPORTED)])
 def test_rotate_refusals(L, change, rc):
     assert call(L.scout_rotate, ROTATE, **change) == rc
 
