@@ -20,8 +20,9 @@
 // scout_predict_q_rotated is the same kernel with another last step: a tile is one head, so a
 // CTA holds whole heads of its batch columns.  The sums go to shared memory in fp32, eight lanes
 // take a head (rotate.cuh), normalise and turn it, and store it rounded once, 16 bytes a lane.
-// The cosines and sines are made while W streams in.  GB300: 15.8 us for 40 x 5120 x 5120, 11.9 us for 8 x 4096 x 4096 in a
-// row of calls (3.4 and 2.8 TB/s of W: ~1.5 us to the first tile, the stream, ~1 us of exchange and 1.3 us of last step).
+// The cosines and sines are made, and the norm's weights read, while W streams in (read in the last step, the weights
+// alone cost 1.3 us).  GB300: 14.0 us for 40 x 5120 x 5120 and 10.7 us for 8 x 4096 x 4096 (3.8 and 3.2 TB/s of W: the
+// launch, ~1.8 us to the first product, the stream at about 6 TB/s, 1.3 and 1.1 us of exchange, 1.2 and 0.6 of last step).
 
 #include "rotate.cuh"
 
@@ -138,10 +139,12 @@ __global__ void __launch_bounds__(kThreadsQ, 1) predict_q_kernel(const __grid_co
   auto m_of = [&](int k) { return ((int)rank + (k >> 3) * (int)S) * 8 + (k & 7); };
   int pos = -1;  // and turn: of the lane's column among the CTA's first 16
   Turn turn;
+  Weights w;
   if constexpr (LAYOUT != kPlain) {
     wait_prerequisites();  // the positions may be an earlier kernel's, as X
     const int m = m_of(warp * 4 + (lane >> 3));
     pos = m < a.M ? a.positions[m] : -1;
+    if (a.norm != nullptr) w = lane_weights(a.norm, lane_chunks<LAYOUT>(sub, a.rope.n));
     turn = lane_turn(a.rope, sub, (uint32_t)max(pos, 0));
   }
   tc_fence_before();
@@ -243,8 +246,6 @@ __global__ void __launch_bounds__(kThreadsQ, 1) predict_q_kernel(const __grid_co
   if constexpr (LAYOUT != kPlain) {
     __syncthreads();
     const int2 at = lane_chunks<LAYOUT>(sub, a.rope.n);
-    Weights w;
-    if (a.norm != nullptr) w = lane_weights(a.norm, at);
     const int columns = (ngroups - (int)rank + (int)S - 1) / (int)S * 8;  // of this CTA
     for (int k0 = 0; k0 < columns; k0 += 16) {
       const int k = k0 + warp * 4 + (lane >> 3);
@@ -320,9 +321,9 @@ int predict(const void* X, const void* W, void* Q, int M, int N, int K, const in
   // ~180 to 220 KB in flight per SM, in stages of up to kMaxKps k-blocks (the fewer the stages, the fewer
   // barrier round trips per byte) but at least two, so that copies and MMAs overlap.  The rotated form keeps what the
   // cluster's CTAs exchange beside the ring, where it is small, so that a CTA sends without waiting for its peers' rings, and
-  // takes three stages where they hold two k-blocks each.  Alone that is faster (GB300, 40 x 5120 x 5120: 16.8 -> 15.3 us,
-  // without turns 14.7, of which the stages 0.2), but not beside the other kernels of a decode step (57.0 us a step
-  // against 56.9, 57.4 with the stages), which calls the plain form.
+  // takes three stages where they hold two k-blocks each.  Alone that is faster (GB300, 40 x 5120 x 5120:
+  // 1.5 us, of which the stages 0.2), but not beside the other kernels of a decode step (57.0 us a step against 56.9,
+  // 57.4 with the stages), which calls the plain form.
   const int exchange = S * owned * 8 * kBM * 4, tile_bytes = kWTileBytes + a.x_tile_bytes;
   const int room = kRingBytes - (LAYOUT != kPlain && S > 1 && exchange <= kApartBytes ? exchange : 0);
   a.kps = max(1, min(kMaxKps, room / 2 / tile_bytes));

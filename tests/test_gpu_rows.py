@@ -489,6 +489,49 @@ def test_append8_of_the_largest_batch():
     assert same(q_out[:w.n], w.turned(rope, w.q, None)[:w.n]) and torch.all(q_out[w.n:] == 3.0)
 
 
+def at_16(t):
+    """The same values at an address that is a multiple of 16, but not of 32."""
+    buf = torch.empty(t.numel() * t.element_size() + 64, dtype=torch.uint8, device="cuda")
+    start = 16 - buf.data_ptr() % 32
+    view = buf[start + (32 if start < 0 else 0):][: t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+    assert view.data_ptr() % 32 == 16
+    return view.copy_(t)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_rows_and_pools_at_16_byte_boundaries(new):
+    rng = np.random.default_rng(new)
+    w = Write(rng, [5, 33], [5 + new, 33 + new], 3, 5, 32, pad=8)
+    rope = bs.rope(1e4, 128)
+    for n in ("K", "V", "q"):
+        x = getattr(w, n)
+        row = at_16(torch.zeros((x.shape[0], x.shape[1] * D + 8), dtype=torch.bfloat16, device="cuda"))
+        view = row[:, :x.shape[1] * D].unflatten(1, (x.shape[1], D))
+        setattr(w, n, view.copy_(x))
+    kw, qw = at_16(w.kw), at_16(w.qw)
+    want_k, want_q = w.turned(rope, w.K, w.kw), w.turned(rope, w.q, w.qw)
+    one = [at_16(bf16(rng, w.n_slots, 32, D)) for _ in "KV"]
+    two = [t.clone() for t in one]
+    q = bs.append_rotated_kv(w.K, w.V, i32(w.pos), rope, w.slot_map, 3, 32, *one, k_norm=kw, q=w.q, q_norm=qw)
+    bs.append_kv(want_k, w.V, w.slot_map, 3, 32, *two)
+    assert same(one[0], two[0]) and same(one[1], two[1]) and same(q, want_q)
+    K, V = pools8(rng, w, "e4m3"), pools8(rng, w, "e4m3")
+    one = [at_16(K[0].view(torch.uint8)).view(DT["e4m3"]), at_16(V[0].view(torch.uint8)).view(DT["e4m3"]), K[1], V[1]]
+    two = [t.clone() for t in one]
+    q = bs.append_rotated_kv8(w.K, w.V, rope, w.table, w.seq_t, 2, 3, 32, *one, prev_len=w.prev_t, k_norm=kw, q=w.q, q_norm=qw)
+    bs.append_kv8(want_k, w.V, w.table, w.seq_t, 2, 3, 32, *two, prev_len=w.prev_t)
+    assert all(same(a, b) for a, b in zip(one, two)) and same(q, want_q)
+    out = [[torch.zeros((2, 3, w.cap * 32, D), dtype=torch.bfloat16, device="cuda") for _ in "KV"] for _ in range(2)]
+    for pools, o in zip((one, two), out):  # an 8-bit pool at 16 bytes is read; a bf16 one, or an output, is not
+        bs.read_kv8(*pools, w.table, w.seq_t, 2, 3, 32, *o)
+    assert same(out[0][0], out[1][0]) and same(out[0][1], out[1][1])
+    with pytest.raises(bs.ScoutError, match="UNSUPPORTED"):
+        bs.read_kv8(*one, w.table, w.seq_t, 2, 3, 32, at_16(out[0][0]), at_16(out[0][1]))
+    pool = at_16(bf16(rng, w.n_slots, 32, D))
+    with pytest.raises(bs.ScoutError, match="UNSUPPORTED"):
+        bs.read_kv(pool, pool, w.table, w.seq_t, 2, 3, 32, *out[0])
+
+
 # ---------------------------------------------------------------------------
 # predict_q_rotated
 # ---------------------------------------------------------------------------
