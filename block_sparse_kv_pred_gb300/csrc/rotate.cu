@@ -5,7 +5,7 @@
 // Its rows' cosines are made once, in registers, while the first heads' rows are on their way; four heads are in flight
 // together.  Bound by DRAM: GB300, 8 prompts of up to 16K tokens, 8 KV and 32 query heads, 266 us for 1.72 GB (6.45 TB/s, 0.96 of the
 // measured copy bandwidth) at 20 warps an SM and half of its issue slots; two heads in flight 282 us, eight 336 (registers); the
-// next heads read before the present ones are turned 280.  A decode step of 40 sequences 2.6 us, 8 x 32 heads 2.05 us:
+// next heads read before the present ones are turned 280.  A decode step of 40 sequences 2.2 us, 8 x 32 heads 1.75 us:
 // the launch and one read.
 #include "rotate.cuh"
 
@@ -55,29 +55,34 @@ __global__ void __launch_bounds__(kRotThreads, 5) rotate_kernel(const RotArgs a)
   const int h0 = part * a.per, h1 = min(r.heads, h0 + a.per);
   const int2 at = is_v ? make_int2(sub * 8, 64 + sub * 8) : lane_chunks<LAYOUT>(sub, a.rope.n);
   const __nv_bfloat16* src = r.src + i * r.ld;
+  const bool norm = r.norm != nullptr;
   Turn t;
   Weights w;
-  const bool norm = r.norm != nullptr;
-  if (!is_v) {
-    t = lane_turn(a.rope, sub, (uint32_t)max(pos, 0));
+  auto prepare = [&] {
+    if (is_v) return;
     if (norm) w = lane_weights(r.norm, at);
-  }
+    t = lane_turn(a.rope, sub, (uint32_t)max(pos, 0));
+  };
+  // One head a warp: its loads go out before the position is there (8 x 32 heads 2.05 -> 1.75 us, a decode step's write 2.65 ->
+  // 2.2; with more heads, whose loads then hold registers meanwhile, 266 -> 269 us).
+  if (U > 1) prepare();
   for (int h = h0; h < h1; h += U) {
     uint4 x[U], y[U];
     int64_t to[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       to[u] = -1;
-      if (pos < 0 || h + u >= h1) continue;
+      if ((U > 1 ? pos < 0 : i >= a.n_tokens) || h + u >= h1) continue;
       to[u] = is_q ? i * r.ld_dst + (h + u) * kD : a.slot_map[i * r.heads + h + u];
       x[u] = ld_stream(src + (h + u) * kD + at.x);
       y[u] = ld_stream(src + (h + u) * kD + at.y);
     }
+    if (U == 1) prepare();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (!is_q) {
         if (to[u] >= a.pool_rows) {
-          if (sub == 0) report(a.status, SCOUT_DEV_BAD_INDEX);
+          if (sub == 0 && pos >= 0) report(a.status, SCOUT_DEV_BAD_INDEX);
           to[u] = -1;
         }
         if (to[u] >= 0) to[u] *= kD;
@@ -89,7 +94,7 @@ __global__ void __launch_bounds__(kRotThreads, 5) rotate_kernel(const RotArgs a)
         turn_head<LAYOUT>(v, t, sub < a.rope.n);
         pack16(v, x[u], y[u]);
       }
-      if (to[u] < 0) continue;
+      if (to[u] < 0 || pos < 0) continue;
       *reinterpret_cast<uint4*>(r.dst + to[u] + at.x) = x[u];
       *reinterpret_cast<uint4*>(r.dst + to[u] + at.y) = y[u];
     }

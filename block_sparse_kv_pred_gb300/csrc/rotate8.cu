@@ -181,14 +181,18 @@ __device__ __forceinline__ void turn_queries(const Rot8Args& a, const int* tok, 
   const int2 at = lane_chunks<LAYOUT>(sub, a.rope.n);
   const __nv_bfloat16* src = a.q + i * a.ld_q;
   __nv_bfloat16* dst = a.q_out + i * a.ld_q_out;
-  int index = 0;
-  if (a.positions == nullptr && live) {
-    const int b = owner_of(tok, a.B, (int)i);
-    index = seq_span(a.prev_len, a.seq_len, b, cap_tokens).prev + (int)i - tok[b];
-  }
-  const Turn t = lane_turn(a.rope, sub, position_of(a, i, index, live, sub));
+  Turn t;
   Weights w;
-  if (a.q_norm != nullptr) w = lane_weights(a.q_norm, at);
+  auto prepare = [&] {
+    int index = 0;
+    if (a.positions == nullptr && live) {
+      const int b = owner_of(tok, a.B, (int)i);
+      index = seq_span(a.prev_len, a.seq_len, b, cap_tokens).prev + (int)i - tok[b];
+    }
+    if (a.q_norm != nullptr) w = lane_weights(a.q_norm, at);
+    t = lane_turn(a.rope, sub, position_of(a, i, index, live, sub));
+  };
+  if (U > 1) prepare();  // (one head: its loads first)
   for (int h = h0; h < h1; h += U) {
     uint4 x[U], y[U];
 #pragma unroll
@@ -197,6 +201,7 @@ __device__ __forceinline__ void turn_queries(const Rot8Args& a, const int* tok, 
       x[u] = ld_stream(src + (h + u) * kD + at.x);
       y[u] = ld_stream(src + (h + u) * kD + at.y);
     }
+    if (U == 1) prepare();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float v[16];

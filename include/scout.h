@@ -469,7 +469,7 @@ int scout_rope_turns(double base, int rot_dim, const scout_rope_scaling* scaling
 /* Heads normalised and turned.
  * x, out     bf16: head (i, h) of D values at i * ld_x (ld_out) + h * D elements; out may be x itself, with the
  *            same stride (no other overlap)
- * positions  int32 [n_tokens]; a negative one marks a padding row, which is neither read nor written
+ * positions  int32 [n_tokens]; a negative one marks a padding row, of which nothing is written
  * norm       bf16 [D], or NULL for no norm: the head is first divided by its root mean square,
  *            x * (sum x^2 / D + eps)^(-1/2) * norm
  * In fp32, rounded to bf16 once.  Requires ld >= heads * D, ld % 8 == 0, at most 2^20 heads (here and in the calls
@@ -480,7 +480,7 @@ int scout_rotate(const void* x, int64_t ld_x, void* out, int64_t ld_out, const i
 /* scout_append_kv with the keys normalised and turned on their way into the cache, and the same tokens' queries
  * beside them (scout_rotate from q to q_out), in one launch.
  * K_new, V_new, slot_map, K_pool, V_pool, dev_status: as scout_append_kv.  positions int32 [n_tokens]: a
- * negative one marks a padding row (nothing of it is read or written, whatever its slots).
+ * negative one marks a padding row (nothing of it is written, whatever its slots).
  * k_norm, q_norm bf16 [D] or NULL; Hq 0 (q and q_out then unused) or the query heads.  q_out may be q. */
 int scout_append_rotated_kv(const void* K_new, int64_t ld_k, const void* V_new, int64_t ld_v,
                             const int32_t* positions, const scout_rope* rope, const void* k_norm, float eps,
