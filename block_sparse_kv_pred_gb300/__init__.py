@@ -501,7 +501,7 @@ def rotate(x, positions, rope, norm=None, eps=1e-6, out=None, stream=None):
     """Heads of bf16 rows x [n_tokens][heads][D] (token strides free), normalised by ``norm`` (bf16 [D], None: not)
     and turned by ``positions`` int32 [n_tokens] -> out, bf16, alike (x itself for in place).  Rows with a
     negative position are left alone."""
-    return _native().rotate(x, positions, *rope._args, norm, eps, out, stream)
+    return _native().rotate(x, positions, rope._args, norm, eps, out, stream)
 
 
 def append_rotated_kv(K_new, V_new, positions, rope, slot_map, Hkv, P, K_pool, V_pool, k_norm=None, q=None, q_norm=None,
@@ -509,7 +509,7 @@ def append_rotated_kv(K_new, V_new, positions, rope, slot_map, Hkv, P, K_pool, V
     """append_kv with the keys normalised (``k_norm``) and turned by ``positions`` int32 [n_tokens] on their way, and
     the same tokens' queries ``q`` [n_tokens][Hq][D] beside them (``q_norm``) into ``q_out`` (q itself for in
     place, None: a new tensor) -> q_out, or None without q.  Rows with a negative position are left alone."""
-    return _native().append_rotated_kv(K_pool, V_pool, Hkv, P, K_new, V_new, positions, *rope._args, k_norm, eps, slot_map,
+    return _native().append_rotated_kv(K_pool, V_pool, Hkv, P, K_new, V_new, positions, rope._args, k_norm, eps, slot_map,
                                        q, q_norm, q_out, status, stream)
 
 
@@ -518,14 +518,14 @@ def append_rotated_kv8(K_new, V_new, rope, page_table, seq_len, B, Hkv, P, K_poo
     """append_kv8 with the keys normalised, turned and rounded to bf16 first, and the same tokens' queries beside
     them, as append_rotated_kv -> q_out, or None without q.  ``positions``: by default each token's index in its
     sequence.  Rows past the last new token are left alone, in q_out too."""
-    return _native().append_rotated_kv8(K_pool, V_pool, B, Hkv, P, K_new, V_new, *rope._args, k_norm, eps, page_table,
+    return _native().append_rotated_kv8(K_pool, V_pool, B, Hkv, P, K_new, V_new, rope._args, k_norm, eps, page_table,
                                         seq_len, K_scale, V_scale, prev_len, positions, q, q_norm, q_out, status, stream)
 
 
 def predict_q_rotated(X, W, positions, rope, norm=None, eps=1e-6, Q=None, status=None, max_ctas=None, stream=None):
     """predict_q with the heads of X W^T normalised (``norm`` bf16 [128], None: not) and turned by ``positions`` int32
     [M] before they are rounded -> Q bf16 [M][N].  Rows with a negative position are not written."""
-    return _native().predict_q_rotated(X, W, positions, *rope._args, norm, eps, Q, status, max_ctas, stream)
+    return _native().predict_q_rotated(X, W, positions, rope._args, norm, eps, Q, status, max_ctas, stream)
 
 
 def read_kv(K_pool, V_pool, page_table, seq_len, B, Hkv, P, K_out, V_out, block_list=None, status=None, stream=None):

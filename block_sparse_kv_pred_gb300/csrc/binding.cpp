@@ -70,8 +70,10 @@ class Args {
 
   // a tensor of any size; its device is looked at in settle()
   const at::Tensor* tensor(const char* name) {
+    return ok_ ? tensor(*at_++, name) : nullptr;
+  }
+  const at::Tensor* tensor(PyObject* o, const char* name) {
     if (!ok_) return nullptr;
-    PyObject* o = *at_++;
     if (!THPVariable_Check(o)) {
       fail("%s must be a CUDA tensor, got %s", name, Py_TYPE(o)->tp_name);
       return nullptr;
@@ -465,13 +467,23 @@ PyObject* sparse_attn8(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// turns, rot_dim, layout, amplitude
+// One argument, a tuple (turns, rot_dim, layout, amplitude): a call with star arguments costs Python more.
 scout_rope rope_of(Args& a) {
   scout_rope r = {};
-  const at::Tensor* t = a.tensor("rope.turns");
-  r.rot_dim = a.i32();
-  r.layout = a.i32();
-  r.amplitude = (float)a.real();
+  PyObject* o = a.raw();
+  if (!a.ok()) return r;
+  if (!PyTuple_CheckExact(o) || PyTuple_GET_SIZE(o) != 4) {
+    a.fail("rope must be a Rope, got %s", Py_TYPE(o)->tp_name);
+    return r;
+  }
+  const at::Tensor* t = a.tensor(PyTuple_GET_ITEM(o, 0), "rope.turns");
+  r.rot_dim = (int)PyLong_AsLong(PyTuple_GET_ITEM(o, 1));
+  r.layout = (int)PyLong_AsLong(PyTuple_GET_ITEM(o, 2));
+  r.amplitude = (float)PyFloat_AsDouble(PyTuple_GET_ITEM(o, 3));
+  if (a.ok() && PyErr_Occurred()) {
+    PyErr_Clear();
+    a.fail("rope must be a Rope: a number was expected");
+  }
   r.turns = static_cast<const uint64_t*>(a.sized(t, "rope.turns", at::kLong, r.rot_dim / 2));
   return r;
 }
@@ -484,10 +496,10 @@ at::Tensor make(const at::Tensor* like, at::IntArrayRef sizes, at::ScalarType ty
   return at::empty(sizes, at::TensorOptions().device(like->device()).dtype(type));
 }
 
-// (x, positions, turns, rot_dim, layout, amplitude, norm | None, eps, out | None, stream | None) -> out
+// (x, positions, rope, norm | None, eps, out | None, stream | None) -> out
 PyObject* rotate(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    Args a(args, n, 10);
+    Args a(args, n, 7);
     const at::Tensor* x = a.tensor("x");
     int64_t rows = 0, D = 0, ld_x = 0, rows_o = 0, D_o = 0, ld_o = 0;
     int heads = 0, heads_o = 0;
@@ -554,11 +566,10 @@ struct Queries {
   }
 };
 
-// (K_pool, V_pool, Hkv, P, K_new, V_new, positions, turns, rot_dim, layout, amplitude, k_norm | None, eps, slot_map,
-//  q | None, q_norm | None, q_out | None, status | None, stream | None) -> q_out | None
+// (K_pool, V_pool, Hkv, P, K_new, V_new, positions, rope, k_norm | None, eps, slot_map, q | None, q_norm | None, q_out | None, status | None, stream | None) -> q_out | None
 PyObject* append_rotated_kv(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    Args a(args, n, 19);
+    Args a(args, n, 16);
     const at::Tensor *kp = a.tensor("K_pool"), *vp = a.tensor("V_pool");
     const int Hkv = a.i32(), P = a.i32();
     if (a.ok() && (kp->dim() != 3 || kp->size(2) != (int)kp->size(2)))
@@ -592,12 +603,12 @@ PyObject* append_rotated_kv(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// (K_pool, V_pool, B, Hkv, P, K_new, V_new, turns, rot_dim, layout, amplitude, k_norm | None, eps, page_table, seq_len,
+// (K_pool, V_pool, B, Hkv, P, K_new, V_new, rope, k_norm | None, eps, page_table, seq_len,
 //  K_scale, V_scale, prev_len | None, positions | None, q | None, q_norm | None, q_out | None, status | None,
 //  stream | None) -> q_out | None
 PyObject* append_rotated_kv8(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    Args a(args, n, 24);
+    Args a(args, n, 21);
     const at::Tensor *kp = a.tensor("K_pool"), *vp = a.tensor("V_pool");
     const int B = a.i32(), Hkv = a.i32(), P = a.i32();
     const int fmt = format_of(a, kp, vp, P);
@@ -635,11 +646,10 @@ PyObject* append_rotated_kv8(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// (X, W, positions, turns, rot_dim, layout, amplitude, norm | None, eps, Q | None, status | None, max_ctas | None,
-//  stream | None) -> Q
+// (X, W, positions, rope, norm | None, eps, Q | None, status | None, max_ctas | None, stream | None) -> Q
 PyObject* predict_q_rotated(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    Args a(args, n, 13);
+    Args a(args, n, 10);
     const at::Tensor *x = a.tensor("X"), *w = a.tensor("W");
     if (a.ok() && (x->dim() != 2 || w->dim() != 2 || x->size(0) != (int)x->size(0) || x->size(1) != (int)x->size(1) ||
                    w->size(0) != (int)w->size(0)))

@@ -404,20 +404,35 @@ def test_append8_prompts_of_many_sequences(B, P):
     check_write8(rng, w, "e4m3", bs.rope(1e4, 128, layout="interleaved"))
 
 
-def test_append8_values_that_are_not_finite():
-    rng = np.random.default_rng(4)
-    w = Write(rng, [3, 0], [60, 20], 3, 0, 32)
+@pytest.mark.parametrize("P", [16, 32, 64])
+@pytest.mark.parametrize("prev,seq", [([3, 0], [60, 20]), ([3, 0, 50], [9, 20, 51])])
+def test_append8_values_that_are_not_finite(P, prev, seq):
+    rng = np.random.default_rng(4 + P)
+    w = Write(rng, prev, seq, 3, 0, P)
     rope = bs.rope(1e4, 64)
-    w.K[5, 1, 7], w.K[20, 0, 100], w.K[70, 2, 33] = float("inf"), -float("inf"), float("nan")
-    w.V[8, 0, 0], w.V[61, 1, 127] = float("inf"), float("nan")
+    last = w.n - 1
+    w.K[2, 1, 7], w.K[20, 0, 100], w.K[last, 2, 33] = float("inf"), -float("inf"), float("nan")
+    w.V[1, 0, 0], w.V[last, 1, 127] = float("inf"), float("nan")
     K, V = pools8(rng, w, "e4m3"), pools8(rng, w, "e4m3")
     for kw in (None, w.kw):
         one = [t.clone() for t in (K[0], V[0], K[1], V[1])]
         two = [t.clone() for t in one]
-        bs.append_rotated_kv8(w.K, w.V, rope, w.table, w.seq_t, 2, 3, 32, *one, prev_len=w.prev_t, k_norm=kw)
-        bs.append_kv8(w.turned(rope, w.K, kw), w.V, w.table, w.seq_t, 2, 3, 32, *two, prev_len=w.prev_t)
+        bs.append_rotated_kv8(w.K, w.V, rope, w.table, w.seq_t, w.B, 3, P, *one, prev_len=w.prev_t, k_norm=kw)
+        bs.append_kv8(w.turned(rope, w.K, kw), w.V, w.table, w.seq_t, w.B, 3, P, *two, prev_len=w.prev_t)
         for a, b in zip(one, two):
             assert same(a, b)
+
+
+def test_writes_without_rows():
+    rng = np.random.default_rng(3)
+    w = Write(rng, [5], [5], 2, 4, 16)
+    rope = bs.rope(1e4, 64)
+    pool, K, V = bf16(rng, w.n_slots, 16, D), pools8(rng, w, "e4m3"), pools8(rng, w, "e4m3")
+    before = [pool.clone(), K[0].clone(), V[1].clone()]
+    q = bs.append_rotated_kv(w.K, w.V, i32([]), rope, w.slot_map, 2, 16, pool, pool, q=w.q)
+    q8 = bs.append_rotated_kv8(w.K, w.V, rope, w.table, w.seq_t, 1, 2, 16, K[0], V[0], K[1], V[1], prev_len=w.prev_t, q=w.q)
+    assert q.shape == q8.shape == (0, 4, D)
+    assert same(before[0], pool) and same(before[1], K[0]) and same(before[2], V[1])
 
 
 def test_append8_zero_rows_and_no_eps():
@@ -826,6 +841,21 @@ def test_add_norm(kind, M, N, wide, post, gate, ahead, alpha, pad):
     assert x[0] is h and x[1] is y and all(same(a, b) for a, b in zip(out, x))
 
 
+def test_add_norm_gates_of_any_stride_and_a_stream_inside_a_wider_one():
+    rng = np.random.default_rng(7)
+    Y, w = bf16(rng, 6, 640), weight(rng, 640)
+    H = bf16(rng, 6, 1920)[:, 640:1280]
+    wide = bf16(rng, 6, 1280)
+    want = bs.add_norm("rms", Y, H.contiguous(), w, gate=wide[:, 640:].contiguous())
+    got = bs.add_norm("rms", Y, H, w, gate=wide[:, 640:])
+    assert got[0].is_contiguous() and all(same(a, b) for a, b in zip(want, got))
+    one = bs.add_norm("rms", Y, H, w, gate=wide[0, 640:].clone())
+    for gate in (wide[:1, 640:].expand(6, 640), wide[:1, 640:].repeat(6, 1)):
+        assert all(same(a, b) for a, b in zip(one, bs.add_norm("rms", Y, H, w, gate=gate)))
+    with pytest.raises(bs.ScoutError, match="INVALID"):  # rows that overlap
+        bs.add_norm("rms", Y, H[:1].expand(6, 640), w)
+
+
 @pytest.mark.parametrize("kind", ["rms", "layer"])
 def test_add_norm_without_an_output_is_the_norms_alone(kind):
     rng = np.random.default_rng(1)
@@ -1054,3 +1084,61 @@ def test_a_layer_from_its_stream_to_its_attention_and_its_host_copy():
     Og, _ = bs.sparse_attn(ql, kp, vp, table, i32(seq), every.cuda(), cnt.cuda(), B, Hq, Hkv, P, cap, scale, ws_a)
     Oc, _ = bs.cpu_attend(ql.cpu(), host[0], host[1], torch.tensor(seq, dtype=torch.int32), every, cnt, B, Hq, Hkv, P, cap, scale)
     assert np.all(np.abs(f64(Og) - np.asarray(Oc)) <= 2e-3 + 1e-2 * np.abs(f64(Og)))
+
+
+def test_a_step_captured_once_and_replayed_as_sequences_grow():
+    """One graph of a layer's row operators over an 8-bit cache, replayed while lengths, rows and residual stream change."""
+    rng = np.random.default_rng(21)
+    B, Hq, Hkv, P, N, cap = 4, 8, 2, 16, 256, 6
+    rope, kw, qw, wn = bs.rope(1e4, 96, layout="interleaved"), weight(rng, D), weight(rng, D), weight(rng, N)
+    Wqkv, Wp = bf16(rng, (Hq + 2 * Hkv) * D, N, gain=False), bf16(rng, Hq * D, N, gain=False)
+    table = i32(rng.permutation(B * Hkv * cap).reshape(B, Hkv, cap))
+    start = np.array([30, 0, 15, 7])
+    st = {"prev": i32(start - (start > 0)), "seq": i32(start), "status": word()}
+    Y, H = bf16(rng, B, N), bf16(rng, B, N)
+    H1, X, Xa = torch.empty_like(H), torch.empty_like(H), torch.empty_like(H)
+    qkv, q_out = torch.empty((B, (Hq + 2 * Hkv) * D), dtype=torch.bfloat16, device="cuda"), torch.empty((B, Hq, D), dtype=torch.bfloat16, device="cuda")
+    Q = torch.empty((B, Hq * D), dtype=torch.bfloat16, device="cuda")
+    w = Write(rng, [0], [1], 1, 0, P)
+    w.n_slots, w.P = B * Hkv * cap, P
+
+    def state():
+        K, V = pools8(np.random.default_rng(5), w, "e4m3"), pools8(np.random.default_rng(6), w, "e4m3")
+        return [K[0], V[0], K[1], V[1]], [torch.zeros((B, Hkv, cap * P, D), dtype=torch.bfloat16, device="cuda") for _ in "KV"]
+
+    def step(pools, copy):
+        rows = qkv.view(B, Hq + 2 * Hkv, D)
+        st["prev"].copy_(st["seq"])
+        st["seq"].add_(1)
+        bs.add_norm("rms", Y, H, wn, w_ahead=kw.repeat(2), H_out=H1, X=X, X_ahead=Xa)
+        torch.matmul(X, Wqkv.t(), out=qkv)
+        bs.append_rotated_kv8(rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:], rope, table, st["seq"], B, Hkv, P, *pools, prev_len=st["prev"],
+                              k_norm=kw, q=rows[:, :Hq], q_norm=qw, q_out=q_out, status=st["status"])
+        bs.read_kv8(*pools, table, st["seq"], B, Hkv, P, *copy, status=st["status"])
+        bs.predict_q_rotated(Xa, Wp, st["prev"], rope, norm=qw, Q=Q, status=st["status"])
+        H.copy_(H1)
+        return [H1, X, Xa, q_out, Q]
+
+    one, two = state(), state()
+    inputs = [bf16(rng, B, N) for _ in range(20)]
+    seq0, H0 = st["seq"].clone(), H.clone()
+    want = []
+    for y in inputs:
+        Y.copy_(y)
+        want.append([t.clone() for t in step(*one)])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    st["seq"].copy_(seq0), H.copy_(H0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=side):
+            out = step(*two)
+    torch.cuda.synchronize()
+    st["seq"].copy_(seq0), H.copy_(H0)
+    for y, expect in zip(inputs, want):
+        Y.copy_(y)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(expect, out))
+    assert all(same(a, b) for a, b in zip(one[0] + one[1], two[0] + two[1])) and int(st["status"]) == 0
