@@ -3,7 +3,7 @@
 //
 // One kernel: a warp takes four tokens and some heads of one kind (queries row to row, keys and values by slot map).
 // Its rows' cosines are made once, in registers, while the first heads' rows are on their way; four heads are in flight
-// together.  Bound by DRAM: GB300, 8 prompts of up to 16K tokens, 8 KV and 32 query heads, 266 us for 1.72 GB (6.45 TB/s, 0.96 of the
+// together.  Bound by DRAM: GB300, 8 prompts of up to 16K tokens, 8 KV and 32 query heads, 264 us for 1.72 GB (6.5 TB/s, 0.97 of the
 // measured copy bandwidth) at 20 warps an SM and half of its issue slots; two heads in flight 282 us, eight 336 (registers); the
 // next heads read before the present ones are turned 280.  A decode step of 40 sequences 2.2 us, 8 x 32 heads 1.75 us:
 // the launch and one read.

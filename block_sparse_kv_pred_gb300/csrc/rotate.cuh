@@ -106,11 +106,14 @@ __device__ __forceinline__ Weights lane_weights(const __nv_bfloat16* norm, const
 
 // The head's norm: by the eight lanes that hold it, all of them.
 __device__ __forceinline__ void norm_head(float (&x)[16], const Weights& weights, float eps) {
-  float ss = 0.f;
+  float p[4];  // four sums side by side: a chain of sixteen would be waited for
 #pragma unroll
-  for (int i = 0; i < 16; ++i) ss = __fmaf_rn(x[i], x[i], ss);
+  for (int i = 0; i < 4; ++i) p[i] = __fmul_rn(x[i], x[i]);
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  for (int i = 4; i < 16; ++i) p[i & 3] = __fmaf_rn(x[i], x[i], p[i & 3]);
+  float ss = __fadd_rn(__fadd_rn(p[0], p[1]), __fadd_rn(p[2], p[3]));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
   const float r = rsqrtf(__fmaf_rn(ss, 1.f / kD, eps));
   float w[16];
   unpack16(weights.a, weights.b, w);
@@ -127,6 +130,103 @@ __device__ __forceinline__ void turn_head(float (&x)[16], const Turn& t, bool tu
     const float a = x[ia], b = x[ib];
     x[ia] = __fmaf_rn(a, t.c[i], -__fmul_rn(b, t.s[i]));
     x[ib] = __fmaf_rn(b, t.c[i], __fmul_rn(a, t.s[i]));
+  }
+}
+
+// The same with two values an instruction (fma.rn.f32x2), bit for bit: fewer instructions, but more registers that have to lie
+// in pairs.  GB300: the keys and values of the 8-bit write's prompts take 94 us without and 90 us with it; the
+// queries, and everything in the bf16 write, are slower with it (266 -> 338 us: their loads no longer go out together).
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair2(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split2(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A lane's 16 channels: the first and the second of its pairs (the channels of its two chunks, in a lane that does not turn).
+struct Pairs {
+  f2 a[4], b[4];
+};
+template <int LAYOUT>
+__device__ __forceinline__ Pairs unpack_pairs(const uint4& lo, const uint4& hi) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  Pairs x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (LAYOUT == SCOUT_ROPE_HALF) {
+      x.a[i] = pair2(bf16_lo(w[i]), bf16_hi(w[i]));
+      x.b[i] = pair2(bf16_lo(w[4 + i]), bf16_hi(w[4 + i]));
+    } else {
+      x.a[i] = pair2(bf16_lo(w[2 * i]), bf16_lo(w[2 * i + 1]));
+      x.b[i] = pair2(bf16_hi(w[2 * i]), bf16_hi(w[2 * i + 1]));
+    }
+  }
+  return x;
+}
+template <int LAYOUT>
+__device__ __forceinline__ void pack_pairs(const Pairs& x, uint4& lo, uint4& hi) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = split2(x.a[i]), b = split2(x.b[i]);
+    w[LAYOUT == SCOUT_ROPE_HALF ? i : 2 * i] = LAYOUT == SCOUT_ROPE_HALF ? pack_bf16(a.x, a.y) : pack_bf16(a.x, b.x);
+    w[LAYOUT == SCOUT_ROPE_HALF ? 4 + i : 2 * i + 1] = LAYOUT == SCOUT_ROPE_HALF ? pack_bf16(b.x, b.y) : pack_bf16(a.y, b.y);
+  }
+  lo = make_uint4(w[0], w[1], w[2], w[3]);
+  hi = make_uint4(w[4], w[5], w[6], w[7]);
+}
+template <int LAYOUT>
+__device__ __forceinline__ void norm_pairs(Pairs& x, const Weights& weights, float eps) {
+  // the four sums of norm_head, two in each of these, in its order
+  f2 s0 = mul2(x.a[0], x.a[0]), s1 = LAYOUT == SCOUT_ROPE_HALF ? mul2(x.a[1], x.a[1]) : mul2(x.b[0], x.b[0]);
+  float ss;
+  if (LAYOUT == SCOUT_ROPE_HALF) {
+    s0 = fma2(x.b[2], x.b[2], fma2(x.b[0], x.b[0], fma2(x.a[2], x.a[2], s0)));
+    s1 = fma2(x.b[3], x.b[3], fma2(x.b[1], x.b[1], fma2(x.a[3], x.a[3], s1)));
+    const float2 p = split2(s0), q = split2(s1);
+    ss = __fadd_rn(__fadd_rn(p.x, p.y), __fadd_rn(q.x, q.y));
+  } else {
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+      s0 = fma2(x.a[i], x.a[i], s0);
+      s1 = fma2(x.b[i], x.b[i], s1);
+    }
+    const float2 p = split2(s0), q = split2(s1);
+    ss = __fadd_rn(__fadd_rn(p.x, q.x), __fadd_rn(p.y, q.y));
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
+  const float r = rsqrtf(__fmaf_rn(ss, 1.f / kD, eps));
+  const f2 r2 = pair2(r, r);
+  const Pairs w = unpack_pairs<LAYOUT>(weights.a, weights.b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x.a[i] = mul2(mul2(x.a[i], r2), w.a[i]);
+    x.b[i] = mul2(mul2(x.b[i], r2), w.b[i]);
+  }
+}
+// c, s: cosines and sines of the lane's pairs, in order
+__device__ __forceinline__ void turn_pairs(Pairs& x, const f2 (&c)[4], const f2 (&s)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f2 a = x.a[i], b = x.b[i];
+    x.a[i] = fma2(a, c[i], mul2(b, s[i]) ^ 0x8000000080000000ull);
+    x.b[i] = fma2(b, c[i], mul2(a, s[i]));
   }
 }
 

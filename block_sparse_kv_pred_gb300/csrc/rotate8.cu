@@ -11,11 +11,12 @@
 //
 // Few (a decode step): a warp takes one head of a block, or one query head of four tokens, with no barrier and little code.
 //
-// GB300, 8 prompts of up to 16K tokens, 8 KV and 32 query heads: 265 us for 1.57 GB (5.9 TB/s, 0.88 of the measured
-// copy bandwidth; blocks of 16 tokens 260, of 64 270), bound by how well 16 warps an SM overlap arithmetic and
-// loads (the keys and values alone: 95 us, against 70 of scout_append_kv8 without turns).  A warp that made its own rows'
-// cosines for each head: 351 us; a CTA's warps holding four rows each of all heads, joined by its barrier: 302.  A decode
-// step of 40 sequences: 3.8 us, a chain of dependent reads (lengths, slot and rows, scale).
+// GB300, 8 prompts of up to 16K tokens, 8 KV and 32 query heads: 260 us for 1.57 GB (6.0 TB/s, 0.90 of the measured
+// copy bandwidth; blocks of 16 tokens 258, of 64 266), bound by how well 16 warps an SM overlap arithmetic and
+// loads (the keys and values alone: 90 us, against 70 of scout_append_kv8 without turns).  A warp that made its own rows'
+// cosines for each head: 351 us; a CTA's warps holding four rows each of all heads, joined by its barrier: 302; half as
+// many rows a warp: 262, but 26 us instead of 24 for 8 prompts of 1,000 tokens.  A decode step of 40 sequences: 4.1 us, a
+// chain of dependent reads (lengths, slot and rows, scale).
 #include "fp8.cuh"
 #include "rotate.cuh"
 
@@ -35,7 +36,7 @@ constexpr int kR8Heads = 16;  // query heads of a warp, one turn made for them
 // New tokens a sequence up to which a call is the second kernel's.  40 sequences (8 KV, 40 query heads), us, first / second
 // kernel: 8 tokens 13.1 / 7.5, 16: 14.7 / 12.5, 32: 18.1 / 23.3; one token 9.6 / 4.0.
 constexpr int kFewTokens = 16;
-constexpr int kHold = 8;  // row steps that a warp holds: a larger block is a pair of warps'
+constexpr int kHold = 8;  // row steps that a warp holds: a larger block is a set of warps'
 
 struct Rot8Args {
   const __nv_bfloat16 *kv[2], *q;  // new rows
@@ -89,15 +90,16 @@ __device__ __forceinline__ Block block_of(const Rot8Args& a, const int* tok, con
   return k;
 }
 
-// The two warps of a pair meet (their own barrier: pairs do not wait for one another).
-__device__ __forceinline__ void pair_sync() {
-  asm volatile("bar.sync %0, 64;" ::"r"(1 + (int)(threadIdx.x >> 6)) : "memory");
+// The N warps of a set meet (at a barrier of their own: sets do not wait for one another).
+template <int N>
+__device__ __forceinline__ void set_sync() {
+  if (N > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / (N * 32)), "n"(N * 32) : "memory");
 }
 
-// The K or V of one head of a block, by a warp, or by a pair (`top`: its warps' maxima, two sets of them) that holds a half of
-// it each.  H: steps held (of four rows each, from row `first`); with MORE the others, up to `steps`, are read again.
+// The K or V of one head of a block, by a set of N warps that hold an Nth of it each (`top`: the maxima of the CTA's warps, two
+// rounds of them).  H: steps held (of four rows each, from row `first`); with MORE the others, up to `steps`, are read again.
 // load(g, x, y) reads the rows of a step (zeros for rows that are not new), turn(g, x, y) turns them.
-template <int P, int F, int H, bool MORE, bool PAIR, class Load, class Turner>
+template <int P, int F, int H, bool MORE, int N, class Load, class Turner>
 __device__ __forceinline__ void quantise(const Rot8Args& a, const Block& k, bool is_v, int slot, const int2& at, int first,
                                          int steps, uint4 (&x)[H], uint4 (&y)[H], uint32_t* top, Load load, Turner turn) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 7;
@@ -119,13 +121,13 @@ __device__ __forceinline__ void quantise(const Rot8Args& a, const Block& k, bool
     m = max_all(max_all(m, lo), hi);
     fin = max_finite(max_finite(fin, lo), hi);
   }
-  auto join = [&](uint32_t v, int set) {
+  auto join = [&](uint32_t v, int round) {
     v = warp_max(v);
-    if (PAIR) {
-      if (lane == 0) top[set * kR8Warps + warp] = v;
-      pair_sync();
-      v = max(v, top[set * kR8Warps + (warp ^ 1)]);
-    }
+    if (N == 1) return v;
+    if (lane == 0) top[round * kR8Warps + warp] = v;
+    set_sync<N>();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v = max(v, top[round * kR8Warps + warp / N * N + i]);
     return v;
   };
   uint32_t big = join(m, 0);
@@ -144,9 +146,8 @@ __device__ __forceinline__ void quantise(const Rot8Args& a, const Block& k, bool
     const float inv = 1.f / scale;  // exact where the scale is a power of two (1 / 2^-126 = 2^126 is finite)
     if (grows) {
       const float ratio = old / need;
-      const int part = PAIR ? warp & 1 : 0;
 #pragma unroll 1
-      for (int r = part * 4 + (lane >> 3); r < k.r0; r += PAIR ? 8 : 4) {
+      for (int r = warp % N * 4 + (lane >> 3); r < k.r0; r += 4 * N) {
         uint4* p = reinterpret_cast<uint4*>(page + r * kD + sub * 16);
         const uint4 c = *p;
         *p = make_uint4(recode4<F>(c.x, ratio), recode4<F>(c.y, ratio), recode4<F>(c.z, ratio), recode4<F>(c.w, ratio));
@@ -166,10 +167,10 @@ __device__ __forceinline__ void quantise(const Rot8Args& a, const Block& k, bool
       if (!is_v) turn(g, lo, hi);
       store(g, lo, hi);
     }
-    __syncwarp();  // every lane has read the old scale, and a pair's other warp before it met this one
-    if (lane == 0 && (!PAIR || (warp & 1) == 0) && (k.r0 == 0 || grows)) *scale_at = scale;
+    __syncwarp();  // every lane has read the old scale, and a set's other warps before they met this one
+    if (lane == 0 && warp % N == 0 && (k.r0 == 0 || grows)) *scale_at = scale;
   }
-  if (PAIR) pair_sync();  // the maxima have been read: the next ones may be written
+  set_sync<N>();  // the maxima have been read: the next ones may be written
 }
 
 // Query rows: four tokens of a warp, heads [h0, h1), U of them in flight together.
@@ -233,6 +234,7 @@ __device__ __forceinline__ void prefixes(const Rot8Args& a, int* tok, int* tou, 
 template <int P, int F, int LAYOUT>
 __global__ void __launch_bounds__(kR8Warps * 32, kR8PerSm) rotate8_kernel(const Rot8Args a) {
   constexpr int H = P / 4 < kHold ? P / 4 : kHold, kSet = P / 4 / H;  // warps of one head's K or V
+  constexpr int kSets = kR8Warps / kSet;
   start_dependent();
   extern __shared__ int sm[];
   __shared__ int partial[2 * 32];
@@ -261,13 +263,13 @@ __global__ void __launch_bounds__(kR8Warps * 32, kR8PerSm) rotate8_kernel(const 
       if (tid == 0) report(a.status, SCOUT_DEV_BAD_INDEX);
       continue;
     }
-    // K and V of the part's heads, dealt to the warps (or pairs) so that each gets as many of either
+    // K and V of the part's heads, dealt to the sets of warps so that each gets as many of either
     const int p1 = 2 * min(a.Hkv, (part + 1) * a.kv_heads);
     bool made = false;
-    for (int p = 2 * part * a.kv_heads + warp / kSet; p < p1 || !made; p += kR8Warps / kSet) {
+    for (int p = 2 * part * a.kv_heads + warp / kSet; p < p1 || !made; p += kSets) {
       const bool mine = p < p1;
       const int h = p >> 1;
-      const bool is_v = (p + p / (kR8Warps / kSet)) & 1;
+      const bool is_v = (kSets == 1 ? p : p + p / kSets) & 1;
       const int2 at = is_v ? make_int2(sub * 16, sub * 16 + 8) : lane_chunks<LAYOUT>(sub, a.rope.n);
       const int64_t ld = a.ld[is_v];
       const __nv_bfloat16* src = a.kv[is_v] + k.i0 * ld + h * kD;
@@ -306,22 +308,22 @@ __global__ void __launch_bounds__(kR8Warps * 32, kR8PerSm) rotate8_kernel(const 
       if (norm) w = lane_weights(a.k_norm, at);
       auto turn = [&](int g, uint4& lo, uint4& hi) {
         const int r = first + 4 * g + (lane >> 3);
-        float v[16];
-        unpack16(lo, hi, v);
-        if (norm) norm_head(v, w, a.eps);
+        Pairs v = unpack_pairs<LAYOUT>(lo, hi);
+        if (norm) norm_pairs<LAYOUT>(v, w, a.eps);
         if (sub < a.rope.n) {
-          Turn t;
+          f2 c[4], s[4];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float4 c = table[i][r][sub], s = table[2 + i][r][sub];
-            t.c[4 * i] = c.x, t.c[4 * i + 1] = c.y, t.c[4 * i + 2] = c.z, t.c[4 * i + 3] = c.w;
-            t.s[4 * i] = s.x, t.s[4 * i + 1] = s.y, t.s[4 * i + 2] = s.z, t.s[4 * i + 3] = s.w;
+            const auto co = *reinterpret_cast<const ulonglong2*>(&table[i][r][sub]);
+            const auto si = *reinterpret_cast<const ulonglong2*>(&table[2 + i][r][sub]);
+            c[2 * i] = co.x, c[2 * i + 1] = co.y;
+            s[2 * i] = si.x, s[2 * i + 1] = si.y;
           }
-          turn_head<LAYOUT>(v, t, true);
+          turn_pairs(v, c, s);
         }
-        pack16(v, lo, hi);
+        pack_pairs<LAYOUT>(v, lo, hi);
       };
-      quantise<P, F, H, false, (kSet > 1)>(a, k, is_v, slot, at, first, H, x, y, top, load, turn);
+      quantise<P, F, H, false, kSet>(a, k, is_v, slot, at, first, H, x, y, top, load, turn);
     }
   }
 }
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kR8Warps * 32, 4) rotate8_few_kernel(const Rot
     };
     uint4 x[1], y[1];
     load(0, x[0], y[0]);
-    quantise<P, F, 1, true, false>(a, k, is_v, slot, at, k.r0, (k.r1 - k.r0 + 3) / 4, x, y, nullptr, load, turn);
+    quantise<P, F, 1, true, 1>(a, k, is_v, slot, at, k.r0, (k.r1 - k.r0 + 3) / 4, x, y, nullptr, load, turn);
   }
 }
 
@@ -487,3 +489,4 @@ extern "C" int scout_append_rotated_kv8(int fmt, const void* K_new, int64_t ld_k
   return fmt == SCOUT_FP8_E4M3 ? dispatch_rotate8<SCOUT_FP8_E4M3>(P, rope->layout, a, stream)
                                : dispatch_rotate8<SCOUT_FP8_E5M2>(P, rope->layout, a, stream);
 }
+
