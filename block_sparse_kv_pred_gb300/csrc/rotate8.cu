@@ -34,7 +34,7 @@ constexpr int kR8PerSm = 4;  // CTAs of the first kernel an SM (128 registers)
 constexpr int kR8Waves = 4;
 constexpr int kR8Heads = 16;  // query heads of a warp, one turn made for them
 // New tokens a sequence up to which a call is the second kernel's.  40 sequences (8 KV, 40 query heads), us, first / second
-// kernel: 8 tokens 13.1 / 7.5, 16: 14.7 / 12.5, 32: 18.1 / 23.3; one token 9.6 / 4.0.
+// kernel: one token 11.2 / 4.1, 8: 11.7 / 7.0, 16: 12.9 / 12.3, 24: 15.3 / 17.6, 32: 17.3 / 23.9.
 constexpr int kFewTokens = 16;
 constexpr int kHold = 8;  // row steps that a warp holds: a larger block is a set of warps'
 
