@@ -110,9 +110,11 @@ __global__ void __launch_bounds__(kThreadsQ, 1) predict_q_kernel(const __grid_co
   const int kb0 = (int)(rank * a.kblocks / S), kb1 = (int)((rank + 1) * a.kblocks / S);
   const int nst = (kb1 - kb0 + a.kps - 1) / a.kps;  // ring stages of this CTA's k range
   auto nk_of = [&](int i) { return min(a.kps, kb1 - kb0 - i * a.kps); };
-  // a kernel that starts early after this one (scout_score_topk) may take SMs as they free up;
-  // it waits for this grid to finish before it reads Q
-  release_dependents();
+  // A kernel that starts early after this one (scout_score_topk) may take SMs as they free up.  It waits for this grid to
+  // finish before it reads Q, but what it reads before that has to be complete by now.  So the rotated form without
+  // pdl, which is scheduled before its predecessor has finished all the same, lets it start after its own wait, further down
+  // (GB300: behind the CTA's barrier 10.5 and 14.0 us for the sizes above, each thread right after its wait 10.6 and 14.2).
+  if (LAYOUT == kPlain || a.early) release_dependents();
 
   // the first pass over the ring needs no free slot: issue it before the TMEM allocation.  W
   // does not depend on an earlier kernel; X may be written by the one this launch follows, so
@@ -151,6 +153,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) predict_q_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  if (LAYOUT != kPlain && !a.early) release_dependents();
   const bool apart = LAYOUT != kPlain && a.recv_at > 0;
   if (apart) cluster_arrive();  // this CTA runs: its shared memory may be written
 

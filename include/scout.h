@@ -91,14 +91,16 @@ typedef enum scout_digest_kind {
  *   scout_score_topk   streams digests, then waits before it reads q;
  *   scout_sparse_attn  sets up its barriers, then waits before its first global read.
  * Each writes its outputs only after that wait.  Everything else it reads must be
- * complete before the kernel it depends on started.  Two ways to start early:
+ * complete before the kernel it depends on started (a kernel that the end of this comment names as
+ * always scheduled early counts as started once it has waited).  Two ways to start early:
  *   pdl = 1          the dependency is the previous kernel on the same stream;
  *   early_event      set on the launch of the kernel depended on (the primary): the
  *                    event (created with cudaEventDisableTiming) is recorded
  *                    programmatically and fires before the primary completes, once
- *                    every CTA of it has passed its trigger: scout_predict_q at its
- *                    start, scout_score_topk once its last unit has been handed out,
- *                    scout_sparse_attn once its attention warps are done.  One of
+ *                    every CTA of it has passed its trigger: scout_predict_q(_rotated) at its
+ *                    start (_rotated without pdl: after its wait), scout_score_topk once
+ *                    its last unit has been handed out, scout_sparse_attn once its
+ *                    attention warps are done.  One of
  *                    these kernels launched on a stream that waits for the event then
  *                    starts early as above.  Anything else that waits for the event
  *                    (a copy, a host wait, another library's kernel) is NOT ordered
@@ -106,7 +108,9 @@ typedef enum scout_digest_kind {
  *                    for those.  NULL: no programmatic event.
  * scout_rotate, scout_append_rotated_kv(8), scout_add_norm, scout_read_kv(8) and, without pdl, scout_predict_q_rotated
  * take no part in this: they are always scheduled while the kernel before them on the stream ends, and wait for it
- * before they read or write anything.  The last of them streams W before that wait with pdl = 1. */
+ * before they read or write anything, and before they let a kernel that starts early after them start: such a kernel
+ * finds everything complete that was launched before them on their stream.  With pdl = 1 scout_predict_q_rotated streams W
+ * before that wait and lets it start at once, as scout_predict_q does. */
 typedef struct scout_launch {
   int max_ctas;
   int pdl;
@@ -490,8 +494,9 @@ int scout_append_rotated_kv(const void* K_new, int64_t ld_k, const void* V_new, 
 
 /* scout_predict_q with the heads of its product normalised and turned before they are rounded: row m of X W^T, N / D
  * heads of D = 128, each normalised by norm (bf16 [D], or NULL) and turned by positions[m] as scout_rotate does.  A row
- * whose position is negative (padding) is computed but not written.  Arguments, limits, launch options and early
- * starts as scout_predict_q, which waits before it reads X; this waits before it reads X and positions. */
+ * whose position is negative (padding) is computed but not written.  Arguments, limits and launch options as
+ * scout_predict_q; with pdl = 1 early starts too, and it waits before it reads X and positions.  Without, it is scheduled
+ * early all the same but waits before it reads anything or lets anything start after it. */
 int scout_predict_q_rotated(const void* X, const void* W, void* Q, int M, int N, int K, const int32_t* positions,
                             const scout_rope* rope, const void* norm, float eps, int32_t* dev_status,
                             const scout_launch* launch, cudaStream_t stream);

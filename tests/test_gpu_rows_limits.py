@@ -1,0 +1,71 @@
+"""A layer's row operators beside early starts of the kernels around them, and at the ends of what they take."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_kv_pred_gb300 as bs
+from _parity import ensure_built
+from test_gpu_rows import D, bf16, i32, same, word
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ensure_built()
+
+
+# ---------------------------------------------------------------------------
+# kernels that start early
+# ---------------------------------------------------------------------------
+LISTS = ("topk", "res", "cpu", "delta")
+
+
+def selection_args(q, digest, seq, bits, B, Hq, Hkv, P, cap, k, out, ws, launch, stream):
+    lists = [out[n + s].data_ptr() for n in LISTS for s in ("", "_count")]
+    return (bs.MINMAX, q.data_ptr(), digest.data_ptr(), seq.data_ptr(), bits.data_ptr(), None, None, B, Hq, Hkv, D, P, cap, k,
+            None, *lists, ws.data_ptr(), ws.numel(), None, launch, stream.cuda_stream)
+
+
+@pytest.mark.parametrize("by", ["pdl", "event"])
+def test_a_selection_that_starts_early_after_a_turned_prediction_finds_the_digests_before_it(by):
+    """Digests, the rotated prediction as it is always launched, and a selection that streams digests before it waits
+    for the prediction: those of the digest kernel, by either way to start early."""
+    rng = np.random.default_rng(1)
+    B, H, P, cap, k = 8, 8, 32, 512, 16
+    rope = bs.rope(1e6, 128)
+    K = torch.from_numpy(rng.standard_normal((B * H * cap, P, D)).astype(np.float32)).to(torch.bfloat16).cuda()
+    table = torch.arange(B * H * cap, dtype=torch.int32, device="cuda").view(B, H, cap)
+    seq = i32([cap * P - 40 * b for b in range(B)])
+    X, W, pos = bf16(rng, B, 512), bf16(rng, H * D, 512), seq - 1
+    bits = torch.full((B, H, cap // 32), 0x55555555, dtype=torch.int32, device="cuda")
+    digest = torch.zeros((B, H, cap, 2, D), dtype=torch.bfloat16, device="cuda")
+    ws, Q = bs.score_topk_workspace(B, H, cap), torch.empty((B, H * D), dtype=torch.bfloat16, device="cuda")
+    bs.build_digest("minmax", K, table, seq, B, H, P, digest)
+    bs.predict_q_rotated(X, W, pos, rope, Q=Q)
+    torch.cuda.synchronize()
+    want = bs.score_topk("minmax", Q.view(B, H, D), digest, seq, bits, B, H, H, P, cap, k, ws)
+    got = {n: torch.empty_like(t) for n, t in want.items()}
+    args, L, st, other = bs.RopeArgs(rope.turns.data_ptr(), 128, 0, 1.0), bs.lib(), torch.cuda.Stream(), torch.cuda.Stream()
+    event = torch.cuda.Event()
+    event.record(st)
+    first = None if by == "pdl" else bs._launch(0, early_event=event)
+    second = bs._launch(0, pdl=True) if by == "pdl" else None
+    for _ in range(20):
+        digest.zero_(), Q.zero_()
+        for t in got.values():
+            t.fill_(-9)
+        torch.cuda.synchronize()
+        bs.build_digest("minmax", K, table, seq, B, H, P, digest, stream=st)
+        assert L.scout_predict_q_rotated(X.data_ptr(), W.data_ptr(), Q.data_ptr(), B, H * D, 512, pos.data_ptr(), ctypes.byref(args),
+                                         None, 1e-6, None, first, st.cuda_stream) == 0
+        on = st
+        if by == "event":
+            on = other
+            other.wait_event(event)
+        assert L.scout_score_topk(*selection_args(Q, digest, seq, bits, B, H, H, P, cap, k, got, ws, second, on)) == 0
+        torch.cuda.synchronize()
+        for n in want:
+            assert torch.equal(got[n], want[n]), n
