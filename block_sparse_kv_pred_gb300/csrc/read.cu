@@ -75,12 +75,16 @@ __global__ void __launch_bounds__(kReadWarps * 32) read_kernel(const ReadArgs a)
     j = (int)(a.heads_inner ? q - b * cap : m);
   }
   const int64_t t0 = (int64_t)j * P + part * R, n = a.seq_len[b];
-  if (t0 >= n) return;
+  if (lane == 0 && n < 0) report(a.status, SCOUT_DEV_BAD_INDEX);
+  if (lane == 0 && n > (int64_t)a.nblk_cap * P) report(a.status, SCOUT_DEV_OVERFLOW);
+  // a listed block needs a slot whether or not it has tokens; without a list entries past the end are not looked at
+  if (a.block_list == nullptr && t0 >= n) return;
   const int slot = a.page_table[((int64_t)b * a.Hkv + h) * a.nblk_cap + j];
   if (slot < 0 || slot >= a.n_slots) {
     if (lane == 0 && (a.block_list != nullptr || slot != -1)) report(a.status, SCOUT_DEV_BAD_INDEX);
     return;
   }
+  if (t0 >= n) return;
   int rows = (int)(n - t0 < R ? n - t0 : R);
   if (t0 + rows > a.T) {
     if (lane == 0) report(a.status, SCOUT_DEV_OVERFLOW);

@@ -604,10 +604,13 @@ int scout_sparse_attn8_merge(int fmt, const void* q, const void* K_pool, const v
  *              unit: [B][Hkv][T][D] in any order of its axes but the last.  host_out 0: device memory; 1: pinned host
  *              memory mapped into the device's address space (as for scout_recall_gather_async).
  * block_list   int32 [n_list][2] of (u, j), or NULL for every valid block.  A (-1, -1) entry is padding; any other entry
- *              outside the tables, or without a slot of the pool, is skipped and sets SCOUT_DEV_BAD_INDEX.  With NULL, blocks
- *              whose page-table entry is -1 (those not on the GPU) are skipped without a report.
+ *              outside the tables, or without a slot of the pool (with tokens or past the sequence's end), is skipped and sets
+ *              SCOUT_DEV_BAD_INDEX.  With NULL, blocks whose page-table entry is -1 (those not on the GPU) are skipped without
+ *              a report, entries past a sequence's end are not looked at.
  * Of a block, the rows t < seq_len[b] are written; everything else in K_out and V_out is left as it was.  Rows with
- * t >= T are left out and set SCOUT_DEV_OVERFLOW.
+ * t >= T of a block that is on the GPU are left out and set SCOUT_DEV_OVERFLOW.
+ * seq_len      of a sequence that is read, in full or by a listed block: above nblk_cap * P it counts as that and sets
+ *              SCOUT_DEV_OVERFLOW, a negative one counts as 0 and sets SCOUT_DEV_BAD_INDEX.
  * scout_read_kv copies; scout_read_kv8 writes code * scale, rounded to bf16 (exact where the scale is a power of two).
  * No workspace.  Requires P in {16, 32, 64}, D = 128, T >= 1, strides >= 0 and multiples of 16, block_list 8-byte, K_out,
  * V_out and bf16 pools 32-byte, 8-bit pools 16-byte aligned, nblk_cap <= 8192, n_slots < 2^31, n_list and
