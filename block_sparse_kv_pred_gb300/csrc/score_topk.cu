@@ -577,6 +577,10 @@ __global__ void __launch_bounds__(kThreadsAll, 1) score_topk_kernel(const __grid
                 "l"(qg + h * kD), "r"(kD * 2), "r"(smem_u32(&full_bar[st]))
                 : "memory");
         } else {
+          if (!q_ready) {  // a unit without blocks needs no q, but its lists are written after that wait as well
+            wait_prerequisites();
+            q_ready = true;
+          }
           mbar_arrive(&full_bar[st]);
         }
       }

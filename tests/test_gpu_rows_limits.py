@@ -69,3 +69,32 @@ def test_a_selection_that_starts_early_after_a_turned_prediction_finds_the_diges
         torch.cuda.synchronize()
         for n in want:
             assert torch.equal(got[n], want[n]), n
+
+
+def test_a_selection_over_empty_sequences_that_starts_early_writes_after_its_wait():
+    """Its lists lie where the kernel before it writes: they are there last, whichever started first."""
+    B, H, P, cap, k = 4, 2, 32, 64, 8
+    rng = np.random.default_rng(2)
+    M, N, K = 256, 128, 32768  # one CTA that streams 25 MB
+    X, W = (torch.ones((n, K), dtype=torch.bfloat16, device="cuda") for n in (M, N))
+    digest = torch.zeros((B, H, cap, 2, D), dtype=torch.bfloat16, device="cuda")
+    q, bits = bf16(rng, B, H, D), torch.zeros((B, H, cap // 32), dtype=torch.int32, device="cuda")
+    ws, L, st = bs.score_topk_workspace(B, H, cap), bs.lib(), torch.cuda.Stream()
+    Q = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+    words = Q.view(torch.int32).flatten()
+    shapes = [(n + s, (B, H, k) if s == "" else (B, H)) for n in LISTS for s in ("", "_count")]
+    out, at = {}, 0
+    for n, shape in shapes:
+        out[n] = words[at:at + int(np.prod(shape))].view(shape)
+        at += int(np.prod(shape))
+    for lens in ([0] * B, [0, -5, 0, -1]):
+        seq = i32(lens)
+        for _ in range(10):
+            words.fill_(-9)
+            torch.cuda.synchronize()
+            assert L.scout_predict_q(X.data_ptr(), W.data_ptr(), Q.data_ptr(), M, N, K, None, bs._launch(1), st.cuda_stream) == 0
+            assert L.scout_score_topk(*selection_args(q, digest, seq, bits, B, H, H, P, cap, k, out, ws, bs._launch(0, pdl=True), st)) == 0
+            torch.cuda.synchronize()
+            for n, shape in shapes:
+                assert torch.all(out[n] == (0 if n.endswith("_count") else -1)), n
+            assert torch.all(Q.flatten()[2 * at:] == float(K))
