@@ -1,6 +1,8 @@
 // scout_rope_turns: the frequencies of rotary positions as fractions of 2^64 of a turn (host code).
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <limits>
 
 #include "scout.h"
 
@@ -40,6 +42,8 @@ extern "C" int scout_rope_turns(double base, int rot_dim, const scout_rope_scali
       last = std::fmin(std::ceil(at(s.low)), rot_dim - 1.0);
     }
   }
+  if (!std::isfinite(base) || amp > (double)std::numeric_limits<float>::max()) return SCOUT_ERR_INVALID_ARG;
+  uint64_t made[64];
   for (int i = 0; i < pairs; ++i) {
     double f = std::pow(base, -2.0 * i / rot_dim);
     switch (kind) {
@@ -59,9 +63,11 @@ extern "C" int scout_rope_turns(double base, int rot_dim, const scout_rope_scali
       default: break;
     }
     const double t = f / kTwoPi;
+    if (!std::isfinite(t)) return SCOUT_ERR_INVALID_ARG;  // a factor or divisor too small for its frequency
     // below 2^64: t - floor(t) is at most 1 - 2^-53
-    turns[i] = (uint64_t)std::ldexp(t - std::floor(t), 64);
+    made[i] = (uint64_t)std::ldexp(t - std::floor(t), 64);
   }
+  std::copy(made, made + pairs, turns);
   *amplitude = (float)amp;
   return SCOUT_OK;
 }

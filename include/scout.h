@@ -455,7 +455,8 @@ typedef struct scout_rope {
  * otherwise 1.
  * SCOUT_ERR_INVALID_ARG (nothing written): a NULL pointer, base not finite or not above 1, an unknown kind, a factor,
  * original, low, divisor that is not finite or not positive where the kind uses it, high not above low, a
- * negative or not finite amplitude.  SCOUT_ERR_UNSUPPORTED: rot_dim not a multiple of 16 in [16, 128]. */
+ * negative or not finite amplitude; a base, frequency or amplitude (as a float) that the scaling takes past what is
+ * finite.  SCOUT_ERR_UNSUPPORTED: rot_dim not a multiple of 16 in [16, 128]. */
 typedef enum scout_rope_kind {
   SCOUT_ROPE_LINEAR = 1,
   SCOUT_ROPE_NTK = 2,
