@@ -445,14 +445,24 @@ _SCALING = {"linear": 1, "ntk": 2, "rotations": 3, "index": 4, "divisors": 5}
 class Rope:
     """Rotary positions of a model's heads: ``turns`` int64 [rot_dim / 2] on the device (each pair's angle a
     position step, as a fraction of 2^64 of a turn), the number of channels turned, their layout and the
-    amplitude.  Made once by ``rope``, passed to every call that turns heads."""
+    amplitude.  Made once by ``rope``, passed to every call that turns heads; read-only."""
     __slots__ = ("turns", "rot_dim", "layout", "amplitude", "_args")
 
     def __init__(self, turns, rot_dim, layout, amplitude):
         if layout not in _LAYOUT:
             raise ScoutError(f"layout must be 'half' or 'interleaved', got {layout!r}")
-        self.turns, self.rot_dim, self.layout, self.amplitude = turns, int(rot_dim), layout, float(amplitude)
-        self._args = (turns, self.rot_dim, _LAYOUT[layout], self.amplitude)
+        rot_dim, amplitude = int(rot_dim), float(amplitude)
+        for name, value in zip(self.__slots__, (turns, rot_dim, layout, amplitude, (turns, rot_dim, _LAYOUT[layout], amplitude))):
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"a Rope is read-only: {name} is given when it is made")
+
+    def __delattr__(self, name):
+        raise AttributeError("a Rope is read-only")
+
+    def __reduce__(self):
+        return type(self), (self.turns, self.rot_dim, self.layout, self.amplitude)
 
 
 def rope(base=10000.0, rot_dim=128, layout="half", scaling=None, device="cuda") -> Rope:

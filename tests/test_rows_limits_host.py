@@ -1,7 +1,10 @@
 """Host side of a layer's row operators at the ends of what they take (no GPU)."""
+import copy
 import ctypes
+import pickle
 
 import pytest
+import torch
 
 import block_sparse_kv_pred_gb300 as bs
 from _parity import ensure_built
@@ -49,3 +52,26 @@ def test_turns_at_the_ends_of_what_is_finite(L, base, rot, s, first, last):
     assert all(0.0 <= t < 1.0 for t in got) and amp.value == pytest.approx(s.get("amplitude", 1.0))
     assert first is None or got[0] == pytest.approx(first, abs=2.0 ** -60)
     assert last is None or got[-1] == pytest.approx(last, abs=2.0 ** -60)
+
+
+# ---------------------------------------------------------------------------
+# Rope
+# ---------------------------------------------------------------------------
+def test_a_rope_is_read_only(L):
+    # calls use the arguments that were put together when it was made: a field that could be set would not reach them
+    r = bs.rope(1e4, 64, layout="interleaved", scaling={"kind": "linear", "factor": 2.0, "amplitude": 1.5}, device="cpu")
+    for name, value in (("amplitude", 2.0), ("layout", "half"), ("rot_dim", 32), ("turns", r.turns.clone()), ("other", 1)):
+        with pytest.raises(AttributeError):
+            setattr(r, name, value)
+        if name != "other":
+            with pytest.raises(AttributeError):
+                delattr(r, name)
+    assert (r.rot_dim, r.layout, r.amplitude) == (64, "interleaved", 1.5) and r.turns.numel() == 32
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy, lambda r: pickle.loads(pickle.dumps(r))], ids=["copy", "deepcopy", "pickle"])
+def test_a_rope_is_copied_whole(L, how):
+    r = bs.rope(1e4, 64, layout="interleaved", scaling={"kind": "linear", "factor": 2.0, "amplitude": 1.5}, device="cpu")
+    c = how(r)
+    assert (c.rot_dim, c.layout, c.amplitude) == (64, "interleaved", 1.5) and torch.equal(c.turns, r.turns)
+    assert c._args[0] is c.turns and c._args[1:] == r._args[1:]
