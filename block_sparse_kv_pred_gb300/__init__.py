@@ -442,6 +442,12 @@ _LAYOUT = {"half": 0, "interleaved": 1}
 _SCALING = {"linear": 1, "ntk": 2, "rotations": 3, "index": 4, "divisors": 5}
 
 
+def _rot_dim(n) -> int:
+    if not -2**31 <= int(n) < 2**31:
+        raise ScoutError(f"rot_dim must fit 32 bits, got {n}")
+    return int(n)
+
+
 class Rope:
     """Rotary positions of a model's heads: ``turns`` int64 [rot_dim / 2] on the device (each pair's angle a
     position step, as a fraction of 2^64 of a turn), the number of channels turned, their layout and the
@@ -451,7 +457,7 @@ class Rope:
     def __init__(self, turns, rot_dim, layout, amplitude):
         if layout not in _LAYOUT:
             raise ScoutError(f"layout must be 'half' or 'interleaved', got {layout!r}")
-        rot_dim, amplitude = int(rot_dim), float(amplitude)
+        rot_dim, amplitude = _rot_dim(rot_dim), float(amplitude)
         for name, value in zip(self.__slots__, (turns, rot_dim, layout, amplitude, (turns, rot_dim, _LAYOUT[layout], amplitude))):
             object.__setattr__(self, name, value)
 
@@ -476,6 +482,7 @@ def rope(base=10000.0, rot_dim=128, layout="half", scaling=None, device="cuda") 
     default 1, of "index" 0.1 ln(factor) + 1).  The formulas are beside scout_rope_turns."""
     import numpy as np
 
+    rot_dim = _rot_dim(rot_dim)
     s = None
     if scaling is not None:
         more = dict(scaling)
@@ -500,9 +507,9 @@ def rope(base=10000.0, rot_dim=128, layout="half", scaling=None, device="cuda") 
                 setattr(s, k, float(v))
     if layout not in _LAYOUT:
         raise ScoutError(f"layout must be 'half' or 'interleaved', got {layout!r}")
-    turns = np.zeros(max(1, int(rot_dim) // 2), dtype=np.uint64)
+    turns = np.zeros(max(1, min(rot_dim // 2, 64)), dtype=np.uint64)  # (more than 64 pairs are refused)
     amp = ctypes.c_float(0)
-    _check(lib().scout_rope_turns(float(base), int(rot_dim), None if s is None else ctypes.byref(s), turns.ctypes.data,
+    _check(lib().scout_rope_turns(float(base), rot_dim, None if s is None else ctypes.byref(s), turns.ctypes.data,
                                   ctypes.byref(amp)), "scout_rope_turns")
     return Rope(torch.from_numpy(turns.view(np.int64)).to(device), rot_dim, layout, amp.value)
 

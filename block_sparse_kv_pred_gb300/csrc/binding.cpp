@@ -477,7 +477,9 @@ scout_rope rope_of(Args& a) {
     return r;
   }
   const at::Tensor* t = a.tensor(PyTuple_GET_ITEM(o, 0), "rope.turns");
-  r.rot_dim = (int)PyLong_AsLong(PyTuple_GET_ITEM(o, 1));
+  const long rot_dim = PyLong_AsLong(PyTuple_GET_ITEM(o, 1));
+  if (rot_dim != (int)rot_dim) a.fail("rope.rot_dim must fit 32 bits, got %ld", rot_dim);
+  r.rot_dim = (int)rot_dim;
   r.layout = (int)PyLong_AsLong(PyTuple_GET_ITEM(o, 2));
   r.amplitude = (float)PyFloat_AsDouble(PyTuple_GET_ITEM(o, 3));
   if (a.ok() && PyErr_Occurred()) {

@@ -75,3 +75,13 @@ def test_a_rope_is_copied_whole(L, how):
     c = how(r)
     assert (c.rot_dim, c.layout, c.amplitude) == (64, "interleaved", 1.5) and torch.equal(c.turns, r.turns)
     assert c._args[0] is c.turns and c._args[1:] == r._args[1:]
+
+
+@pytest.mark.parametrize("rot", [2 ** 32 + 64, 2 ** 31 + 64, -2 ** 32 + 64, 2 ** 70])
+def test_a_rope_of_more_channels_than_32_bits_hold_is_refused(L, rot):
+    # not cut to its low 32 bits, which name 64 channels here
+    x, p = torch.zeros((2, 3, 128), dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(bs.ScoutError, match="rot_dim"):
+        bs.rotate(x, p, bs.Rope(torch.zeros(32, dtype=torch.int64), rot, "half", 1.0))
+    with pytest.raises(bs.ScoutError):
+        bs.rope(1e4, rot, device="cpu")
