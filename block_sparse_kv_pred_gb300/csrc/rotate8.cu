@@ -235,6 +235,7 @@ template <int P, int F, int LAYOUT>
 __global__ void __launch_bounds__(kR8Warps * 32, kR8PerSm) rotate8_kernel(const Rot8Args a) {
   constexpr int H = P / 4 < kHold ? P / 4 : kHold, kSet = P / 4 / H;  // warps of one head's K or V
   constexpr int kSets = kR8Warps / kSet;
+  static_assert(kSets % 2 == 0, "a head's K and V are of one round of the sets: exactly one of them is V");
   start_dependent();
   extern __shared__ int sm[];
   __shared__ int partial[2 * 32];
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kR8Warps * 32, kR8PerSm) rotate8_kernel(const 
     for (int p = 2 * part * a.kv_heads + warp / kSet; p < p1 || !made; p += kSets) {
       const bool mine = p < p1;
       const int h = p >> 1;
-      const bool is_v = (kSets == 1 ? p : p + p / kSets) & 1;
+      const bool is_v = (p + p / kSets) & 1;
       const int2 at = is_v ? make_int2(sub * 16, sub * 16 + 8) : lane_chunks<LAYOUT>(sub, a.rope.n);
       const int64_t ld = a.ld[is_v];
       const __nv_bfloat16* src = a.kv[is_v] + k.i0 * ld + h * kD;
