@@ -7,7 +7,7 @@
 // every head of the token.
 //
 // The angle is an integer product modulo 2^64 (turns as fractions of 2^64), so a far position costs no
-// precision and no reduction.  Every rounding is
+// precision beside the table's own, and no reduction.  Every rounding is
 // written out (no contraction is left to the compiler), so that each kernel that turns a head gets the same bits.
 #pragma once
 
@@ -41,8 +41,8 @@ __device__ __forceinline__ int2 lane_chunks(int sub, int n) {
 
 // sin and cos of a turn given as a fraction of 2^32: the nearest quarter turn by integers, and polynomials
 // in the square of the rest, |rest| <= 1/8 turn (minimax, fitted by exchange: the sine's quotient by the rest to
-// 2^-28, the cosine to 2^-34).  Off by at most 1.7 and 1.2 roundings of fp32 over 2 million angles, with a
-// third of the instructions of sincospi, whose code a short launch has to fetch.
+// 2^-28, the cosine to 2^-34).  Off by at most 1.7 and 1.2 times 2^-24, and by 2.9 and 1.7 times 2^-24 of themselves,
+// over 2 million angles (bounds by arithmetic: 4 and 3 of themselves), with a third of the instructions of sincospi, whose code a short launch has to fetch.
 __device__ __forceinline__ void sincos_turn(uint32_t turn, float& s, float& c) {
   const uint32_t quarter = (turn + 0x20000000u) & 0xc0000000u;
   const float x = __fmul_rn((float)(int32_t)(turn - quarter), 0x1p-32f), z = __fmul_rn(x, x);

@@ -426,8 +426,10 @@ int scout_add_norm(int kind, const void* Y, int64_t ld_y, const void* w_post, co
  * (SCOUT_ROPE_HALF) or (2i, 2i + 1) (SCOUT_ROPE_INTERLEAVED).  At position p it becomes
  *   (a, b) -> amplitude * (a cos(p f_i) - b sin(p f_i), b cos(p f_i) + a sin(p f_i));
  * the other channels stay as they are.  turns[i] is f_i in turns, f_i / (2 pi) modulo 1, as
- * a fraction of 2^64: p * turns[i] modulo 2^64 is the pair's angle to 2^-33 of a turn at any
- * position, in integers.
+ * a fraction of 2^64: p * turns[i] modulo 2^64 is the pair's angle, in integers, and is rounded to
+ * 2^-32 of a turn.  At any position that is 2^-33 of a turn from the angle of the table; a table made by
+ * scout_rope_turns comes from fp64, a few times 2^-53 of f_i from its formula, which a position multiplies
+ * (about 2^-24 of a turn at position 2^31 for f_i = 1).
  *
  * turns      uint64 [rot_dim / 2], DEVICE memory, 16-byte aligned
  * rot_dim    a multiple of 16, at most D

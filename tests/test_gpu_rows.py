@@ -3,10 +3,11 @@
 Tolerances, u = 2^-24 the unit of an fp32 rounding.  A result rounded to bf16 is off by 2^-8 of itself beside
 its fp32 error.
 
-Turned heads, with s the length of a channel's pair (amplitude and norm included): the angle's conversion to
-fp32 is off by u of at most pi; sincospi by 2 ulp, 4 u; the amplitude, the two products and the sum 4 u.  The
-norm: its sum has 19 roundings of positive terms and the eps, which count half in the root, rsqrtf 2 ulp = 4 u, two
-products: 16 u.  Together below 32 u s.
+Turned heads, with s the length of a channel's pair (amplitude and norm included): the angle is off by 2^-33 of a turn,
+0.02 u s; sine and cosine by 4 u of themselves (tests/test_rows_limits_host.py), the amplitude's product by u, one of the
+two products by u and their sum by u: 7.1 u s, as the products' magnitudes add up to s at most.  The norm: its sum has 4
+roundings of positive terms in a lane and 5 where lanes are joined, and the eps, which count half in the root, rsqrtf 2 ulp =
+4 u, two products: 11 u.  Together below 32 u s.
 
 Predicted queries: K products summed in fp32, each partial sum off by at most 2 u (the tensor core cuts) of sum_k |x_k w_k|:
 e = (2 K + 16) u sum |x w| for each entry before norm and turn.  A norm multiplies an entry's error by its factor and adds the

@@ -1,8 +1,11 @@
 """Host side of a layer's row operators at the ends of what they take (no GPU)."""
 import copy
 import ctypes
+import os
 import pickle
+import subprocess
 
+import numpy as np
 import pytest
 import torch
 
@@ -85,3 +88,63 @@ def test_a_rope_of_more_channels_than_32_bits_hold_is_refused(L, rot):
         bs.rotate(x, p, bs.Rope(torch.zeros(32, dtype=torch.int64), rot, "half", 1.0))
     with pytest.raises(bs.ScoutError):
         bs.rope(1e4, rot, device="cpu")
+
+
+# ---------------------------------------------------------------------------
+# cosine and sine of a turn
+# ---------------------------------------------------------------------------
+# csrc/rotate.cuh's sincos_turn itself, its intrinsics written as the host's (each a single rounding).  With u = 2^-24 and
+# z = x^2 at most 1/64, errors to first order:
+#   x is off by u of itself (the integer's conversion), z by 3 u of itself.
+#   sine: the inner steps leave 46.5 u; the last one z 46.5 u + 3 u 0.65 + its rounding 4 u (half a step in [4, 8)) + the
+#   constant's rounding 2.9 u + the fit 0.1 u = 9.7 u of at least 5.65, 1.7 u; times x and rounded: 3.7 u of the sine.
+#   cosine: the inner steps leave 36 u; the last one z 36 u + 3 u 0.3 + its rounding u / 2 = 2 u of at least 0.7: 2.8 u.
+# Odd quarters exchange the two.
+SIN, COS = 4 * 2.0 ** -24, 3 * 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def sincos(tmp_path_factory):
+    csrc = os.path.join(os.path.dirname(bs.__file__), "csrc")
+    with open(os.path.join(csrc, "rotate.cuh")) as f:
+        text = f.read()
+    at = text.index("__device__ __forceinline__ void sincos_turn")
+    body = text[at:text.index("\n}\n", at) + 3]
+    d = tmp_path_factory.mktemp("sincos")
+    (d / "s.cpp").write_text("""#include <cmath>
+#include <cstdint>
+#include <cstring>
+#define __device__
+#define __forceinline__ inline
+static float __fmul_rn(float a, float b) { return a * b; }
+static float __fmaf_rn(float a, float b, float c) { return std::fma(a, b, c); }
+static float __uint_as_float(uint32_t v) { float f; std::memcpy(&f, &v, 4); return f; }
+static uint32_t __float_as_uint(float f) { uint32_t v; std::memcpy(&v, &f, 4); return v; }
+""" + body + """extern "C" void run(const uint32_t* t, long n, float* s, float* c) {
+  for (long i = 0; i < n; ++i) sincos_turn(t[i], s[i], c[i]);
+}
+""")
+    subprocess.run(["g++", "-std=c++17", "-O2", "-ffp-contract=off", "-shared", "-fPIC", "-o", d / "s.so", d / "s.cpp"], check=True)
+    run = ctypes.CDLL(str(d / "s.so")).run
+
+    def call(t):
+        s, c = np.empty(len(t), np.float32), np.empty(len(t), np.float32)
+        run(*(ctypes.c_void_p(a.ctypes.data) if i != 1 else ctypes.c_long(a) for i, a in enumerate((t, len(t), s, c))))
+        return s, c
+    return call
+
+
+def test_cosine_and_sine_of_a_turn_are_within_their_bounds(sincos):
+    rng = np.random.default_rng(0)
+    near = np.concatenate([np.arange(-3000, 3001), [2 ** k for k in range(12, 29)], [-2 ** k for k in range(12, 29)]])
+    t = np.concatenate([(np.arange(8)[:, None] * 2 ** 29 + near).ravel(), rng.integers(0, 2 ** 32, 1 << 20),
+                        rng.integers(0, 2 ** 26, 1 << 16) - 2 ** 25]) % 2 ** 32
+    s, c = sincos(np.ascontiguousarray(t.astype(np.uint32)))
+    quarter = (t + 2 ** 29) // 2 ** 30 % 4
+    rest = (t + 2 ** 29) % 2 ** 30 - 2 ** 29  # exact
+    a = rest * (2 * np.pi / 2 ** 32)
+    sin, cos = np.sin(a), np.cos(a)
+    want_s, want_c = np.choose(quarter, [sin, cos, -sin, -cos]), np.choose(quarter, [cos, -sin, -cos, sin])
+    odd = quarter % 2 == 1
+    for got, want, bound in ((s, want_s, np.where(odd, COS, SIN)), (c, want_c, np.where(odd, SIN, COS))):
+        assert np.all(np.abs(got - want) <= bound * np.abs(want))
