@@ -98,3 +98,61 @@ def test_a_selection_over_empty_sequences_that_starts_early_writes_after_its_wai
             for n, shape in shapes:
                 assert torch.all(out[n] == (0 if n.endswith("_count") else -1)), n
             assert torch.all(Q.flatten()[2 * at:] == float(K))
+
+
+def test_a_captured_selection_that_starts_early_after_a_turned_prediction_and_a_joined_stream():
+    """One graph: two streams joined before a row kernel, copies and fills between row kernels, digests, the rotated
+    prediction, a selection that starts early.  Replayed over inputs that change."""
+    rng = np.random.default_rng(3)
+    B, H, P, cap, k, N = 8, 8, 32, 256, 16, 512
+    rope = bs.rope(1e6, 128)
+    K = torch.zeros((B * H * cap, P, D), dtype=torch.bfloat16, device="cuda")
+    table = torch.arange(B * H * cap, dtype=torch.int32, device="cuda").view(B, H, cap)
+    seq = i32([cap * P - 40 * b for b in range(B)])
+    Y, S, W, w = bf16(rng, B, N), bf16(rng, B, N), bf16(rng, H * D, N), bf16(rng, N)
+    pos, heads = torch.zeros_like(seq), bf16(rng, B, H, D)
+    bits = torch.full((B, H, cap // 32), 0x55555555, dtype=torch.int32, device="cuda")
+    digest = torch.zeros((B, H, cap, 2, D), dtype=torch.bfloat16, device="cuda")
+    ws, Q = bs.score_topk_workspace(B, H, cap), torch.empty((B, H * D), dtype=torch.bfloat16, device="cuda")
+    S2, X, R, R2 = torch.empty_like(S), torch.empty_like(Y), torch.empty_like(heads), torch.empty_like(heads)
+    shape = {n + s: (B, H, k) if s == "" else (B, H) for n in LISTS for s in ("", "_count")}
+    got = {n: torch.empty(s, dtype=torch.int32, device="cuda") for n, s in shape.items()}
+    args, L = bs.RopeArgs(rope.turns.data_ptr(), 128, 0, 1.0), bs.lib()
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    launch = bs._launch(0, pdl=True)
+
+    def run(second):
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            bs.add_norm("rms", Y, S, w, H_out=S2, X=X)
+        with torch.cuda.stream(main):
+            pos.copy_(seq).sub_(1)
+            bs.rotate(heads, pos, rope, out=R)
+            R2.copy_(R)
+            bs.rotate(R2, pos, rope, out=R2)
+            main.wait_stream(side)
+            digest.fill_(0)
+            bs.build_digest("minmax", K, table, seq, B, H, P, digest)
+        assert L.scout_predict_q_rotated(X.data_ptr(), W.data_ptr(), Q.data_ptr(), B, H * D, N, pos.data_ptr(), ctypes.byref(args),
+                                         None, 1e-6, None, None, main.cuda_stream) == 0
+        assert L.scout_score_topk(*selection_args(Q, digest, seq, bits, B, H, H, P, cap, k, got, ws, second, main)) == 0
+
+    run(None)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        run(launch)
+    for i in range(5):
+        K.copy_(torch.from_numpy(rng.standard_normal(K.shape).astype(np.float32)))
+        Y.copy_(bf16(rng, B, N)), heads.copy_(bf16(rng, B, H, D)), seq.sub_(17 * i)
+        torch.cuda.synchronize()
+        run(None)
+        torch.cuda.synchronize()
+        want = {n: t.clone() for n, t in got.items()} | {"Q": Q.clone(), "X": X.clone(), "R": R.clone(), "R2": R2.clone()}
+        for t in (*got.values(), Q, X, R, R2):
+            t.fill_(-9)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for n, t in {**got, "Q": Q, "X": X, "R": R, "R2": R2}.items():
+            assert same(t, want[n]), n
