@@ -10,6 +10,9 @@
 // Bound by DRAM: GB300, 131,072 x 4,096, fp32 stream, norms before and after, a gate: 925 us for 6.44 GB (7.0 TB/s, above the
 // measured copy rate); 40 x 5,120 2.8 us, the launch and one read.  Rows past 16,384 are one a SM at a time, whose reads and
 // writes do not overlap (8,192 x 32,768: 5.1 TB/s).
+// A row of 128 leaves half of its warp's lanes without a chunk (1,048,576 rows, bf16 stream, two norms: 280 us, 4.8 TB/s; 524,288
+// rows of 256: 193 us, 7.0 TB/s).  SCOUT_NORM_LAYER waits for a sum more between a row's reads and writes, and reads biases:
+// 154 us for 16,384 x 5,120 (125), 895 for 131,072 x 4,096 (770), 392 and 222 for the two above, 3.1 for 40 x 5,120 (2.7).
 #include "common.cuh"
 
 namespace scout {

@@ -21,8 +21,10 @@
 // CTA holds whole heads of its batch columns.  The sums go to shared memory in fp32, eight lanes
 // take a head (rotate.cuh), normalise and turn it, and store it rounded once, 16 bytes a lane.
 // The cosines and sines are made, and the norm's weights read, while W streams in (read in the last step, the weights
-// alone cost 1.3 us).  GB300: 14.0 us for 40 x 5120 x 5120 and 10.7 us for 8 x 4096 x 4096 (3.8 and 3.2 TB/s of W: the
+// alone cost 1.3 us).  GB300: 14.0 us for 40 x 5120 x 5120 and 10.5 us for 8 x 4096 x 4096 (3.8 and 3.2 TB/s of W: the
 // launch, ~1.8 us to the first product, the stream at about 6 TB/s, 1.3 and 1.1 us of exchange, 1.2 and 0.6 of last step).
+// 128 and 256 x 5120 x 5120: 17.8 and 25.5 us (2.9 and 2.1 TB/s of W: X's tiles take up to two thirds of the ring, and what is
+// exchanged grows with the rows).
 
 #include "rotate.cuh"
 

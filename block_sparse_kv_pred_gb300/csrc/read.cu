@@ -5,8 +5,10 @@
 // stores the prompts below take 81 us, with sixteen lanes and 16-byte accesses 73).  One item a warp: a grid of resident
 // CTAs that stride over the items takes 10% longer.
 //
-// Bound by DRAM: GB300, 8 prompts of up to 16K tokens, 8 KV heads, out of an 8-bit cache: 66.3 us for 428 MB (6.5 TB/s, 0.96 of
-// the measured copy bandwidth), out of a bf16 one 85.5 us for 570 MB; 320 blocks by list: 2.9 us, the launch and two dependent reads.
+// Bound by DRAM: GB300, 8 prompts of up to 16K tokens, 8 KV heads, out of an 8-bit cache: 65.4 us for 428 MB (6.5 TB/s, 0.98 of
+// the measured copy bandwidth), out of a bf16 one 85.5 us for 570 MB; 320 blocks by list: 2.8 us, the launch and two dependent reads.
+// Into pinned host memory by the link: 365 MB of rows 1,887 us (193 GB/s, as a plain copy's), 320 blocks 16.5 us (173), out of
+// either cache and in either order of the rows.
 #include "fp8.cuh"
 
 namespace scout {

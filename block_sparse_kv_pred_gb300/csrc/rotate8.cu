@@ -15,7 +15,7 @@
 // copy bandwidth; blocks of 16 tokens 258, of 64 266), bound by how well 16 warps an SM overlap arithmetic and
 // loads (the keys and values alone: 90 us, against 70 of scout_append_kv8 without turns).  A warp that made its own rows'
 // cosines for each head: 351 us; a CTA's warps holding four rows each of all heads, joined by its barrier: 302; half as
-// many rows a warp: 262, but 26 us instead of 24 for 8 prompts of 1,000 tokens.  A decode step of 40 sequences: 4.1 us, a
+// many rows a warp: 262, but 26 us instead of 24 for 8 prompts of 1,000 tokens.  A decode step of 40 sequences: 4.2 us, a
 // chain of dependent reads (lengths, slot and rows, scale).
 #include "fp8.cuh"
 #include "rotate.cuh"
@@ -34,7 +34,9 @@ constexpr int kR8PerSm = 4;  // CTAs of the first kernel an SM (128 registers)
 constexpr int kR8Waves = 4;
 constexpr int kR8Heads = 16;  // query heads of a warp, one turn made for them
 // New tokens a sequence up to which a call is the second kernel's.  40 sequences (8 KV, 40 query heads), us, first / second
-// kernel: one token 11.2 / 4.1, 8: 11.7 / 7.0, 16: 12.9 / 12.3, 24: 15.3 / 17.6, 32: 17.3 / 23.9.
+// kernel: one token 11.2 / 4.1, 8: 11.7 / 7.0, 16: 12.9 / 12.3, 24: 15.3 / 17.6, 32: 17.3 / 23.9.  The mean decides, so a
+// chunk among many single tokens is the second kernel's as well: 255 of them and 3,800 tokens of another sequence (8 KV, 32 query
+// heads) take 61.5 us in one call, 9.4 and 22.2 in two.
 constexpr int kFewTokens = 16;
 constexpr int kHold = 8;  // row steps that a warp holds: a larger block is a set of warps'
 
